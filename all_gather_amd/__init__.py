@@ -1,4 +1,5 @@
-"""Python binding of libmr, the MI355X W-way sum-reduce and param-contiguous gather library.
+"""Python binding of libmr, the MI355X W-way sum-reduce and param-contiguous gather library, with the operators of
+a training step around them (layer norm, gradient norm, AdamW).
 
 A thin ctypes layer over the C ABI declared in include/mr.h: it turns torch tensors into device
 pointers, sizes and the current HIP stream, calls the entry point of the same name and raises on a
@@ -8,8 +9,9 @@ fallback.  If libmr.so has not been built, loading it raises.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import os
-from typing import Sequence
+from typing import Any, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmr.so")
@@ -25,6 +27,7 @@ STATUS = {
     -6: "MR_ERR_ENGINE",
 }
 DTYPE_CODE = {"bf16": 0, "fp16": 1, "fp32": 2, "int32": 3}
+STATE_FORMAT = {32: 0, 8: 1}
 MODE_CODE = {"oneshot": 0, "twoshot": 1}
 OPTION_CODE = {"twoshot_sync": 0, "spin_limit": 1, "tile_shape": 2, "sdma_cu_below": 3}
 TWOSHOT_SYNC = {"tile": 0, "chunk": 1, "grid": 2, "last": 3, "auto": 4}
@@ -32,6 +35,18 @@ TILE_SHAPE = {"auto": 0, "wide": 1, "medium": 2, "narrow": 3, "wide_pair": 4}
 MAX_W = 16
 MAX_PARAMS_PER_LAUNCH = 128
 MAX_TABLE_W = 64
+
+ADAMW_BLOCK = 32
+
+
+class _AdamWStateC(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("m", "v", "m_scale", "v_scale", "master")]
+
+
+class _AdamWHyperC(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_uint64), ("seed", ctypes.c_uint64)]
+
 
 # Exported symbols of include/mr.h, with ctypes signatures.
 _SIGS = {
@@ -63,6 +78,18 @@ _SIGS = {
                                                       ctypes.POINTER(ctypes.c_uint64), ctypes.c_int, ctypes.c_int,
                                                       ctypes.c_void_p, ctypes.c_void_p]),
     "mr_sdma_engines": (ctypes.c_int, []),
+    "mr_layer_norm_forward": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int] + [ctypes.c_void_p] * 3 +
+                              [ctypes.c_size_t] * 2 + [ctypes.c_int] * 2 + [ctypes.c_double] + [ctypes.c_void_p] * 5),
+    "mr_layer_norm_backward": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_size_t] * 2 + [ctypes.c_int] * 2 +
+                               [ctypes.c_void_p] * 4),
+    "mr_grad_norm": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_uint64), ctypes.c_int,
+                                    ctypes.c_int, ctypes.c_double, ctypes.c_double, ctypes.c_void_p, ctypes.c_void_p]),
+    "mr_adamw_state_elems": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint64), ctypes.c_int,
+                                            ctypes.POINTER(ctypes.c_uint64)]),
+    "mr_adamw_step": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p),
+                                     ctypes.POINTER(ctypes.c_uint64)] + [ctypes.c_int] * 4 +
+                      [ctypes.POINTER(_AdamWStateC), ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(_AdamWStateC),
+                       ctypes.POINTER(_AdamWHyperC), ctypes.c_void_p, ctypes.c_void_p]),
     "mr_set_option": (ctypes.c_int, [ctypes.c_int, ctypes.c_int64]),
     "mr_get_option": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_int64)]),
 }
@@ -299,6 +326,229 @@ def allgather_list(shards: Sequence, outs: Sequence, stream=None):
     _check(lib().mr_allgather_list(ptrs, len(shards), shards[0].numel(), DTYPE_CODE[dtype_name(shards[0])], optrs,
                                    _stream_handle(stream)), "mr_allgather_list")
     return outs
+
+
+# ------------------------------------------------------------- the training step around the exchange
+
+def _opt(t, what: str, ref_dtype, numel: int):
+    """Pointer of an optional tensor of ``numel`` elements of one of the dtypes ``ref_dtype``; None stays None."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.is_contiguous() and t.numel() == numel and t.dtype in ref_dtype):
+        raise ValueError(f"{what} must be a contiguous device tensor of {numel} elements of {' or '.join(map(str, ref_dtype))}")
+    return t.data_ptr()
+
+
+def _weights_dtype(ref, *weights):
+    """The dtype of the weights that are given (ref's or fp32, all alike; ref's if none is)."""
+    have = [w.dtype for w in weights if w is not None]
+    wdt = have[0] if have else ref.dtype
+    if any(d != wdt for d in have) or (wdt != ref.dtype and wdt != _torch().float32):
+        raise ValueError(f"weights and their gradients must all be {ref.dtype} or all torch.float32")
+    return wdt
+
+
+def _ptr_array(ptrs):
+    return (ctypes.c_void_p * max(len(ptrs), 1))(*ptrs)
+
+
+def prepare_layer_norm_forward(bufs: Sequence, gamma, beta, y, eps: float = 1e-5, residual=None, x_out=None, mean=None,
+                               rstd=None, stream=None):
+    """Pre-marshalled mr_layer_norm_forward over the last dimension of ``y``."""
+    _dev_tensor(y, "y")
+    n, cols = y.numel(), y.shape[-1] if y.dim() else 1
+    rows, f32 = n // cols if cols else 0, (_torch().float32,)
+    same, wdt = (y.dtype,), _weights_dtype(y, gamma, beta)
+    ptrs = _ptr_array([_opt(b, "rank buffer", same, n) for b in bufs])
+    dt = DTYPE_CODE[dtype_name(y)]
+    args = (ptrs, len(bufs), _opt(residual, "residual", same, n), _opt(gamma, "gamma", (wdt,), cols),
+            _opt(beta, "beta", (wdt,), cols), rows, cols, dt, dt if wdt == y.dtype else DTYPE_CODE["fp32"], eps,
+            _opt(x_out, "x_out", same, n), y.data_ptr(), _opt(mean, "mean", f32, rows), _opt(rstd, "rstd", f32, rows),
+            _stream_handle(stream))
+    return _prepared("mr_layer_norm_forward", lib().mr_layer_norm_forward, args,
+                     (list(bufs), gamma, beta, y, residual, x_out, mean, rstd))
+
+
+def layer_norm_forward(bufs: Sequence, gamma, beta, y, eps: float = 1e-5, residual=None, x_out=None, mean=None, rstd=None,
+                       stream=None):
+    """y = layer norm, over the last dimension, of x = the fp32 sum of the tensors ``bufs`` (rank order) and ``residual``.
+
+    ``bufs`` with one tensor and no residual is a plain layer norm; with W tensors it is what follows a
+    tensor-parallel all-reduce.  ``gamma`` / ``beta`` may be None (ones / zeros).  ``x_out`` receives x (the residual
+    stream, and the backward pass's input); ``mean`` and ``rstd`` (fp32, one per row) the statistics."""
+    prepare_layer_norm_forward(bufs, gamma, beta, y, eps, residual, x_out, mean, rstd, stream)()
+    return y
+
+
+def prepare_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None, stream=None):
+    """Pre-marshalled mr_layer_norm_backward."""
+    _dev_tensor(dy, "dy")
+    n, cols = dy.numel(), dy.shape[-1] if dy.dim() else 1
+    rows, f32 = n // cols if cols else 0, (_torch().float32,)
+    same, wdt = (dy.dtype,), _weights_dtype(dy, gamma, dgamma, dbeta)
+    if x is None or mean is None or rstd is None:
+        raise ValueError("x, mean and rstd are needed")
+    dt = DTYPE_CODE[dtype_name(dy)]
+    args = (dy.data_ptr(), _opt(x, "x", same, n), _opt(gamma, "gamma", (wdt,), cols), _opt(mean, "mean", f32, rows),
+            _opt(rstd, "rstd", f32, rows), _opt(dres, "dres", same, n), rows, cols, dt,
+            dt if wdt == dy.dtype else DTYPE_CODE["fp32"], _opt(dx, "dx", same, n), _opt(dgamma, "dgamma", (wdt,), cols),
+            _opt(dbeta, "dbeta", (wdt,), cols), _stream_handle(stream))
+    return _prepared("mr_layer_norm_backward", lib().mr_layer_norm_backward, args,
+                     (dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres))
+
+
+def layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None, stream=None):
+    """Gradients of layer_norm_forward: ``dx`` (of every rank buffer and the residual alike; plus ``dres``, the gradient
+    that reaches x beside the norm), ``dgamma`` and ``dbeta`` (sums over the rows).  Any of the three may be None."""
+    prepare_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres, stream)()
+    return dx
+
+
+def _tensor_list(tensors, what: str, counts=None):
+    """Pointers of contiguous device tensors of one dtype (and of the given element counts)."""
+    for i, t in enumerate(tensors):
+        if not (t.is_cuda and t.is_contiguous()) or t.dtype != tensors[0].dtype:
+            raise ValueError(f"{what} must be contiguous device tensors of one dtype")
+        if counts is not None and t.numel() != counts[i]:
+            raise ValueError(f"{what}[{i}] must hold {counts[i]} elements")
+    if counts is not None and len(tensors) != len(counts):
+        raise ValueError(f"{what}: {len(counts)} tensors are needed")
+    return _ptr_array([t.data_ptr() or None for t in tensors])
+
+
+def prepare_grad_norm(grads: Sequence, out, max_norm: float = 0.0, scale: float = 1.0, stream=None):
+    """Pre-marshalled mr_grad_norm."""
+    grads = list(grads)
+    _opt(out, "out", (_torch().float32,), 3)
+    _dev_tensor(out, "out")
+    ptrs = _tensor_list(grads, "grads")
+    counts = (ctypes.c_uint64 * max(len(grads), 1))(*[t.numel() for t in grads])
+    dt = DTYPE_CODE[dtype_name(grads[0])] if grads else DTYPE_CODE["fp32"]
+    args = (ptrs, counts, len(grads), dt, scale, max_norm, out.data_ptr(), _stream_handle(stream))
+    return _prepared("mr_grad_norm", lib().mr_grad_norm, args, (grads, out))
+
+
+def grad_norm(grads: Sequence, out, max_norm: float = 0.0, scale: float = 1.0, stream=None):
+    """out (3 floats) = [N, factor, finite]: N = scale * the 2-norm of all ``grads`` together, factor = scale * min(1,
+    max_norm / (N + 1e-6)) (scale alone without a max_norm), finite = 1 if every element is finite, else 0 (and factor
+    0).  adamw_step takes it as ``clip``."""
+    prepare_grad_norm(grads, out, max_norm, scale, stream)()
+    return out
+
+
+@dataclasses.dataclass
+class AdamWState:
+    """The flat optimizer state of a list of tensors (mr_adamw_step's layout: each tensor's part starts on a multiple of
+    32 elements).  32-bit moments: ``m`` and ``v`` fp32.  8-bit (MXFP8): ``m`` and ``v`` (the second moment's square
+    root) torch.float8_e4m3fn with one torch.float8_e8m0fnu scale per 32 elements in ``m_scale`` and ``v_scale``.
+    ``master``: fp32 copies of 16-bit parameters, or None."""
+
+    m: Any
+    v: Any
+    m_scale: Any = None
+    v_scale: Any = None
+    master: Any = None
+
+    @property
+    def bits(self) -> int:
+        return 32 if self.m_scale is None else 8
+
+    def moments(self):
+        """(m, v) as fp32: what the state stands for, for inspection and checkpoints."""
+        if self.bits == 32:
+            return self.m, self.v
+        m, r = (q.float().view(-1, ADAMW_BLOCK).mul(s.float().view(-1, 1)).view(-1)
+                for q, s in ((self.m, self.m_scale), (self.v, self.v_scale)))
+        return m, r * r
+
+
+def adamw_offsets(counts: Sequence[int]) -> tuple[list[int], int]:
+    """(first element of each tensor in the flat state, its total length)."""
+    c = (ctypes.c_uint64 * max(len(counts), 1))(*counts)
+    total = ctypes.c_uint64(0)
+    _check(lib().mr_adamw_state_elems(c, len(counts), ctypes.byref(total)), "mr_adamw_state_elems")
+    at, n = [], 0
+    for k in counts:
+        at.append(n)
+        n += -(-k // ADAMW_BLOCK) * ADAMW_BLOCK
+    return at, int(total.value)
+
+
+def adamw_init(params: Sequence, bits: int = 32, master: bool = False) -> AdamWState:
+    """A zero state for ``params``; with ``master``, fp32 copies of them."""
+    torch = _torch()
+    if bits not in STATE_FORMAT:
+        raise ValueError("bits must be 32 or 8")
+    counts = [p.numel() for p in params]
+    at, n = adamw_offsets(counts)
+    dev = params[0].device
+    st = AdamWState(torch.zeros(n, device=dev), torch.zeros(n, device=dev)) if bits == 32 else AdamWState(
+        *(torch.zeros(n, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)),
+        *(torch.zeros(n // ADAMW_BLOCK, dtype=torch.uint8, device=dev).view(torch.float8_e8m0fnu) for _ in range(2)))
+    if master:
+        st.master = torch.zeros(n, device=dev)
+        for p, a, k in zip(params, at, counts):
+            st.master[a:a + k].copy_(p.detach().reshape(-1))
+    return st
+
+
+def _state_c(st: AdamWState, n: int) -> _AdamWStateC:
+    torch = _torch()
+    if st.m is None or st.v is None:
+        raise ValueError("the state needs m and v")
+    if st.bits == 32:
+        want, scales = (torch.float32,), (None, None)
+        if st.v_scale is not None:
+            raise ValueError("v_scale without m_scale")
+    else:
+        want, f8 = (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
+        scales = (_opt(st.m_scale, "m_scale", f8, n // ADAMW_BLOCK), _opt(st.v_scale, "v_scale", f8, n // ADAMW_BLOCK))
+    return _AdamWStateC(_opt(st.m, "m", want, n), _opt(st.v, "v", want, n), *scales,
+                        _opt(st.master, "master", (torch.float32,), n))
+
+
+def prepare_adamw(params: Sequence, grads: Sequence, state: AdamWState, params_out=None, state_out: AdamWState | None = None,
+                  betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01, clip=None, seed: int = 0, stream=None):
+    """Pre-marshalled mr_adamw_step for tensors that stay where they are: the returned ``call(lr, step)`` takes step
+    ``step`` (from 1).  Results go in place, or to ``params_out`` / ``state_out``."""
+    params, grads = list(params), list(grads)
+    counts = [p.numel() for p in params]
+    _, n = adamw_offsets(counts)
+    pp, gp = _tensor_list(params, "params"), _tensor_list(grads, "grads", counts)
+    po = None if params_out is None else _tensor_list(list(params_out), "params_out", counts)
+    if params_out is not None and params and params_out[0].dtype != params[0].dtype:
+        raise ValueError("params_out must be of the params' dtype")
+    if params and dtype_name(grads[0]) not in (dtype_name(params[0]), "fp32"):
+        raise ValueError("grads must be of the params' dtype or torch.float32")
+    sin = _state_c(state, n)
+    if state_out is not None and state_out.bits != state.bits:
+        raise ValueError("state_out must be in the state's format")
+    sout = None if state_out is None else _state_c(state_out, n)
+    _opt(clip, "clip", (_torch().float32,), 3)
+    hyper = _AdamWHyperC(0.0, betas[0], betas[1], eps, weight_decay, 0, seed)
+    args = (pp, gp, (ctypes.c_uint64 * max(len(counts), 1))(*counts), len(counts),
+            DTYPE_CODE[dtype_name(params[0])] if params else 2, DTYPE_CODE[dtype_name(grads[0])] if grads else 2,
+            STATE_FORMAT[state.bits], ctypes.byref(sin), po, None if sout is None else ctypes.byref(sout), ctypes.byref(hyper),
+            None if clip is None else clip.data_ptr(), _stream_handle(stream))
+    f = lib().mr_adamw_step
+
+    def call(lr: float, step: int) -> None:
+        hyper.lr, hyper.step = lr, step
+        st = f(*args)
+        if st != MR_OK:
+            raise MRError(st, "mr_adamw_step")
+
+    call.keepalive = (params, grads, state, params_out, state_out, clip, sin, sout, hyper)
+    return call
+
+
+def adamw_step(params: Sequence, grads: Sequence, state: AdamWState, lr: float, step: int, params_out=None,
+               state_out: AdamWState | None = None, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+               clip=None, seed: int = 0, stream=None) -> None:
+    """One AdamW step (decoupled weight decay) over all ``params`` in one launch per 80 tensors, in place or into
+    ``params_out`` / ``state_out``.  ``clip``: grad_norm's record, whose factor multiplies the gradients and which leaves the
+    step out where a gradient is not finite.  ``seed``: of the 8-bit state's stochastic rounding."""
+    prepare_adamw(params, grads, state, params_out, state_out, betas, eps, weight_decay, clip, seed, stream)(lr, step)
 
 
 def workspace_bytes(W: int, n: int, dtype: str) -> int:

@@ -15,6 +15,7 @@
 
 #include "mr_internal.h"
 #include "mr_probe.h"
+#include "mr_train.h"
 
 namespace {
 
@@ -406,9 +407,20 @@ namespace mr {
 
 void set_last_hip_error(int e) { g_last_hip_error = e; }
 
+bool trace_on() { return g_trace; }
+
 size_t workspace_bytes_for(size_t n, int esize) { return ws_bytes_for(n, esize); }
 
 hipError_t clear_workspace_words(char* base, size_t bytes, hipStream_t st) { return ws_clear(base, bytes, st); }
+
+mr_status stream_workspace(hipStream_t st, size_t bytes, Ctrl** ctrl, char** data) {
+  Workspace ws;
+  const mr_status s = get_workspace(st, bytes, 1, 0, &ws);
+  if (s != MR_OK) return s;
+  *ctrl = reinterpret_cast<Ctrl*>(ws.base);
+  *data = ws.base + ws_stage_offset(ws.bytes);
+  return MR_OK;
+}
 
 mr_status check_allreduce_args(const void* const* bufs, int W, size_t n, mr_dtype dtype, const void* out, mr_mode mode) {
   if (W < 1 || W > MR_MAX_W) return MR_ERR_INVALID_ARG;

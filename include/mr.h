@@ -223,6 +223,120 @@ mr_status mr_allgather_param_contig_shards(const void* const* shards, int W, int
                                            mr_dtype dtype, void* out, mr_stream stream);
 
 /*
+ * mr_layer_norm_forward -- layer norm of the sum of W rank buffers and a residual.
+ *
+ * For every row of `cols` elements, in fp32 and in this order,
+ *     x = widen(bufs[0]) + widen(bufs[1]) + ... + widen(bufs[W-1]) + widen(residual)
+ *     mean = avg(x),  var = avg((x - mean)^2),  rstd = 1 / sqrt(var + eps)
+ *     y = narrow((x - mean) * rstd * gamma + beta)
+ * W = 1 without a residual is a plain layer norm.  W > 1 is what follows a tensor-parallel all-reduce: the
+ * one-shot sum of mr_allreduce_sum, the residual and the norm in one pass, x rounded once, when it is stored.
+ *
+ *  bufs      host array of W (1 .. MR_MAX_W) device pointers, each rows*cols elements of `dtype`.
+ *  residual  device, rows*cols elements, or NULL.
+ *  gamma, beta  device, cols elements of `wdtype`; NULL stands for ones / zeros.
+ *  dtype     MR_BF16, MR_FP16 or MR_FP32; wdtype: dtype or MR_FP32.  Others -> MR_ERR_DTYPE.
+ *  x_out     device, rows*cols elements: narrow(x), the residual stream and what the backward pass takes; or NULL.
+ *  y         device, rows*cols elements.
+ *  mean, rstd  device, rows floats each, for the backward pass; or NULL.
+ *  x_out and y may each be one of the bufs or the residual exactly; any other overlap of an output with an
+ *  input or another output -> MR_ERR_ALIAS.  Pointers are multiples of their element size (else
+ *  MR_ERR_INVALID_ARG); rows need not start on any larger grid.  rows == 0 or cols == 0 is a no-op.
+ *  cols < 2^31, eps finite and >= 0.  Infinities and NaN give what the formula gives, in their row only.
+ */
+mr_status mr_layer_norm_forward(const void* const* bufs, int W, const void* residual, const void* gamma, const void* beta,
+                                size_t rows, size_t cols, mr_dtype dtype, mr_dtype wdtype, double eps, void* x_out, void* y,
+                                float* mean, float* rstd, mr_stream stream);
+
+/*
+ * mr_layer_norm_backward -- the gradients of mr_layer_norm_forward.
+ *
+ * With xh = (x - mean) * rstd and gd = gamma * dy (rows as above, fp32),
+ *     dx     = narrow(rstd * (gd - avg(gd) - xh * avg(gd * xh)) + dres)
+ *     dgamma = sum over rows of dy * xh,   dbeta = sum over rows of dy      (rounded once, to wdtype)
+ * dx is the gradient of every rank buffer and of the residual alike.  The weight gradients' sums are fp32 in an
+ * order set by the shape alone: results are the same bits on every call.
+ *
+ *  dy, x     device, rows*cols elements of `dtype`; x is the forward pass's x_out (or its one buffer).
+ *  gamma     as in the forward pass (NULL: ones);  mean, rstd: rows floats from the forward pass.
+ *  dres      device, rows*cols elements: the gradient that reaches x beside the norm; or NULL.
+ *  dx        device, rows*cols elements, or NULL; may be dy, x or dres exactly.
+ *  dgamma, dbeta  device, cols elements of `wdtype`, or NULL.  With rows == 0 they become zeros.
+ *  Other overlaps, types and alignments as above.  Takes up to 16 MiB for cols <= 8192 (more for wider rows) of the
+ *  stream's library workspace (see mr_set_workspace) for the weight gradients.
+ */
+mr_status mr_layer_norm_backward(const void* dy, const void* x, const void* gamma, const float* mean, const float* rstd,
+                                 const void* dres, size_t rows, size_t cols, mr_dtype dtype, mr_dtype wdtype, void* dx,
+                                 void* dgamma, void* dbeta, mr_stream stream);
+
+/*
+ * mr_grad_norm -- the 2-norm of a list of gradients and the factor that clips it.
+ *
+ *     out[0] = N = scale * sqrt(sum over all tensors of g^2)
+ *     out[1] = scale * min(1, max_norm / (N + 1e-6))     (scale alone where max_norm <= 0)
+ *     out[2] = 1 if every element is finite, else 0      (out[1] is then 0)
+ * The sum is fp64 and in an order set by the sizes alone.  mr_adamw_step takes `out` as its `clip`, so a
+ * step reads the factor on the device and is left out where a gradient is not finite, with no host round trip.
+ *
+ *  grads   host array of P device pointers, counts[i] elements of `dtype` (MR_BF16, MR_FP16, MR_FP32) each,
+ *          multiples of the element size; counts[i] == 0 allowed (its pointer is not read), and P == 0.
+ *  scale   finite and > 0: e.g. 1 / the loss scale.  max_norm: finite.
+ *  out     device, 3 floats; overlap with a gradient -> MR_ERR_ALIAS.
+ *  Takes a few KiB of the stream's library workspace.
+ */
+mr_status mr_grad_norm(const void* const* grads, const uint64_t* counts, int P, mr_dtype dtype, double scale,
+                       double max_norm, float* out, mr_stream stream);
+
+/*
+ * mr_adamw_step -- one AdamW step over a list of tensors.
+ *
+ * For every element, in fp32, with step t and f = clip[1] (1 without clip),
+ *     g = f * grad,  m' = beta1*m + (1-beta1)*g,  v' = beta2*v + (1-beta2)*g^2
+ *     p' = (1 - lr*weight_decay)*p - lr/(1-beta1^t) * m' / (sqrt(v')/sqrt(1-beta2^t) + eps)
+ *
+ * The optimizer state is flat: tensor i's part starts at the sum of the earlier counts, each rounded up to a
+ * multiple of 32, and mr_adamw_state_elems gives its total length.  Elements between tensors are kept at 0.
+ *
+ * MR_STATE_FP32:  m and v are floats.  m_scale and v_scale are NULL.
+ * MR_STATE_MXFP8: m and v are bytes, E4M3 numbers in blocks of 32 that share a scale 2^(b-127), b the block's
+ *     byte in m_scale / v_scale (the OCP microscaling format MXFP8).  v holds the square root of the second
+ *     moment.  The scale is the smallest that brings the block's largest magnitude to 448 or less (b = 255: not
+ *     finite, the whole block reads as NaN).  Values are rounded to one of their two neighbours, up with
+ *     probability (distance to the lower) / (spacing), by 16 bits of a hash of (seed, t, element): calls with the same
+ *     arguments give the same bits.  A second moment that is not zero is never rounded to zero.  A state of zero bytes is
+ *     the start.  The step itself uses m' and v' before they are rounded.
+ * master: floats, or NULL.  With it, p is read from master and written to both; `params` is not read (and may be NULL
+ *     if params_out is given).  Only for 16-bit parameters.
+ *
+ *  params, grads  host arrays of P device pointers, counts[i] elements each, of dtype and grad_dtype (MR_FP32, or
+ *           MR_BF16/MR_FP16 with grad_dtype the same or MR_FP32), multiples of their element size.
+ *  state    host struct of device pointers, 256-byte aligned (scales: any).
+ *  params_out, state_out  where results go; NULL: in place.  Each output may be its own input exactly; any
+ *           other overlap -> MR_ERR_ALIAS.
+ *  hyper    host struct; beta1, beta2 in [0, 1), eps >= 0, lr and weight_decay finite, t >= 1.
+ *  clip     device, mr_grad_norm's 3 floats, or NULL.  Where clip[2] is 0 the step is not taken: outputs
+ *           are the inputs (params_out the rounded master, with one).
+ *  Up to 80 tensors go in one launch; counts[i] == 0 is allowed, counts[i] <= 2^33.
+ */
+typedef enum mr_state_format { MR_STATE_FP32 = 0, MR_STATE_MXFP8 = 1 } mr_state_format;
+typedef struct mr_adamw_state {
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  float* master;
+} mr_adamw_state;
+typedef struct mr_adamw_hyper {
+  double lr, beta1, beta2, eps, weight_decay;
+  uint64_t step; /* t, from 1 */
+  uint64_t seed;
+} mr_adamw_hyper;
+mr_status mr_adamw_state_elems(const uint64_t* counts, int P, uint64_t* elems);
+mr_status mr_adamw_step(const void* const* params, const void* const* grads, const uint64_t* counts, int P, mr_dtype dtype,
+                        mr_dtype grad_dtype, mr_state_format format, const mr_adamw_state* state, void* const* params_out,
+                        const mr_adamw_state* state_out, const mr_adamw_hyper* hyper, const float* clip, mr_stream stream);
+
+/*
  * Two-shot workspace.
  *
  * By default the library allocates, on first two-shot use of a (device, stream) pair, a grow-only
