@@ -33,7 +33,7 @@ struct Ctrl {
   uint32_t err[64];              // bit 0: a wait gave up after the spin limit (that call's output is not
                                  // valid); bits 1 and 2: the XCD-local two-shot recomputed units after a
                                  // wait gave up / whose producer ran on another XCD (output valid)
-  uint32_t arrived[64];          // workgroups of a gradient norm that have written their sums
+  uint32_t arrived[9][64];       // gradient norm: workgroups that have written their sums, in 8 sets, and complete sets
 };
 static_assert(sizeof(Ctrl) <= kCtrlBytes, "ctrl layout");
 

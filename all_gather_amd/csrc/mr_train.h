@@ -6,9 +6,14 @@
 namespace mr {
 
 // ---------------------------------------------------------------------------------------- layer norm
+constexpr int kNormPack = 8;  // elements per pack: what a lane takes of a row at once
+
+// The lanes that hold a row with one pack each, from the row's packs (a wave's part up to 64, whole waves above).
+inline int norm_lanes(size_t packs) {
+  return packs <= 8 ? 8 : packs <= 32 ? 32 : packs <= 64 ? 64 : packs <= 128 ? 128 : packs <= 256 ? 256 : packs <= 512 ? 512 : 1024;
+}
 struct NormFwdArgs {
-  const char* in[MR_MAX_W];  // rank buffers, added in order
-  const char* residual;      // added last; may be null
+  const char* in[MR_MAX_W + 1];  // the rank buffers and then the residual, added in this order
   const char* gamma;         // null: ones
   const char* beta;          // null: zeros
   char* x_out;               // may be null
@@ -17,7 +22,7 @@ struct NormFwdArgs {
   float* rstd;               // may be null
   size_t rows, cols;
   float eps;
-  int W;
+  int terms;                 // entries of `in`
 };
 hipError_t launch_norm_fwd(const NormFwdArgs& a, mr_dtype dt, mr_dtype wdt, hipStream_t st);
 
@@ -41,18 +46,19 @@ uint32_t norm_bwd_groups(size_t rows, size_t cols);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, mr_dtype dt, mr_dtype wdt, hipStream_t st);
 
 // --------------------------------------------------------------------------------- gradient norm, AdamW
-constexpr int kNormTensors = 128;          // tensors per launch (their table rides in the kernel arguments)
-constexpr uint32_t kNormTile = 4096;       // elements per tile
-constexpr uint32_t kNormMaxGroups = 2048;  // workgroups, and so partial sums, per launch
+constexpr int kNormTensors = 128;           // tensors per launch (their table rides in the kernel arguments)
+constexpr uint32_t kNormTileBytes = 16384;  // of one tensor
+constexpr uint32_t kNormMaxGroups = 512;    // workgroups, and so partial sums, per launch: two to a compute unit
+constexpr uint32_t kNormSets = 8;           // arrivals are counted in sets, then sets: one address takes 11.6 ns an arrival
 struct GradNormArgs {
   const char* g[kNormTensors];
   uint64_t n[kNormTensors];
   uint32_t tile_prefix[kNormTensors + 1];
   uint32_t P;
-  double* part;        // partial sums of squares, one per workgroup of every launch of the call
-  uint32_t part_base;  // this launch's first one
-  uint32_t finish;     // 1: the last launch; its last workgroup adds all of them up
-  uint32_t* arrived;   // zero between launches
+  double* part;             // partial sums of squares, one per workgroup of every launch of the call
+  uint32_t part_base;       // this launch's first one
+  uint32_t finish;          // 1: the last launch; its last workgroup adds all of them up
+  uint32_t (*arrived)[64];  // zero between launches
   double scale, max_norm;
   float* out;
 };

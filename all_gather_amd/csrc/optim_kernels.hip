@@ -21,78 +21,110 @@
 namespace mr {
 namespace {
 
-constexpr int kLanes = 256;
-
-// The tensor whose tiles hold tile t: tile_prefix[s] <= t < tile_prefix[s + 1].
-__device__ __forceinline__ uint32_t tensor_of(const uint32_t* tile_prefix, uint32_t P, uint32_t t) {
-  uint32_t lo = 0, hi = P;
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) >> 1;
-    if (tile_prefix[mid] <= t) lo = mid; else hi = mid;
+// The tensor whose tiles hold tile t: tile_prefix[s] <= t < tile_prefix[s + 1].  Every lane holds entries of the table
+// and compares them at once: a search would wait for a load of the launch's arguments at each of its steps.
+template <int N>
+struct TensorTable {
+  static constexpr int kWords = (N + 63) / 64;
+  uint32_t first[kWords];
+  __device__ TensorTable(const uint32_t* tile_prefix, uint32_t P) {
+    const uint32_t lane = threadIdx.x & 63;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const uint32_t i = w * 64 + lane;
+      first[w] = i < P ? tile_prefix[i] : 0xffffffffu;
+    }
   }
-  return lo;
-}
+  __device__ uint32_t find(uint32_t t) const {
+    uint32_t n = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(first[w] <= t));
+    return n - 1;
+  }
+};
 
 // --------------------------------------------------------------------------------------- gradient norm
 
+constexpr int kNormLanes = 512;
+
 // Sum of x over the workgroup, in every lane.
 __device__ __forceinline__ double group_sum(double x) {
-  __shared__ double lds[kLanes / 64];
+  __shared__ double lds[kNormLanes / 64];
   x = wave_sum(x);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
   __syncthreads();
   x = 0.0;
 #pragma unroll
-  for (int i = 0; i < kLanes / 64; ++i) x += lds[i];
+  for (int i = 0; i < kNormLanes / 64; ++i) x += lds[i];
   return x;
 }
 
 // Squares are added in fp64: fp32's rate on this part's vector units, and a sum of fp32 squares that no finite
-// gradient overflows, so the sum is finite exactly where every gradient is.  The workgroup that arrives last
-// adds the workgroups' sums in their order: the result does not depend on which one that is.
+// gradient overflows, so the sum is finite exactly where every gradient is.  Workgroups walk the tiles, the next one's
+// loads issued before this one's sums.  The workgroup that arrives last adds the workgroups' sums in their order: the
+// result does not depend on which one that is.
 template <class T>
-__global__ __launch_bounds__(kLanes) void grad_norm(GradNormArgs a) {
+__global__ __launch_bounds__(kNormLanes) void grad_norm(GradNormArgs a) {
   constexpr int kN = 16 / T::kSize;  // elements per 16-byte pack
-  constexpr int kU = kNormTile / (kLanes * kN);
-  double s = 0.0;
-  for (uint32_t t = blockIdx.x; t < a.tile_prefix[a.P]; t += gridDim.x) {
-    const uint32_t i = tensor_of(a.tile_prefix, a.P, t);
-    const uint64_t e0 = static_cast<uint64_t>(t - a.tile_prefix[i]) * kNormTile;
+  constexpr uint32_t kTile = kNormTileBytes / T::kSize;
+  constexpr int kU = kTile / (kNormLanes * kN);
+  const TensorTable<kNormTensors> table(a.tile_prefix, a.P);
+  const uint32_t tiles = a.tile_prefix[a.P];
+  struct Tile {
+    Raw<T, kN> r[kU];
+  };
+  auto fetch = [&](uint32_t t) {
+    Tile x;
+    const uint32_t i = table.find(t);
+    const uint64_t e0 = static_cast<uint64_t>(t - a.tile_prefix[i]) * kTile;
     const uint64_t left = a.n[i] - e0;
     const char* p = a.g[i] + e0 * T::kSize;
-    Raw<T, kN> r[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const uint32_t e = (u * kLanes + threadIdx.x) * kN;
-      const int cnt = e >= left ? 0 : left - e < kN ? static_cast<int>(left - e) : kN;
-      r[u] = load_part<T, kN, true>(p + e * T::kSize, cnt);
+      const uint32_t e = (u * kNormLanes + threadIdx.x) * kN;
+      if (left >= kTile)
+        x.r[u] = load_raw<T, kN, true>(p + e * T::kSize);
+      else
+        x.r[u] = load_part<T, kN, true>(p + e * T::kSize, e >= left ? 0 : left - e < kN ? static_cast<int>(left - e) : kN);
     }
+    return x;
+  };
+  double s = 0.0;
+  uint32_t t = blockIdx.x;
+  Tile next;
+  if (t < tiles) next = fetch(t);
+  for (; t < tiles; t += gridDim.x) {
+    const Tile now = next;
+    if (t + gridDim.x < tiles) next = fetch(t + gridDim.x);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       float f[kN];
-      widen(r[u], f);
+      widen(now.r[u], f);
 #pragma unroll
       for (int j = 0; j < kN; ++j) s = __builtin_fma(static_cast<double>(f[j]), static_cast<double>(f[j]), s);
     }
   }
   s = group_sum(s);
-  const uint32_t mine = a.part_base + blockIdx.x;
-  __shared__ uint32_t last;
+  __shared__ bool last;
   if (threadIdx.x == 0) {
-    __hip_atomic_store(a.part + mine, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = 0;
-    if (a.finish)
-      last = __hip_atomic_fetch_add(a.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    __hip_atomic_store(a.part + a.part_base + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = false;
+    if (a.finish) {
+      const uint32_t set = blockIdx.x % kNormSets, sets = gridDim.x < kNormSets ? gridDim.x : kNormSets;
+      const uint32_t members = (gridDim.x - set + kNormSets - 1) / kNormSets;
+      if (__hip_atomic_fetch_add(&a.arrived[set][0], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == members - 1)
+        last = __hip_atomic_fetch_add(&a.arrived[kNormSets][0], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == sets - 1;
+    }
   }
   __syncthreads();
   if (!last) return;
   s = 0.0;
-  for (uint32_t i = threadIdx.x; i < a.part_base + gridDim.x; i += kLanes)
+  for (uint32_t i = threadIdx.x; i < a.part_base + gridDim.x; i += kNormLanes)
     s += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   s = group_sum(s);
+  if (threadIdx.x <= kNormSets) __hip_atomic_store(&a.arrived[threadIdx.x][0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   if (threadIdx.x == 0) {
-    __hip_atomic_store(a.arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const double norm = a.scale * __builtin_sqrt(s);
     const bool finite = norm <= 1.7976931348623157e308;  // false for NaN too
     double f = a.max_norm > 0.0 ? a.max_norm / (norm + 1e-6) : 1.0;
@@ -126,20 +158,6 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
   return x > z ? x : z;
 }
 
-// |y| (0 .. 448) on the E4M3 grid, up with probability (distance to the lower neighbour) / (spacing): r16 / 2^16
-// of a spacing is added and the bits below the third mantissa bit are dropped.  Below 2^-6, the smallest normal
-// number, the spacing stays 2^-9: adding 2^-6 first puts it there.
-__device__ __forceinline__ float round_e4m3(float y, uint32_t r16) {
-  const float small = y < 0.015625f ? 0.015625f : 0.0f;
-  const uint32_t b = (__float_as_uint(y + small) + (r16 << 4)) & 0xfff00000u;
-  return __uint_as_float(b) - small;
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b, uint32_t old, bool high) {
-  return high ? __builtin_amdgcn_cvt_pk_fp8_f32(a, b, static_cast<int>(old), true)
-              : __builtin_amdgcn_cvt_pk_fp8_f32(a, b, static_cast<int>(old), false);
-}
-
 // 32 random bits of element idx of the flat state: a Weyl step on the key of (seed, step) and one
 // multiply-xorshift round.
 __device__ __forceinline__ uint32_t random_bits(uint32_t key, uint64_t idx) {
@@ -165,7 +183,11 @@ __device__ __forceinline__ void mx_load(const char* c, uint32_t byte, float (&f)
 }
 
 // This lane's eight of the block's 32 values (four neighbouring lanes hold a block) as codes; the block's byte.
-template <bool Floor, int Shift>
+// v_cvt_sr_fp8_f32 adds the random word's upper 20 bits below the third mantissa bit (below 2^-6, the smallest
+// normal number, below the 2^-9 place) and drops what lies there: up with probability (distance to the lower
+// neighbour) / (spacing).  It takes 16 of them here, from the lower half of r, or for `Second` from the upper half.  Second
+// moments are raised to the smallest code, 2^-9, unless they are zero.
+template <bool Second>
 __device__ __forceinline__ u32x2 mx_encode(const float (&f)[8], const uint32_t (&r)[8], uint32_t* byte) {
   uint32_t top = 0;
 #pragma unroll
@@ -176,24 +198,37 @@ __device__ __forceinline__ u32x2 mx_encode(const float (&f)[8], const uint32_t (
   const uint32_t e = mx_byte(quad_max(top));
   *byte = e;
   const float inv = __uint_as_float((254u - (e < 253u ? e : 253u)) << 23);
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = __builtin_fabsf(f[i]) * inv;
-    q[i] = round_e4m3(y, (r[i] >> Shift) & 0xffffu);
-    if (Floor) q[i] = y > 0.0f && q[i] == 0.0f ? 0.001953125f : q[i];
-    q[i] = e == 255u ? 0.0f : __builtin_copysignf(q[i], f[i]);
-  }
-  u32x2 w = {0, 0};
+  u32x2 w;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    w[i] = e4m3x2(q[4 * i], q[4 * i + 1], 0, false);
-    w[i] = e4m3x2(q[4 * i + 2], q[4 * i + 3], w[i], true);
+    int x = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float y = f[4 * i + j] * inv;
+      if (Second) y = y > 0.0f ? __builtin_fmaxf(y, 0.001953125f) : 0.0f;
+      const uint32_t bits = Second ? r[4 * i + j] & 0xffff0000u : r[4 * i + j] << 16;
+      x = j == 0   ? __builtin_amdgcn_cvt_sr_fp8_f32(y, bits, x, 0)
+          : j == 1 ? __builtin_amdgcn_cvt_sr_fp8_f32(y, bits, x, 1)
+          : j == 2 ? __builtin_amdgcn_cvt_sr_fp8_f32(y, bits, x, 2)
+                   : __builtin_amdgcn_cvt_sr_fp8_f32(y, bits, x, 3);
+    }
+    w[i] = e == 255u ? 0u : static_cast<uint32_t>(x);
   }
   return w;
 }
 
 // ------------------------------------------------------------------------------------------------- AdamW
+
+constexpr int kLanes = 256;
+
+// sqrt and quotient from the hardware's square root and reciprocal, each within 1 ulp (the correctly rounded ones take
+// three times the operations, and the 8-bit step is bound by its operations).  v_sqrt_f32 flushes subnormals, so
+// small arguments are scaled by 2^64.  The divisor is never subnormal: it is at least eps, or the root of an fp32 number.
+__device__ __forceinline__ float root(float v) {
+  const bool small = v < 7.8886090522101181e-31f;  // 2^-100
+  const float r = __builtin_amdgcn_sqrtf(v * (small ? 18446744073709551616.0f : 1.0f));
+  return r * (small ? 2.3283064365386963e-10f : 1.0f);
+}
 
 // Elements a lane takes at once: 8 where the moments are bytes (8 codes are 8 bytes, four lanes a block), 4
 // where they are fp32 (one 16-byte access each).
@@ -235,7 +270,7 @@ __device__ __forceinline__ void keep_tile(const AdamArgs& a, uint32_t i, uint64_
 template <class T, class G, bool Mx, bool Master>
 __global__ __launch_bounds__(kLanes) void adamw(AdamArgs a) {
   constexpr int E = kLaneElems<Mx>;
-  const uint32_t i = tensor_of(a.tile_prefix, a.P, blockIdx.x);
+  const uint32_t i = TensorTable<kAdamTensors>(a.tile_prefix, a.P).find(blockIdx.x);
   const uint64_t e = static_cast<uint64_t>(blockIdx.x - a.tile_prefix[i]) * kTileElems<Mx> + threadIdx.x * E;
   const uint64_t n = a.n[i];
   const int cnt = e >= n ? 0 : n - e < E ? static_cast<int>(n - e) : E;
@@ -271,19 +306,24 @@ __global__ __launch_bounds__(kLanes) void adamw(AdamArgs a) {
 #pragma unroll
   for (int j = 0; j < E; ++j) {
     const float gj = g[j] * factor;
-    m[j] = j < cnt ? m[j] * a.b1 + gj * a.c1 : 0.0f;
-    v[j] = j < cnt ? v[j] * a.b2 + gj * gj * a.c2 : 0.0f;
-    r[j] = __builtin_sqrtf(v[j]);
-    const float u = m[j] / __builtin_fmaf(r[j], a.inv_sqrt_bc2, a.eps);
-    p[j] = j < cnt ? p[j] * a.keep - u * a.lr_t : 0.0f;
+    m[j] = m[j] * a.b1 + gj * a.c1;
+    v[j] = v[j] * a.b2 + gj * gj * a.c2;
+    r[j] = root(v[j]);
+    const float u = m[j] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[j], a.inv_sqrt_bc2, a.eps));
+    p[j] = p[j] * a.keep - u * a.lr_t;
+  }
+  if (cnt < E) {  // elements between tensors are kept at zero
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (j >= cnt) p[j] = m[j] = v[j] = r[j] = 0.0f;
   }
   if (cnt) store_part<T, E, true>(a.po[i] + e * T::kSize, p, cnt);
   if constexpr (Mx) {  // all lanes: the block's scale is the largest of four lanes' values
     uint32_t bits[E], mb, vb;
 #pragma unroll
     for (int j = 0; j < E; ++j) bits[j] = random_bits(a.key, idx + j);
-    const u32x2 mw = mx_encode<false, 0>(m, bits, &mb);
-    const u32x2 vw = mx_encode<true, 16>(r, bits, &vb);
+    const u32x2 mw = mx_encode<false>(m, bits, &mb);
+    const u32x2 vw = mx_encode<true>(r, bits, &vb);
     if (live) {
       __builtin_nontemporal_store(mw, reinterpret_cast<u32x2*>(a.out.m + idx));
       __builtin_nontemporal_store(vw, reinterpret_cast<u32x2*>(a.out.v + idx));
@@ -322,7 +362,7 @@ void adam_format(const AdamArgs& a, mr_state_format fmt, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_grad_norm(const GradNormArgs& a, mr_dtype dt, hipStream_t st) {
-  const dim3 grid(grad_norm_groups(a.tile_prefix[a.P])), block(kLanes);
+  const dim3 grid(grad_norm_groups(a.tile_prefix[a.P])), block(kNormLanes);
   if (dt == MR_FP32)
     hipLaunchKernelGGL((grad_norm<EFp32>), grid, block, 0, st, a);
   else if (dt == MR_BF16)

@@ -173,12 +173,30 @@ __device__ __forceinline__ void store_part(char* p, const float (&f)[N], int cnt
     if (i < cnt) store1<T>(p + i * T::kSize, f[i]);
 }
 
-// Sum over the 64 lanes of a wave, in every lane (a butterfly: the order is fixed).
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) x += __shfl_xor(x, m);
+// Sum over the B neighbouring lanes (8, 32 or 64) that hold a row, in every one of them, in a fixed order.  Moves within 16
+// lanes ride on the adds as DPP operands (quads by 1 and 2, then the mirrored half row and row); the four rows of a
+// wave are read into scalar registers.  A butterfly of LDS-routed shuffles took the backward pass 3% longer.
+template <int Ctrl>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), Ctrl, 0xf, 0xf, true));
+}
+template <int B>
+__device__ __forceinline__ float lanes_sum(float x) {
+  static_assert(B == 8 || B == 32 || B == 64, "lanes of a row");
+  x += dpp<0xB1>(x);   // quad lanes 1 0 3 2
+  x += dpp<0x4E>(x);   // quad lanes 2 3 0 1
+  x += dpp<0x141>(x);  // half row mirrored
+  if constexpr (B > 8) x += dpp<0x140>(x);  // row mirrored
+  if constexpr (B == 32) x += __shfl_xor(x, 16);
+  if constexpr (B == 64) {
+    const int b = __float_as_int(x);
+    x = (__int_as_float(__builtin_amdgcn_readlane(b, 0)) + __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
+        (__int_as_float(__builtin_amdgcn_readlane(b, 32)) + __int_as_float(__builtin_amdgcn_readlane(b, 48)));
+  }
   return x;
 }
+
+// Sum over the 64 lanes of a wave, in every lane (a butterfly: the order is fixed).
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
   for (int m = 32; m; m >>= 1) x += __shfl_xor(x, m);

@@ -120,7 +120,8 @@ mr_status layer_norm_forward(const void* const* bufs, int W, const void* residua
     return MR_ERR_ALIAS;
   for (int r = 0; r < W; ++r)
     if (!outs.admits(bufs[r], bytes, in_place)) return MR_ERR_ALIAS;
-  a.residual = static_cast<const char*>(residual);
+  a.terms = W;
+  if (residual) a.in[a.terms++] = static_cast<const char*>(residual);
   a.gamma = static_cast<const char*>(gamma);
   a.beta = static_cast<const char*>(beta);
   a.x_out = static_cast<char*>(x_out);
@@ -130,7 +131,6 @@ mr_status layer_norm_forward(const void* const* bufs, int W, const void* residua
   a.rows = rows;
   a.cols = cols;
   a.eps = static_cast<float>(eps);
-  a.W = W;
   if (mr::trace_on())
     std::fprintf(stderr, "[mr] layer_norm forward W=%d rows=%zu cols=%zu dtype=%d\n", W, rows, cols, static_cast<int>(dtype));
   const hipError_t e = mr::launch_norm_fwd(a, dtype, wdtype, st);
@@ -219,7 +219,7 @@ mr_status grad_norm(const void* const* grads, const uint64_t* counts, int P, mr_
   reset();
   for (int i = 0; i < P; ++i) {
     if (counts[i] == 0) continue;
-    const uint32_t tiles = static_cast<uint32_t>((counts[i] + mr::kNormTile - 1) / mr::kNormTile);
+    const uint32_t tiles = static_cast<uint32_t>((counts[i] * es + mr::kNormTileBytes - 1) / mr::kNormTileBytes);
     a.g[a.P] = static_cast<const char*>(grads[i]);
     a.n[a.P] = counts[i];
     a.tile_prefix[a.P + 1] = a.tile_prefix[a.P] + tiles;
