@@ -168,10 +168,16 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
 #pragma unroll
             for (int i = 0; i < kV; ++i) f[i] += part[(s * kV + i) * B + lane];
       }
-      if (sub == 0)
+      if (sub == 0) {
+        float* o = out + h * a.cols + c.at[k];
+        if (c.lo[k] == 0) {
+          store_raw<EFp32, kV, false>(reinterpret_cast<char*>(o), narrow<EFp32, kV>(f));
+        } else {
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-          if (i >= c.lo[k]) out[h * a.cols + c.at[k] + i] = f[i];
+          for (int i = 0; i < kV; ++i)
+            if (i >= c.lo[k]) o[i] = f[i];
+        }
+      }
     }
 }
 
@@ -249,24 +255,25 @@ __global__ __launch_bounds__(64) void norm_bwd_any_weights(NormBwdArgs a) {
   store_part<EFp32, kV, false>(reinterpret_cast<char*>(out + a.cols), db, cnt);
 }
 
-// dgamma and dbeta: the sum of the groups' rows of `part`.  A workgroup takes 64 of the 2*cols columns; its
-// 16 waves each add up every 16th group, and the first wave adds the 16 sums.
+// dgamma and dbeta: the sum of the groups' rows of `part`.  A workgroup takes 32 of the 2*cols columns; its 32
+// half waves each add up every 32nd group (8 loads of 256 groups, all in flight), and the first adds the 32 sums.
 template <class WT>
 __global__ __launch_bounds__(1024) void norm_bwd_finish(NormBwdArgs a) {
-  __shared__ float lds[16][64];
-  const size_t c = static_cast<size_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
-  const int w = threadIdx.x >> 6;
+  constexpr int kCols = 32, kParts = 1024 / kCols;
+  __shared__ float lds[kParts][kCols];
+  const size_t c = static_cast<size_t>(blockIdx.x) * kCols + threadIdx.x % kCols;
+  const uint32_t w = threadIdx.x / kCols;
   float s = 0.0f;
   if (c < 2 * a.cols) {
 #pragma unroll 8
-    for (uint32_t g = w; g < a.groups; g += 16) s += a.part[static_cast<size_t>(g) * 2 * a.cols + c];
+    for (uint32_t g = w; g < a.groups; g += kParts) s += a.part[static_cast<size_t>(g) * 2 * a.cols + c];
   }
-  lds[w][threadIdx.x & 63] = s;
+  lds[w][threadIdx.x % kCols] = s;
   __syncthreads();
   if (w || c >= 2 * a.cols) return;
   s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s += lds[i][threadIdx.x];
+  for (int i = 0; i < kParts; ++i) s += lds[i][threadIdx.x];
   char* out = c < a.cols ? a.dgamma : a.dbeta;
   if (out) store1<WT>(out + (c < a.cols ? c : c - a.cols) * WT::kSize, s);
 }
@@ -310,7 +317,7 @@ hipError_t bwd(const NormBwdArgs& a, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   if (a.dgamma || a.dbeta)
-    hipLaunchKernelGGL((norm_bwd_finish<WT>), dim3(static_cast<uint32_t>((2 * a.cols + 63) / 64)), dim3(1024), 0, st, a);
+    hipLaunchKernelGGL((norm_bwd_finish<WT>), dim3(static_cast<uint32_t>((2 * a.cols + 31) / 32)), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 

@@ -12,6 +12,9 @@
 namespace mr {
 namespace {
 
+#ifndef MR_NF_DEPTH
+#define MR_NF_DEPTH 3
+#endif
 #ifndef MR_NF_LANES
 #define MR_NF_LANES 256
 #endif
@@ -55,7 +58,7 @@ __global__ __launch_bounds__(B < kFwdLanes ? kFwdLanes : B) void norm_fwd_row(No
     const size_t at = row * a.cols;
     float x[K][kV];
     if constexpr (Sum) {
-      constexpr int kDepth = K >= 4 ? 1 : 4 / K;  // inputs loaded before the first is added
+      constexpr int kDepth = K >= 4 ? 1 : MR_NF_DEPTH / K;  // inputs loaded before the first is added
       for (int r = 0; r < a.terms; r += kDepth) {
         Raw<T, kV> w[kDepth][K];
 #pragma unroll
@@ -188,7 +191,7 @@ __global__ __launch_bounds__(B) void norm_fwd_any(NormFwdArgs a) {
 }
 
 #ifndef MR_NF_SUMALL
-#define MR_NF_SUMALL 0
+#define MR_NF_SUMALL 1
 #endif
 template <class T, class WT, int B, int K>
 void fwd_row(const NormFwdArgs& a, hipStream_t st) {
