@@ -6,12 +6,6 @@
 namespace mr {
 
 // ---------------------------------------------------------------------------------------- layer norm
-constexpr int kNormPack = 8;  // elements per pack: what a lane takes of a row at once
-
-// The lanes that hold a row with one pack each, from the row's packs (a wave's part up to 64, whole waves above).
-inline int norm_lanes(size_t packs) {
-  return packs <= 8 ? 8 : packs <= 32 ? 32 : packs <= 64 ? 64 : packs <= 128 ? 128 : packs <= 256 ? 256 : packs <= 512 ? 512 : 1024;
-}
 struct NormFwdArgs {
   const char* in[MR_MAX_W + 1];  // the rank buffers and then the residual, added in this order
   const char* gamma;         // null: ones
@@ -23,6 +17,7 @@ struct NormFwdArgs {
   size_t rows, cols;
   float eps;
   int terms;                 // entries of `in`
+  int waves;                 // waves to a row (set by the launch)
 };
 hipError_t launch_norm_fwd(const NormFwdArgs& a, mr_dtype dt, mr_dtype wdt, hipStream_t st);
 
@@ -39,10 +34,11 @@ struct NormBwdArgs {
   float* part;        // [groups][2][cols] partial weight gradients (null: none wanted)
   size_t rows, cols;
   uint32_t groups;
+  int waves;          // waves to a row (set by the launch)
 };
 // Row groups of the backward pass of this shape: each sums its rows' part of the weight gradients in
 // registers and writes one row of `part`.  A function of the shape alone, so results do not depend on the device.
-uint32_t norm_bwd_groups(size_t rows, size_t cols);
+uint32_t norm_bwd_groups(size_t rows, size_t cols, mr_dtype dt);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, mr_dtype dt, mr_dtype wdt, hipStream_t st);
 
 // --------------------------------------------------------------------------------- gradient norm, AdamW

@@ -13,44 +13,48 @@
 namespace mr {
 namespace {
 
-constexpr int kBwdLanes = 1024;
-#ifndef MR_NB_AHEAD
-#define MR_NB_AHEAD 1
-#endif
-constexpr int kDepth = MR_NB_AHEAD;
+constexpr int kBwdLanes = 1024;  // most lanes of a workgroup
 
-// Workgroup b of `groups` takes row sets b, b + groups, ...; a set is one row for each B lanes.  The next set's x and
-// dy are loaded before this set's sums where registers allow.
-template <class T, class WT, int B, int K>
+// Workgroup b of `groups` takes row sets b, b + groups, ...; a set is as many rows as the workgroup holds.  The next set's
+// x and dy are loaded before this set's sums where registers allow; as in the forward pass every full round issues the same
+// loads and stores on every path.
+template <class T, class WT, int B, int K, bool Dres>
 __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
-  constexpr int kRows = kBwdLanes / B;
-  constexpr bool kAhead = K == 1;  // and gamma stays in registers
-  __shared__ float lds[2][2][kBwdLanes / 64];
-  __shared__ float part[kRows > 1 ? kBwdLanes * kV : 1];
-  const int lane = threadIdx.x % B;
-  const RowPacks<B, K> c(static_cast<uint32_t>(a.cols), lane);
-  uint32_t sub = threadIdx.x / B;
-  if (B >= 64) sub = __builtin_amdgcn_readfirstlane(sub);
+  constexpr int kV = kPack<T>;
+  constexpr bool kAhead = K * kV <= 8;
+  constexpr bool kHold = K == 1;  // gamma stays in registers
+  __shared__ WaveWords lds[2][2][B == kWaves ? 8 : 1];  // rows of several waves: at most 8 fit a workgroup
+  __shared__ float part[K == 1 ? kBwdLanes / 2 * kV : 1];
+  const int lanes = B == kWaves ? a.waves * 64 : B;
+  const int lane = threadIdx.x % lanes;
+  const RowPacks<kV, K> c(static_cast<uint32_t>(a.cols), lane, lanes);
+  const uint32_t set = blockDim.x / lanes;
+  uint32_t sub = threadIdx.x / lanes;
+  if (B == kWaves) sub = __builtin_amdgcn_readfirstlane(sub);
+  const int wave = (threadIdx.x >> 6) - static_cast<int>(sub) * a.waves;  // of this row
+  if (B == kWaves && a.waves > 1) {
+    if (threadIdx.x < 512) reinterpret_cast<float*>(lds)[threadIdx.x] = 0.0f;
+    __syncthreads();
+  }
   const float inv = 1.0f / static_cast<float>(a.cols);
   float dg[K][kV], db[K][kV];
   Raw<WT, kV> gamma;
-  if (kAhead) gamma = load_weights<WT>(a.gamma, c.at[0], 1.0f);
+  if (kHold) gamma = load_weights<WT, kV>(a.gamma, c.at[0], 1.0f);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < kV; ++i) dg[k][i] = db[k][i] = 0.0f;
   struct Row {
-    Raw<T, kV> x[K], dy[K];
+    Raw<T, kV> dres[Dres ? K : 1], x[K], dy[K];
     float mean, rstd;
   };
-  // A set may hold rows past the end: they repeat the last row, add nothing and store nothing, so that every lane
-  // reaches the barriers.
-  auto fetch = [&](size_t base) {
+  auto fetch = [&](size_t from) {  // rows past the end: the last row
     Row r;
-    const size_t row = base + sub < a.rows ? base + sub : a.rows - 1;
+    const size_t row = from + sub < a.rows ? from + sub : a.rows - 1;
     const size_t at = row * a.cols;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      if (Dres) r.dres[k] = load_raw<T, kV, true>(a.dres + (at + c.at[k]) * T::kSize);
       r.x[k] = load_raw<T, kV, true>(a.x + (at + c.at[k]) * T::kSize);
       r.dy[k] = load_raw<T, kV, true>(a.dy + (at + c.at[k]) * T::kSize);
     }
@@ -58,95 +62,93 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
     r.rstd = a.rstd[row];
     return r;
   };
-  const size_t stride = static_cast<size_t>(gridDim.x) * kRows;
-  size_t base = static_cast<size_t>(blockIdx.x) * kRows;
-  Row next[kDepth];
-  if (kAhead)
+  // The row's two sums, and its part of the weight sums; elements before lo belong to another lane.
+  auto sums = [&](const Row& r, int k, int lo, float* c1, float* c2) {
+    float xf[kV], df[kV], gf[kV];
+    widen(r.x[k], xf);
+    widen(r.dy[k], df);
+    widen(kHold ? gamma : load_weights<WT, kV>(a.gamma, c.at[k], 1.0f), gf);
+    auto add = [&](int i) {
+      const float xh = (xf[i] - r.mean) * r.rstd;
+      const float gd = gf[i] * df[i];
+      *c1 += gd;
+      *c2 = __builtin_fmaf(gd, xh, *c2);
+      dg[k][i] = __builtin_fmaf(df[i], xh, dg[k][i]);
+      db[k][i] += df[i];
+    };
+    if (wave_full(lo)) {
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-      if (base + d * stride < a.rows) next[d] = fetch(base + d * stride);
+      for (int i = 0; i < kV; ++i) add(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+        if (i >= lo) add(i);
+    }
+  };
   int flip = 0;
-  for (; base < a.rows; base += stride) {
-    const bool mine = base + sub < a.rows;
-    const size_t at = (mine ? base + sub : a.rows - 1) * a.cols;
-    const Row r = kAhead ? next[0] : fetch(base);
-    Raw<T, kV> dres[K];
-    if (kAhead && a.dres)
+  auto row_sums = [&](const Row& r, float* c1, float* c2) {
+    float x = lanes_sum<B>(*c1), y = lanes_sum<B>(*c2);
+    if (Dres)  // has arrived before the barrier: dx may take its place, and a short last pack reads a neighbour's elements
 #pragma unroll
-      for (int k = 0; k < K; ++k) dres[k] = load_raw<T, kV, true>(a.dres + (at + c.at[k]) * T::kSize);
-    if (kAhead) {
+      for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int d = 1; d < kDepth; ++d) next[d - 1] = next[d];
-      if (base + kDepth * stride < a.rows) next[kDepth - 1] = fetch(base + kDepth * stride);
-    }
-    float c1 = 0.0f, c2 = 0.0f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int lo = mine ? c.lo[k] : kV;
-      float xf[kV], df[kV], gf[kV];
-      widen(r.x[k], xf);
-      widen(r.dy[k], df);
-      widen(kAhead ? gamma : load_weights<WT>(a.gamma, c.at[k], 1.0f), gf);
-      auto add = [&](int i) {
-        const float xh = (xf[i] - r.mean) * r.rstd;
-        const float gd = gf[i] * df[i];
-        c1 += gd;
-        c2 = __builtin_fmaf(gd, xh, c2);
-        dg[k][i] = __builtin_fmaf(df[i], xh, dg[k][i]);
-        db[k][i] += df[i];
-      };
-      if (wave_full(lo)) {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) add(i);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-          if (i >= lo) add(i);
-      }
-    }
-    if constexpr (B <= 64) {
-      c1 = lanes_sum<B>(c1);
-      c2 = lanes_sum<B>(c2);
-    } else {  // two sets of words in turn: one barrier a round
-      constexpr int kWaves = B / 64;
-      const int wave = threadIdx.x >> 6;
-      c1 = lanes_sum<64>(c1);
-      c2 = lanes_sum<64>(c2);
+        for (int i = 0; i < Raw<T, kV>::kWords; ++i) asm volatile("" ::"v"(r.dres[k].w[i]));
+    if (B == kWaves && a.waves > 1) {  // two sets of words in turn: one barrier a round
       if ((threadIdx.x & 63) == 0) {
-        lds[flip][0][wave] = c1;
-        lds[flip][1][wave] = c2;
+        lds[flip][0][sub].w[wave] = x;
+        lds[flip][1][sub].w[wave] = y;
       }
       __syncthreads();
-      c1 = c2 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) {
-        c1 += lds[flip][0][sub * kWaves + i];
-        c2 += lds[flip][1][sub * kWaves + i];
-      }
+      x = words_sum(lds[flip][0][sub], a.waves);
+      y = words_sum(lds[flip][1][sub], a.waves);
       flip ^= 1;
     }
-    c1 *= inv;
-    c2 *= inv;
-    if (!a.dx || !mine) continue;
+    *c1 = x * inv;
+    *c2 = y * inv;
+  };
+  auto store = [&](const Row& r, int k, size_t at, float c1, float c2) {
+    float xf[kV], gf[kV], df[kV], dx[kV];
+    widen(r.x[k], xf);
+    widen(r.dy[k], df);
+    widen(kHold ? gamma : load_weights<WT, kV>(a.gamma, c.at[k], 1.0f), gf);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (c.lo[k] == kV) continue;
-      float xf[kV], gf[kV], df[kV], dx[kV];
-      widen(r.x[k], xf);
-      widen(r.dy[k], df);
-      widen(kAhead ? gamma : load_weights<WT>(a.gamma, c.at[k], 1.0f), gf);
-#pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const float xh = (xf[i] - r.mean) * r.rstd;
-        dx[i] = r.rstd * (gf[i] * df[i] - __builtin_fmaf(xh, c2, c1));
-      }
-      if (a.dres) {
-        widen(kAhead ? dres[k] : load_raw<T, kV, true>(a.dres + (at + c.at[k]) * T::kSize), df);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) dx[i] += df[i];
-      }
-      store_raw<T, kV, true>(a.dx + (at + c.at[k]) * T::kSize, narrow<T, kV>(dx));
+    for (int i = 0; i < kV; ++i) {
+      const float xh = (xf[i] - r.mean) * r.rstd;
+      dx[i] = r.rstd * (gf[i] * df[i] - __builtin_fmaf(xh, c2, c1));
     }
+    if (Dres) {
+      widen(r.dres[Dres ? k : 0], df);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) dx[i] += df[i];
+    }
+    store_raw<T, kV, true>(a.dx + (at + c.at[k]) * T::kSize, narrow<T, kV>(dx));
+  };
+  const size_t stride = static_cast<size_t>(gridDim.x) * set;
+  size_t base = static_cast<size_t>(blockIdx.x) * set;
+  Row next;
+  if (kAhead) next = fetch(base);
+  for (; base + set <= a.rows; base += stride) {
+    const size_t at = (base + sub) * a.cols;
+    const Row r = kAhead ? next : fetch(base);
+    if (kAhead) next = fetch(base + stride);
+    float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) sums(r, k, c.lo[k], &c1, &c2);
+    row_sums(r, &c1, &c2);
+#pragma unroll
+    for (int k = 0; k < K; ++k) store(r, k, at, c1, c2);
+  }
+  if (base < a.rows) {  // a last set with fewer rows than the workgroup holds: the others add and store nothing
+    const bool mine = base + sub < a.rows;
+    const size_t at = (mine ? base + sub : a.rows - 1) * a.cols;
+    const Row r = fetch(base);
+    float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) sums(r, k, mine ? c.lo[k] : kV, &c1, &c2);
+    row_sums(r, &c1, &c2);
+    if (mine)
+#pragma unroll
+      for (int k = 0; k < K; ++k) store(r, k, at, c1, c2);
   }
   if (!a.part) return;
   float* out = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.cols;
@@ -157,17 +159,18 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
       float f[kV];
 #pragma unroll
       for (int i = 0; i < kV; ++i) f[i] = h ? db[k][i] : dg[k][i];
-      if constexpr (kRows > 1) {  // add the set's rows up
-        __syncthreads();
+      if (K == 1)  // add the set's rows up, the upper half's to the lower half's
+        for (uint32_t n = set; n > 1; n = (n + 1) / 2) {
+          const uint32_t half = (n + 1) / 2;
+          if (sub >= half && sub < n)
 #pragma unroll
-        for (int i = 0; i < kV; ++i) part[(sub * kV + i) * B + lane] = f[i];
-        __syncthreads();
-        if (sub == 0)
-#pragma unroll 1
-          for (int s = 1; s < kRows; ++s)
+            for (int i = 0; i < kV; ++i) part[((sub - half) * kV + i) * lanes + lane] = f[i];
+          __syncthreads();
+          if (sub < n - half)
 #pragma unroll
-            for (int i = 0; i < kV; ++i) f[i] += part[(s * kV + i) * B + lane];
-      }
+            for (int i = 0; i < kV; ++i) f[i] += part[(sub * kV + i) * lanes + lane];
+          __syncthreads();
+        }
       if (sub == 0) {
         float* o = out + h * a.cols + c.at[k];
         if (c.lo[k] == 0) {
@@ -185,7 +188,8 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
 // before it writes that pack, so dx may take the place of one of them.
 template <class T, class WT, int B>
 __global__ __launch_bounds__(B) void norm_bwd_any_dx(NormBwdArgs a) {
-  __shared__ float lds[2][B / 64];
+  __shared__ WaveWords lds[2];
+  constexpr int kV = kPack<T>;
   const float inv = 1.0f / static_cast<float>(a.cols);
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const size_t at = row * a.cols;
@@ -205,7 +209,7 @@ __global__ __launch_bounds__(B) void norm_bwd_any_dx(NormBwdArgs a) {
     };
     float c1 = 0.0f, c2 = 0.0f;
     for (size_t col = threadIdx.x * kV; col < a.cols; col += B * kV) {
-      load(col, in_row(col, a.cols));
+      load(col, in_row<kV>(col, a.cols));
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         c1 += gd[i];
@@ -213,10 +217,10 @@ __global__ __launch_bounds__(B) void norm_bwd_any_dx(NormBwdArgs a) {
       }
     }
     // a set of words for each sum: a wave may start its next row while others read this one's second sum
-    c1 = row_sum<B>(c1, lds[0]) * inv;
-    c2 = row_sum<B>(c2, lds[1]) * inv;
+    c1 = workgroup_sum<B>(c1, lds[0]) * inv;
+    c2 = workgroup_sum<B>(c2, lds[1]) * inv;
     for (size_t col = threadIdx.x * kV; col < a.cols; col += B * kV) {
-      const int cnt = in_row(col, a.cols);
+      const int cnt = in_row<kV>(col, a.cols);
       load(col, cnt);
       float dx[kV], f[kV];
 #pragma unroll
@@ -231,11 +235,12 @@ __global__ __launch_bounds__(B) void norm_bwd_any_dx(NormBwdArgs a) {
   }
 }
 
-// Rows of any length: a wave's 512 columns over the rows blockIdx.y, blockIdx.y + gridDim.y, ...
+// Rows of any length: a wave's 64 packs of columns over the rows blockIdx.y, blockIdx.y + gridDim.y, ...
 template <class T>
 __global__ __launch_bounds__(64) void norm_bwd_any_weights(NormBwdArgs a) {
+  constexpr int kV = kPack<T>;
   const size_t col = (static_cast<size_t>(blockIdx.x) * 64 + threadIdx.x) * kV;
-  const int cnt = in_row(col, a.cols);
+  const int cnt = in_row<kV>(col, a.cols);
   if (!cnt) return;
   float dg[kV], db[kV], x[kV], dy[kV];
 #pragma unroll
@@ -278,12 +283,28 @@ __global__ __launch_bounds__(1024) void norm_bwd_finish(NormBwdArgs a) {
   if (out) store1<WT>(out + (c < a.cols ? c : c - a.cols) * WT::kSize, s);
 }
 
-constexpr size_t kHeldPacks = 2048;  // longest row held in registers (two packs a lane)
-bool held(size_t cols) { return cols >= kV && (cols + kV - 1) / kV <= kHeldPacks; }
+// The shape of a row that is held in registers: lanes (B, waves) and packs a lane; K = 0 if it is not.
+struct Held {
+  int B, waves, K;
+};
+Held held(size_t cols, int kV) {
+  const size_t packs = (cols + kV - 1) / kV;
+  if (cols < static_cast<size_t>(kV) || cols > 16384) return {0, 0, 0};
+  if (packs <= 32) return {packs <= 8 ? 8 : packs <= 16 ? 16 : 32, 1, 1};
+  const int waves = static_cast<int>((packs + 63) / 64);
+  return waves <= 16 ? Held{kWaves, waves, 1} : waves <= 32 ? Held{kWaves, (waves + 1) / 2, 2} : Held{kWaves, (waves + 3) / 4, 4};
+}
+// Rows of a set, whose sums meet in LDS with one pack a lane.
+int set_of(const Held& h) { return h.K > 1 ? 1 : 1024 / (h.B == kWaves ? h.waves * 64 : h.B); }
 
 template <class T, class WT, int B, int K>
-void bwd_row(const NormBwdArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((norm_bwd_row<T, WT, B, K>), dim3(a.groups), dim3(kBwdLanes), 0, st, a);
+void bwd_row(NormBwdArgs a, const Held& h, hipStream_t st) {
+  a.waves = h.waves;
+  const dim3 grid(a.groups), block(set_of(h) * (B == kWaves ? h.waves * 64 : B));
+  if (a.dres)
+    hipLaunchKernelGGL((norm_bwd_row<T, WT, B, K, true>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((norm_bwd_row<T, WT, B, K, false>), grid, block, 0, st, a);
 }
 
 template <class T, class WT, int B>
@@ -295,24 +316,26 @@ void bwd_any(const NormBwdArgs& a, size_t packs, hipStream_t st) {
 
 template <class T, class WT>
 hipError_t bwd(const NormBwdArgs& a, hipStream_t st) {
+  constexpr int kV = kPack<T>;
   const size_t packs = (a.cols + kV - 1) / kV;
   if (a.rows) {
+    const Held h = held(a.cols, kV);
     if (a.cols < kV)
       bwd_any<T, WT, 64>(a, packs, st);
-    else if (!held(a.cols))
+    else if (h.K == 0 || !a.dx)
       bwd_any<T, WT, 1024>(a, packs, st);
-    else if (packs > 1024)
-      bwd_row<T, WT, 1024, 2>(a, st);
-    else
-      switch (norm_lanes(packs)) {
-        case 8: bwd_row<T, WT, 8, 1>(a, st); break;
-        case 32: bwd_row<T, WT, 32, 1>(a, st); break;
-        case 64: bwd_row<T, WT, 64, 1>(a, st); break;
-        case 128: bwd_row<T, WT, 128, 1>(a, st); break;
-        case 256: bwd_row<T, WT, 256, 1>(a, st); break;
-        case 512: bwd_row<T, WT, 512, 1>(a, st); break;
-        default: bwd_row<T, WT, 1024, 1>(a, st); break;
-      }
+    else if (h.B == 8)
+      bwd_row<T, WT, 8, 1>(a, h, st);
+    else if (h.B == 16)
+      bwd_row<T, WT, 16, 1>(a, h, st);
+    else if (h.B == 32)
+      bwd_row<T, WT, 32, 1>(a, h, st);
+    else if (h.K == 1)
+      bwd_row<T, WT, kWaves, 1>(a, h, st);
+    else if (h.K == 2)
+      bwd_row<T, WT, kWaves, 2>(a, h, st);
+    else if constexpr (kV == 4)
+      bwd_row<T, WT, kWaves, 4>(a, h, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -326,10 +349,9 @@ hipError_t bwd(const NormBwdArgs& a, hipStream_t st) {
 #ifndef MR_NB_GROUPS
 #define MR_NB_GROUPS 256
 #endif
-uint32_t norm_bwd_groups(size_t rows, size_t cols) {
-  const size_t packs = (cols + kV - 1) / kV;
-  const size_t set = !held(cols) ? 1 : packs > 1024 ? 1 : kBwdLanes / norm_lanes(packs);  // rows of a workgroup at a time
-  const size_t most = held(cols) ? MR_NB_GROUPS : 64;
+uint32_t norm_bwd_groups(size_t rows, size_t cols, mr_dtype dt) {
+  const Held h = held(cols, 16 / elem_size(dt));
+  const size_t set = h.K ? set_of(h) : 1, most = h.K ? MR_NB_GROUPS : 64;
   const size_t want = (rows + set - 1) / set;
   return static_cast<uint32_t>(want < most ? want : most);
 }

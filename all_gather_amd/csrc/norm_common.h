@@ -6,22 +6,29 @@
 
 namespace mr {
 
-constexpr int kV = kNormPack;
+// Elements of a pack, what a lane takes of a row at once: 16 bytes of the row's type, so that neighbouring lanes' accesses
+// adjoin (two 16-byte accesses a lane, 32 bytes apart, took an fp32 forward pass of 16384 x 2048 15% longer).
+template <class T>
+constexpr int kPack = 16 / T::kSize;
 
-// A lane's packs of a row of `cols` >= 8 elements, B lanes with K packs each.  The row's last pack, if short, is read
-// as the row's last 8 elements, of which the first `lo` belong to the neighbouring pack: every access is one whole pack,
-// and both lanes store the same bits where they overlap (predicated single elements instead took a 200003 x 509
-// fp16 backward pass 16% longer).  A pack past the row's end has lo = 8: read as that last pack, never stored.
-template <int B, int K>
+// A row lies over B lanes, K packs a lane: B = 8, 16 or 32 (a wave holds several rows), or B = kWaves: whole waves, as many as
+// the row takes, a number known at launch.
+constexpr int kWaves = 64;
+
+// A lane's packs of V elements of a row of `cols` >= V elements on `lanes` lanes.  The row's last pack, if short, is read as
+// the row's last V elements, of which the first `lo` belong to the neighbouring pack: every access is one whole pack, and both
+// lanes store the same bits where they overlap (predicated single elements instead took a 200003 x 509 fp16
+// backward pass 16% longer).  A pack past the row's end has lo = V: read as that last pack, never stored.
+template <int V, int K>
 struct RowPacks {
   uint32_t at[K];
   int lo[K];
-  __device__ RowPacks(uint32_t cols, int lane) {
+  __device__ RowPacks(uint32_t cols, int lane, int lanes) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const uint32_t col = (static_cast<uint32_t>(k) * B + lane) * kV;
-      at[k] = col < cols - kV ? col : cols - kV;
-      lo[k] = static_cast<int>(col - at[k] < kV ? col - at[k] : kV);
+      const uint32_t col = (static_cast<uint32_t>(k) * lanes + lane) * V;
+      at[k] = col < cols - V ? col : cols - V;
+      lo[k] = static_cast<int>(col - at[k] < V ? col - at[k] : V);
     }
   }
 };
@@ -30,57 +37,64 @@ struct RowPacks {
 __device__ __forceinline__ bool wave_full(int lo) { return __builtin_amdgcn_ballot_w64(lo != 0) == 0; }
 
 // A lane's pack of the weights, or `other` in its place.
-template <class WT>
-__device__ __forceinline__ Raw<WT, kV> load_weights(const char* w, uint32_t at, float other) {
-  if (w) return load_raw<WT, kV, false>(w + static_cast<size_t>(at) * WT::kSize);
-  float f[kV];
+template <class WT, int V>
+__device__ __forceinline__ Raw<WT, V> load_weights(const char* w, uint32_t at, float other) {
+  if (w) return load_raw<WT, V, false>(w + static_cast<size_t>(at) * WT::kSize);
+  float f[V];
 #pragma unroll
-  for (int i = 0; i < kV; ++i) f[i] = other;
-  return narrow<WT, kV>(f);
+  for (int i = 0; i < V; ++i) f[i] = other;
+  return narrow<WT, V>(f);
 }
 
-// Elements of a pack at `col` that lie in the row (0 .. 8).
+// Elements of a pack of V at `col` that lie in the row (0 .. V).
+template <int V>
 __device__ __forceinline__ int in_row(size_t col, size_t cols) {
-  return col >= cols ? 0 : cols - col < kV ? static_cast<int>(cols - col) : kV;
+  return col >= cols ? 0 : cols - col < V ? static_cast<int>(cols - col) : V;
 }
 
-// Sum over the B lanes of a row, in every one of them; above a wave through `lds` (a word per wave of the workgroup).
+// Words of the waves' sums, one line of 16 for each row of the workgroup; those no wave writes are zero.
+struct alignas(16) WaveWords {
+  float w[16];
+};
+__device__ __forceinline__ float words_sum(const WaveWords& l, int waves) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  const f32x4* q = reinterpret_cast<const f32x4*>(l.w);
+  f32x4 s = q[0];
+  if (waves > 4) s += q[1];
+  if (waves > 8) s += q[2] + q[3];
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// Sum over a workgroup of B lanes, in every one of them.
 template <int B>
-__device__ __forceinline__ float row_sum(float x, float* lds) {
-  if constexpr (B <= 64) {
-    return lanes_sum<B>(x);
-  } else {
-    constexpr int kWaves = B / 64;
-    const int wave = threadIdx.x >> 6;
-    x = lanes_sum<64>(x);
-    if ((threadIdx.x & 63) == 0) lds[wave] = x;
-    __syncthreads();
-    x = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) x += lds[wave / kWaves * kWaves + i];
-    return x;
-  }
+__device__ __forceinline__ float workgroup_sum(float x, WaveWords& l) {
+  x = lanes_sum<64>(x);
+  if (B == 64) return x;
+  if ((threadIdx.x & 63) == 0) l.w[threadIdx.x >> 6] = x;
+  __syncthreads();
+  return words_sum(l, B / 64);
 }
 
 // A launch holds less than 2^32 lanes; kernels loop over the rows past their grid.
 inline uint32_t norm_grid(size_t groups) { return static_cast<uint32_t>(groups < (size_t{1} << 20) ? groups : size_t{1} << 20); }
 
 // Grid of a kernel whose workgroups walk the rows: as many workgroups as the device holds at once, or `groups`.
-// (Looked up once per kernel and device.)
+// (Looked up once per kernel, device and workgroup size.)
 template <auto Kernel>
 uint32_t resident_grid(int lanes, size_t groups) {
   constexpr int kDevices = 64;
-  static std::atomic<long long> cache[kDevices];  // 0: not looked up yet
+  static std::atomic<long long> cache[kDevices][17];  // by waves of a workgroup; 0: not looked up yet
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kDevices) return norm_grid(groups);
-  long long n = cache[dev].load(std::memory_order_relaxed);
+  std::atomic<long long>& slot = cache[dev][lanes / 64];
+  long long n = slot.load(std::memory_order_relaxed);
   if (n == 0) {
     int per_cu = 0, cus = 0;
     n = -1;
     if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, Kernel, lanes, 0) == hipSuccess &&
         hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && per_cu > 0 && cus > 0)
       n = static_cast<long long>(per_cu) * cus;
-    cache[dev].store(n, std::memory_order_relaxed);
+    slot.store(n, std::memory_order_relaxed);
   }
   if (n <= 0 || groups <= static_cast<size_t>(n)) return norm_grid(groups);
   const size_t rounds = (groups + n - 1) / n;  // the same number of rounds for every workgroup, or one less

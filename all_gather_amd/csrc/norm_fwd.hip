@@ -12,82 +12,89 @@
 namespace mr {
 namespace {
 
-#ifndef MR_NF_DEPTH
-#define MR_NF_DEPTH 3
-#endif
-#ifndef MR_NF_LANES
-#define MR_NF_LANES 256
-#endif
-constexpr int kFwdLanes = MR_NF_LANES;  // lanes of a workgroup (more where a row takes more)
+constexpr int kFwdLanes = 256;  // lanes of a workgroup whose rows take a wave or less each
 
-// Row held in registers by B lanes, K packs each.  Workgroups walk rows b, b + grid, ...: gamma and beta are
-// loaded once, and with one input the next row's packs are loaded before this row's sums.
+// Row held in registers.  Workgroups walk rows b, b + grid, ...: gamma and beta are loaded once, and with one input the
+// next row's packs are loaded before this row's sums.  Loads and stores leave through one counter that a wait can only
+// count back on, so every full round issues the same ones on every path: lanes past the row's end store its last pack
+// once more, and the row's statistics collect in registers until a wave's lanes are full.  (With predicated stores a
+// round waited for the last one's stores to reach memory: 16384 x 8192 bf16 took 95 to 129 us.)
 template <class T, class WT, int B, int K, bool Sum>
-__global__ __launch_bounds__(B < kFwdLanes ? kFwdLanes : B) void norm_fwd_row(NormFwdArgs a) {
-  constexpr int kLanes = B < kFwdLanes ? kFwdLanes : B;
-  constexpr int kRows = kLanes / B;
-  __shared__ float lds[2][kLanes / 64];
-  const RowPacks<B, K> c(static_cast<uint32_t>(a.cols), threadIdx.x % B);
+__global__ __launch_bounds__(1024, K == 1 ? 8 : 4) void norm_fwd_row(NormFwdArgs a) {
+  constexpr int kV = kPack<T>;
+  constexpr bool kHold = K == 1;                 // gamma and beta stay in registers
+  constexpr bool kAhead = !Sum && K * kV <= 8;   // the next row's packs are loaded ahead
+  __shared__ WaveWords lds[2][B == kWaves ? 4 : 1];  // rows of 1 wave need none, of more at most 4 fit a workgroup
+  const int lanes = B == kWaves ? a.waves * 64 : B;
+  const int lane = threadIdx.x % lanes;
+  const RowPacks<kV, K> c(static_cast<uint32_t>(a.cols), lane, lanes);
+  const uint32_t set = blockDim.x / lanes;  // rows of the workgroup at a time
   const float inv = 1.0f / static_cast<float>(a.cols);
-  uint32_t sub = threadIdx.x / B;
-  if (B >= 64) sub = __builtin_amdgcn_readfirstlane(sub);
-  constexpr bool kHold = K == 1;                // gamma and beta stay in registers
-  constexpr bool kAhead = !Sum && K * T::kSize <= 4;
+  uint32_t sub = threadIdx.x / lanes;
+  if (B == kWaves) sub = __builtin_amdgcn_readfirstlane(sub);
+  if (B == kWaves && a.waves > 1) {
+    if (threadIdx.x < 128) lds[threadIdx.x >> 6][(threadIdx.x >> 4) & 3].w[threadIdx.x & 15] = 0.0f;
+    __syncthreads();
+  }
+  const int wave = (threadIdx.x >> 6) - static_cast<int>(sub) * a.waves;  // of this row
+  // Sum over the lanes of the row, in every one of them.  A round's two sums use words of their own, so a wave may start
+  // its next round while others end this one.
+  auto row_sum = [&](float x, WaveWords* words) {
+    x = lanes_sum<B>(x);
+    if (B == kWaves && a.waves > 1) {
+      if ((threadIdx.x & 63) == 0) words[sub].w[wave] = x;
+      __syncthreads();
+      x = words_sum(words[sub], a.waves);
+    }
+    return x;
+  };
   Raw<WT, kV> g[kHold ? K : 1], b[kHold ? K : 1];
   if (kHold) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      g[k] = load_weights<WT>(a.gamma, c.at[k], 1.0f);
-      b[k] = load_weights<WT>(a.beta, c.at[k], 0.0f);
+      g[k] = load_weights<WT, kV>(a.gamma, c.at[k], 1.0f);
+      b[k] = load_weights<WT, kV>(a.beta, c.at[k], 0.0f);
     }
   }
-  // Rows of the workgroup's last round may lie past the end: they repeat the last row and store nothing, so that every
-  // lane reaches the barriers.
-  Raw<T, kV> next[K];
-  auto fetch = [&](size_t base) {
-    const size_t row = base + sub < a.rows ? base + sub : a.rows - 1;
-#pragma unroll
-    for (int k = 0; k < K; ++k) next[k] = load_raw<T, kV, true>(a.in[0] + (row * a.cols + c.at[k]) * T::kSize);
+  const size_t stride = static_cast<size_t>(gridDim.x) * set;
+  size_t base = static_cast<size_t>(blockIdx.x) * set;
+  struct Row {
+    Raw<T, kV> x[K];
   };
-  const size_t stride = static_cast<size_t>(gridDim.x) * kRows;
-  size_t base = static_cast<size_t>(blockIdx.x) * kRows;
-  if (kAhead) fetch(base);
-  for (; base < a.rows; base += stride) {
-    const bool mine = base + sub < a.rows;
-    const size_t row = mine ? base + sub : a.rows - 1;
-    const size_t at = row * a.cols;
-    float x[K][kV];
-    if constexpr (Sum) {
-      constexpr int kDepth = K >= 4 ? 1 : MR_NF_DEPTH / K;  // inputs loaded before the first is added
-      for (int r = 0; r < a.terms; r += kDepth) {
-        Raw<T, kV> w[kDepth][K];
+  auto fetch = [&](size_t from) {  // rows past the end: the last row
+    Row r;
+    const size_t row = from + sub < a.rows ? from + sub : a.rows - 1;
 #pragma unroll
-        for (int j = 0; j < kDepth; ++j)
-          if (r + j < a.terms)
+    for (int k = 0; k < K; ++k) r.x[k] = load_raw<T, kV, true>(a.in[0] + (row * a.cols + c.at[k]) * T::kSize);
+    return r;
+  };
+  auto sum_inputs = [&](size_t at, float (&x)[K][kV]) {
+    constexpr int kTerms = K >= 4 ? 1 : 3 / K;  // inputs loaded before the first is added
+    for (int r = 0; r < a.terms; r += kTerms) {
+      Raw<T, kV> w[kTerms][K];
 #pragma unroll
-            for (int k = 0; k < K; ++k) w[j][k] = load_raw<T, kV, true>(a.in[r + j] + (at + c.at[k]) * T::kSize);
+      for (int j = 0; j < kTerms; ++j)
+        if (r + j < a.terms)
 #pragma unroll
-        for (int j = 0; j < kDepth; ++j)
-          if (r + j < a.terms)
+          for (int k = 0; k < K; ++k) w[j][k] = load_raw<T, kV, true>(a.in[r + j] + (at + c.at[k]) * T::kSize);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-              float f[kV];
-              widen(w[j][k], f);
-              if (j == 0 && r == 0) {
+      for (int j = 0; j < kTerms; ++j)
+        if (r + j < a.terms)
 #pragma unroll
-                for (int i = 0; i < kV; ++i) x[k][i] = f[i];
-              } else {
+          for (int k = 0; k < K; ++k) {
+            float f[kV];
+            widen(w[j][k], f);
+            if (j == 0 && r == 0) {
 #pragma unroll
-                for (int i = 0; i < kV; ++i) x[k][i] += f[i];
-              }
+              for (int i = 0; i < kV; ++i) x[k][i] = f[i];
+            } else {
+#pragma unroll
+              for (int i = 0; i < kV; ++i) x[k][i] += f[i];
             }
-      }
-    } else {
-      if (!kAhead) fetch(base);
-#pragma unroll
-      for (int k = 0; k < K; ++k) widen(next[k], x[k]);
-      if (kAhead && base + stride < a.rows) fetch(base + stride);
+          }
     }
+  };
+  auto stats = [&](const float (&x)[K][kV], float* mean, float* rstd) {
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -99,47 +106,98 @@ __global__ __launch_bounds__(B < kFwdLanes ? kFwdLanes : B) void norm_fwd_row(No
         for (int i = 0; i < kV; ++i) s += i >= c.lo[k] ? x[k][i] : 0.0f;
       }
     }
-    // the two rounds of row sums use LDS words of their own, so a wave may start its next row while others end this one
-    const float mean = row_sum<B>(s, lds[0]) * inv;
+    const float m = row_sum(s, lds[0]) * inv;
     s = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (wave_full(c.lo[k])) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) s = __builtin_fmaf(x[k][i] - mean, x[k][i] - mean, s);
+        for (int i = 0; i < kV; ++i) s = __builtin_fmaf(x[k][i] - m, x[k][i] - m, s);
       } else {
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-          const float d = i >= c.lo[k] ? x[k][i] - mean : 0.0f;
+          const float d = i >= c.lo[k] ? x[k][i] - m : 0.0f;
           s = __builtin_fmaf(d, d, s);
         }
       }
     }
-    const float rstd = 1.0f / __builtin_sqrtf(row_sum<B>(s, lds[1]) * inv + a.eps);
-    if (!mine) continue;
+    *mean = m;
+    *rstd = 1.0f / __builtin_sqrtf(row_sum(s, lds[1]) * inv + a.eps);
+  };
+  auto store = [&](size_t at, const float (&x)[K][kV], float mean, float rstd) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (c.lo[k] == kV) continue;
-      if (a.x_out) store_raw<T, kV, true>(a.x_out + (at + c.at[k]) * T::kSize, narrow<T, kV>(x[k]));
+      if (Sum && a.x_out) store_raw<T, kV, true>(a.x_out + (at + c.at[k]) * T::kSize, narrow<T, kV>(x[k]));
       float gf[kV], bf[kV], y[kV];
-      widen(kHold ? g[k] : load_weights<WT>(a.gamma, c.at[k], 1.0f), gf);
-      widen(kHold ? b[k] : load_weights<WT>(a.beta, c.at[k], 0.0f), bf);
+      widen(kHold ? g[k] : load_weights<WT, kV>(a.gamma, c.at[k], 1.0f), gf);
+      widen(kHold ? b[k] : load_weights<WT, kV>(a.beta, c.at[k], 0.0f), bf);
 #pragma unroll
       for (int i = 0; i < kV; ++i) y[i] = __builtin_fmaf((x[k][i] - mean) * rstd, gf[i], bf[i]);
       store_raw<T, kV, true>(a.y + (at + c.at[k]) * T::kSize, narrow<T, kV>(y));
     }
-    if (threadIdx.x % B == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
+  };
+  // Lane j keeps the statistics of round first + j until the lanes are full.
+  constexpr int kKeep = B == kWaves ? 64 : B;
+  float kept_mean = 0.0f, kept_rstd = 0.0f;
+  int kept = 0;
+  size_t first = base;
+  auto flush = [&] {
+    const size_t row = first + static_cast<size_t>(lane) * stride + sub;
+    if (lane < kept && row < a.rows) {
+      if (a.mean) a.mean[row] = kept_mean;
+      if (a.rstd) a.rstd[row] = kept_rstd;
     }
+    first += kept * stride;
+    kept = 0;
+  };
+  auto keep = [&](float mean, float rstd) {
+    if (lane % kKeep == kept) {
+      kept_mean = mean;
+      kept_rstd = rstd;
+    }
+    if (++kept == kKeep) flush();
+  };
+  Row next;
+  if (kAhead) next = fetch(base);
+  for (; base + set <= a.rows; base += stride) {
+    const size_t at = (base + sub) * a.cols;
+    float x[K][kV], mean, rstd;
+    if constexpr (Sum) {
+      sum_inputs(at, x);
+    } else {
+      const Row r = kAhead ? next : fetch(base);
+      if (kAhead) next = fetch(base + stride);
+#pragma unroll
+      for (int k = 0; k < K; ++k) widen(r.x[k], x[k]);
+    }
+    stats(x, &mean, &rstd);
+    store(at, x, mean, rstd);
+    keep(mean, rstd);
   }
+  if (base < a.rows) {  // a last set with fewer rows than the workgroup holds
+    const bool mine = base + sub < a.rows;
+    const size_t at = (mine ? base + sub : a.rows - 1) * a.cols;
+    float x[K][kV], mean, rstd;
+    if constexpr (Sum) {
+      sum_inputs(at, x);
+    } else {
+      const Row r = fetch(base);
+#pragma unroll
+      for (int k = 0; k < K; ++k) widen(r.x[k], x[k]);
+    }
+    stats(x, &mean, &rstd);
+    if (mine) store(at, x, mean, rstd);
+    keep(mean, rstd);
+  }
+  flush();
 }
 
 // Rows of any length: three sweeps over the row, the later two from the caches.  A lane reads every input
 // of a pack before it writes that pack, so outputs may replace inputs exactly.
 template <class T, class WT, int B>
 __global__ __launch_bounds__(B) void norm_fwd_any(NormFwdArgs a) {
-  __shared__ float lds[2][B / 64];
+  __shared__ WaveWords lds[2];
+  constexpr int kV = kPack<T>;
   const float inv = 1.0f / static_cast<float>(a.cols);
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const size_t at = row * a.cols;
@@ -154,14 +212,14 @@ __global__ __launch_bounds__(B) void norm_fwd_any(NormFwdArgs a) {
     };
     float s = 0.0f;
     for (size_t col = threadIdx.x * kV; col < a.cols; col += B * kV) {
-      load(col, in_row(col, a.cols));
+      load(col, in_row<kV>(col, a.cols));
 #pragma unroll
       for (int i = 0; i < kV; ++i) s += x[i];
     }
-    const float mean = row_sum<B>(s, lds[0]) * inv;
+    const float mean = workgroup_sum<B>(s, lds[0]) * inv;
     s = 0.0f;
     for (size_t col = threadIdx.x * kV; col < a.cols; col += B * kV) {
-      const int cnt = in_row(col, a.cols);
+      const int cnt = in_row<kV>(col, a.cols);
       load(col, cnt);
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
@@ -169,9 +227,9 @@ __global__ __launch_bounds__(B) void norm_fwd_any(NormFwdArgs a) {
         s = __builtin_fmaf(d, d, s);
       }
     }
-    const float rstd = 1.0f / __builtin_sqrtf(row_sum<B>(s, lds[1]) * inv + a.eps);
+    const float rstd = 1.0f / __builtin_sqrtf(workgroup_sum<B>(s, lds[1]) * inv + a.eps);
     for (size_t col = threadIdx.x * kV; col < a.cols; col += B * kV) {
-      const int cnt = in_row(col, a.cols);
+      const int cnt = in_row<kV>(col, a.cols);
       load(col, cnt);
       if (a.x_out) store_part<T, kV, true>(a.x_out + (at + col) * T::kSize, x, cnt);
       float gf[kV], bf[kV], y[kV];
@@ -190,44 +248,40 @@ __global__ __launch_bounds__(B) void norm_fwd_any(NormFwdArgs a) {
   }
 }
 
-#ifndef MR_NF_SUMALL
-#define MR_NF_SUMALL 1
-#endif
+// With several inputs every row set has a workgroup of its own: a row's loads are many, and a resident grid's last
+// round leaves units idle (2048 rows of 4096, W = 8 with a residual: 33.4 us, 34.4 on a resident grid).
 template <class T, class WT, int B, int K>
-void fwd_row(const NormFwdArgs& a, hipStream_t st) {
-  constexpr int kLanes = B < kFwdLanes ? kFwdLanes : B;
-  const size_t groups = (a.rows + kLanes / B - 1) / (kLanes / B);
-  if (a.terms > 1)
-    hipLaunchKernelGGL((norm_fwd_row<T, WT, B, K, true>), dim3(MR_NF_SUMALL ? norm_grid(groups) : resident_grid<norm_fwd_row<T, WT, B, K, true>>(kLanes, groups)),
-                       dim3(kLanes), 0, st, a);
+void fwd_row(NormFwdArgs a, int waves, hipStream_t st) {
+  a.waves = waves;
+  const int lanes = B == kWaves ? waves * 64 : B;
+  const int block = lanes < kFwdLanes ? kFwdLanes / lanes * lanes : lanes;  // up to 4 rows of a wave or more
+  const size_t groups = (a.rows + block / lanes - 1) / (block / lanes);
+  if (a.terms > 1 || a.x_out)
+    hipLaunchKernelGGL((norm_fwd_row<T, WT, B, K, true>), dim3(norm_grid(groups)), dim3(block), 0, st, a);
   else
-    hipLaunchKernelGGL((norm_fwd_row<T, WT, B, K, false>), dim3(resident_grid<norm_fwd_row<T, WT, B, K, false>>(kLanes, groups)),
-                       dim3(kLanes), 0, st, a);
+    hipLaunchKernelGGL((norm_fwd_row<T, WT, B, K, false>), dim3(resident_grid<norm_fwd_row<T, WT, B, K, false>>(block, groups)),
+                       dim3(block), 0, st, a);
 }
 
-#ifndef MR_NF_K
-#define MR_NF_K 1
-#endif
 template <class T, class WT>
 hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
+  constexpr int kV = kPack<T>;
   const size_t packs = (a.cols + kV - 1) / kV;
+  const int waves = static_cast<int>((packs + 63) / 64);  // with one pack a lane
   if (a.cols < kV)
     hipLaunchKernelGGL((norm_fwd_any<T, WT, 64>), dim3(norm_grid(a.rows)), dim3(64), 0, st, a);
-  else if (packs <= 1024)
-#define MR_LANES(B) fwd_row<T, WT, (B / MR_NF_K < 64 ? B : B / MR_NF_K), (B / MR_NF_K < 64 ? 1 : MR_NF_K)>(a, st)
-    switch (norm_lanes(packs)) {
-      case 8: MR_LANES(8); break;
-      case 32: MR_LANES(32); break;
-      case 64: MR_LANES(64); break;
-      case 128: MR_LANES(128); break;
-      case 256: MR_LANES(256); break;
-      case 512: MR_LANES(512); break;
-      default: MR_LANES(1024); break;
-    }
-  else if (packs <= 2048)
-    fwd_row<T, WT, 1024, 2>(a, st);
-  else if (packs <= 4096)
-    fwd_row<T, WT, 1024, 4>(a, st);
+  else if (packs <= 8)
+    fwd_row<T, WT, 8, 1>(a, 1, st);
+  else if (packs <= 16)
+    fwd_row<T, WT, 16, 1>(a, 1, st);
+  else if (packs <= 32)
+    fwd_row<T, WT, 32, 1>(a, 1, st);
+  else if (waves <= 16)
+    fwd_row<T, WT, kWaves, 1>(a, waves, st);
+  else if (waves <= 32)
+    fwd_row<T, WT, kWaves, 2>(a, (waves + 1) / 2, st);
+  else if (waves <= 64)
+    fwd_row<T, WT, kWaves, 4>(a, (waves + 3) / 4, st);
   else
     hipLaunchKernelGGL((norm_fwd_any<T, WT, 1024>), dim3(norm_grid(a.rows)), dim3(1024), 0, st, a);
   return hipGetLastError();

@@ -173,7 +173,7 @@ __device__ __forceinline__ void store_part(char* p, const float (&f)[N], int cnt
     if (i < cnt) store1<T>(p + i * T::kSize, f[i]);
 }
 
-// Sum over the B neighbouring lanes (8, 32 or 64) that hold a row, in every one of them, in a fixed order.  Moves within 16
+// Sum over the B neighbouring lanes (8, 16, 32 or 64) that hold a row, in every one of them, in a fixed order.  Moves within 16
 // lanes ride on the adds as DPP operands (quads by 1 and 2, then the mirrored half row and row); the four rows of a
 // wave are read into scalar registers.  A butterfly of LDS-routed shuffles took the backward pass 3% longer.
 template <int Ctrl>
@@ -182,7 +182,7 @@ __device__ __forceinline__ float dpp(float x) {
 }
 template <int B>
 __device__ __forceinline__ float lanes_sum(float x) {
-  static_assert(B == 8 || B == 32 || B == 64, "lanes of a row");
+  static_assert(B == 8 || B == 16 || B == 32 || B == 64, "lanes of a row");
   x += dpp<0xB1>(x);   // quad lanes 1 0 3 2
   x += dpp<0x4E>(x);   // quad lanes 2 3 0 1
   x += dpp<0x141>(x);  // half row mirrored

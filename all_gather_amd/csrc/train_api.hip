@@ -169,7 +169,7 @@ mr_status layer_norm_backward(const void* dy, const void* x, const void* gamma, 
   a.dbeta = static_cast<char*>(dbeta);
   a.rows = rows;
   a.cols = cols;
-  a.groups = mr::norm_bwd_groups(rows, cols);
+  a.groups = mr::norm_bwd_groups(rows, cols, dtype);
   if (dgamma || dbeta) {
     mr::Ctrl* ctrl = nullptr;
     char* data = nullptr;
