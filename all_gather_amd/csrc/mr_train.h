@@ -43,8 +43,14 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, mr_dtype dt, mr_dtype wdt, hipS
 
 // --------------------------------------------------------------------------------- gradient norm, AdamW
 constexpr int kNormTensors = 128;           // tensors per launch (their table rides in the kernel arguments)
-constexpr uint32_t kNormTileBytes = 16384;  // of one tensor
-constexpr uint32_t kNormMaxGroups = 512;    // workgroups, and so partial sums, per launch: two to a compute unit
+#ifndef MR_GN_TILE
+#define MR_GN_TILE 16384
+#endif
+#ifndef MR_GN_GROUPS
+#define MR_GN_GROUPS 512
+#endif
+constexpr uint32_t kNormTileBytes = MR_GN_TILE;  // of one tensor
+constexpr uint32_t kNormMaxGroups = MR_GN_GROUPS;    // workgroups, and so partial sums, per launch: two to a compute unit
 constexpr uint32_t kNormSets = 8;           // arrivals are counted in sets, then sets: one address takes 11.6 ns an arrival
 struct GradNormArgs {
   const char* g[kNormTensors];
@@ -82,7 +88,9 @@ struct AdamArgs {
   AdamState in, out;
   const float* clip;                        // {norm, factor, all finite} or null
   float b1, c1, b2, c2, eps, keep, lr_t, inv_sqrt_bc2;  // keep = 1 - lr*wd, lr_t = lr / (1 - b1^t)
+  float root_b2, root_c2;  // 8-bit moments: sqrt(b2), sqrt(c2) times 2^kAdamUp, and inv_sqrt_bc2 over it
 };
+constexpr int kAdamUp = 16;
 uint32_t adam_tile_elems(mr_dtype dt, mr_dtype gdt, mr_state_format fmt, bool master);
 hipError_t launch_adam(const AdamArgs& a, mr_dtype dt, mr_dtype gdt, mr_state_format fmt, hipStream_t st);
 

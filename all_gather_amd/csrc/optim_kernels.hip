@@ -111,9 +111,11 @@ __global__ __launch_bounds__(kNormLanes) void grad_norm(GradNormArgs a) {
     __hip_atomic_store(a.part + a.part_base + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     last = false;
     if (a.finish) {
-      const uint32_t set = blockIdx.x % kNormSets, sets = gridDim.x < kNormSets ? gridDim.x : kNormSets;
-      const uint32_t members = (gridDim.x - set + kNormSets - 1) / kNormSets;
-      if (__hip_atomic_fetch_add(&a.arrived[set][0], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == members - 1)
+      const uint32_t sets = gridDim.x < 4 * kNormSets ? 1 : kNormSets, set = blockIdx.x % sets;
+      const uint32_t members = (gridDim.x - set + sets - 1) / sets;
+      if (sets == 1)
+        last = __hip_atomic_fetch_add(&a.arrived[0][0], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == members - 1;
+      else if (__hip_atomic_fetch_add(&a.arrived[set][0], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == members - 1)
         last = __hip_atomic_fetch_add(&a.arrived[kNormSets][0], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == sets - 1;
     }
   }
@@ -143,38 +145,69 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
   return __uint_as_float(byte == 255 ? 0x7fc00000u : b);
 }
 
-// Scale byte of a block whose largest magnitude has the fp32 bits `top`: the smallest power of two that brings
-// it to 448, E4M3's largest, or less; 255 if it is infinite or NaN (as an integer NaN is the largest of all).
+// Scale byte of a block whose largest magnitude, times 2^Up, has the fp32 bits `top`: the smallest power of two that
+// brings it to 448, E4M3's largest, or less; 255 if it is infinite or NaN (as an integer NaN is the largest of all).
+template <int Up>
 __device__ __forceinline__ uint32_t mx_byte(uint32_t top) {
-  const int b = static_cast<int>((top + 0x1fffffu) >> 23) - 8;  // mantissas above 1.75 carry into the exponent
+  const int b = static_cast<int>((top + 0x1fffffu) >> 23) - 8 - Up;  // mantissas above 1.75 carry into the exponent
   return top >= 0x7f800000u ? 255u : static_cast<uint32_t>(b < 0 ? 0 : b);
 }
 
-// Largest of the four lanes of a quad, in each of them.
-__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
-  const uint32_t y = __builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xf, 0xf, true);  // lanes 1 0 3 2
-  x = x > y ? x : y;
-  const uint32_t z = __builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xf, 0xf, true);  // lanes 2 3 0 1
-  return x > z ? x : z;
+// Largest of the lanes that hold a block, E elements each, in every one of them.
+template <int E>
+__device__ __forceinline__ uint32_t block_max(uint32_t x) {
+  const auto with = [&](int y) { x = x > static_cast<uint32_t>(y) ? x : static_cast<uint32_t>(y); };
+  with(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xf, 0xf, true));   // quad lanes 1 0 3 2
+  with(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xf, 0xf, true));   // quad lanes 2 3 0 1
+  if (E == 4) with(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x141, 0xf, 0xf, true));  // half row mirrored
+  return x;
 }
 
-// 32 random bits of element idx of the flat state: a Weyl step on the key of (seed, step) and one
-// multiply-xorshift round.
-__device__ __forceinline__ uint32_t random_bits(uint32_t key, uint64_t idx) {
-  uint32_t x = key + static_cast<uint32_t>(idx) * 0x9E3779B1u + static_cast<uint32_t>(idx >> 32) * 0x85EBCA77u;
-  x ^= x >> 16;
-  x *= 0x7FEB352Du;
-  return x ^ (x >> 15);
-}
-
-// Eight codes at c (8 bytes, aligned) times the block's scale.
-__device__ __forceinline__ void mx_load(const char* c, uint32_t byte, float (&f)[8]) {
-  const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(c));
-  const float s = mx_scale(byte);
+// 32 random bits for each of the elements idx .. idx + E - 1 of the flat state (idx a multiple of E): a Weyl step on the
+// key of (seed, step) and one multiply-xorshift round.
+template <int E>
+__device__ __forceinline__ void random_bits(uint32_t key, uint64_t idx, uint32_t (&r)[E]) {
+  const uint32_t first = key + static_cast<uint32_t>(idx) * 0x9E3779B1u + static_cast<uint32_t>(idx >> 32) * 0x85EBCA77u;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[i]), false);
-    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[i]), true);
+  for (int j = 0; j < E; ++j) {
+    uint32_t x = first + static_cast<uint32_t>(j) * 0x9E3779B1u;
+    x ^= x >> 16;
+    x *= 0x7FEB352Du;
+    r[j] = x ^ (x >> 15);
+  }
+}
+
+// The codes of E neighbouring elements (aligned).
+template <int E>
+struct Codes {
+  uint32_t w[E / 4];
+};
+template <int E>
+__device__ __forceinline__ Codes<E> load_codes(const char* p) {
+  Codes<E> c;
+  if constexpr (E == 8) {
+    const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+    c.w[0] = v[0];
+    c.w[1] = v[1];
+  } else {
+    c.w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+  }
+  return c;
+}
+template <int E>
+__device__ __forceinline__ void store_codes(char* p, const Codes<E>& c) {
+  if constexpr (E == 8)
+    __builtin_nontemporal_store(u32x2{c.w[0], c.w[1]}, reinterpret_cast<u32x2*>(p));
+  else
+    __builtin_nontemporal_store(c.w[0], reinterpret_cast<uint32_t*>(p));
+}
+// The codes' values times s.
+template <int E>
+__device__ __forceinline__ void mx_decode(const Codes<E>& c, float s, float (&f)[E]) {
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) {
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.w[i]), false);
+    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.w[i]), true);
     f[4 * i] = lo[0] * s;
     f[4 * i + 1] = lo[1] * s;
     f[4 * i + 2] = hi[0] * s;
@@ -182,39 +215,40 @@ __device__ __forceinline__ void mx_load(const char* c, uint32_t byte, float (&f)
   }
 }
 
-// This lane's eight of the block's 32 values (four neighbouring lanes hold a block) as codes; the block's byte.
+// This lane's E of the block's 32 values (neighbouring lanes hold a block) as codes; the block's byte.
 // v_cvt_sr_fp8_f32 adds the random word's upper 20 bits below the third mantissa bit (below 2^-6, the smallest
 // normal number, below the 2^-9 place) and drops what lies there: up with probability (distance to the lower
 // neighbour) / (spacing).  It takes 16 of them here, from the lower half of r, or for `Second` from the upper half.  Second
 // moments are raised to the smallest code, 2^-9, unless they are zero.
-template <bool Second>
-__device__ __forceinline__ u32x2 mx_encode(const float (&f)[8], const uint32_t (&r)[8], uint32_t* byte) {
+// f holds the values times 2^Up.
+template <bool Second, int Up, int E>
+__device__ __forceinline__ Codes<E> mx_encode(const float (&f)[E], const uint32_t (&r)[E], uint32_t* byte) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __float_as_uint(f[i]) & 0x7fffffffu;
+  for (int i = 0; i < E; ++i) {
+    const uint32_t b = Second ? __float_as_uint(f[i]) : __float_as_uint(f[i]) & 0x7fffffffu;  // roots have no sign
     top = top > b ? top : b;
   }
-  const uint32_t e = mx_byte(quad_max(top));
+  const uint32_t e = mx_byte<Up>(block_max<E>(top));
   *byte = e;
-  const float inv = __uint_as_float((254u - (e < 253u ? e : 253u)) << 23);
-  u32x2 w;
+  const float inv = __uint_as_float((254u - Up - (e < 253u - Up ? e : 253u - Up)) << 23);
+  Codes<E> c;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < E / 4; ++i) {
     int x = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float y = f[4 * i + j] * inv;
-      if (Second) y = y > 0.0f ? __builtin_fmaxf(y, 0.001953125f) : 0.0f;
+      if (Second) y = __builtin_amdgcn_fmed3f(y, 0.001953125f, y * 1.2676506002282294e30f);  // 2^-9; y * 2^100
       const uint32_t bits = Second ? r[4 * i + j] & 0xffff0000u : r[4 * i + j] << 16;
       x = j == 0   ? __builtin_amdgcn_cvt_sr_fp8_f32(y, bits, x, 0)
           : j == 1 ? __builtin_amdgcn_cvt_sr_fp8_f32(y, bits, x, 1)
           : j == 2 ? __builtin_amdgcn_cvt_sr_fp8_f32(y, bits, x, 2)
                    : __builtin_amdgcn_cvt_sr_fp8_f32(y, bits, x, 3);
     }
-    w[i] = e == 255u ? 0u : static_cast<uint32_t>(x);
+    c.w[i] = e == 255u ? 0u : static_cast<uint32_t>(x);
   }
-  return w;
+  return c;
 }
 
 // ------------------------------------------------------------------------------------------------- AdamW
@@ -223,19 +257,19 @@ constexpr int kLanes = 256;
 
 // sqrt and quotient from the hardware's square root and reciprocal, each within 1 ulp (the correctly rounded ones take
 // three times the operations, and the 8-bit step is bound by its operations).  v_sqrt_f32 flushes subnormals, so
-// small arguments are scaled by 2^64.  The divisor is never subnormal: it is at least eps, or the root of an fp32 number.
+// small arguments are scaled by 2^64; the 8-bit step, which never holds v itself, carries the root times 2^16 all through
+// instead (v is then normal for every root above 2^-79, and finite for gradients below 2^47).  The divisor is never
+// subnormal: it is at least eps, or the root of an fp32 number.
 __device__ __forceinline__ float root(float v) {
   const bool small = v < 7.8886090522101181e-31f;  // 2^-100
   const float r = __builtin_amdgcn_sqrtf(v * (small ? 18446744073709551616.0f : 1.0f));
   return r * (small ? 2.3283064365386963e-10f : 1.0f);
 }
 
-// Elements a lane takes at once: 8 where the moments are bytes (8 codes are 8 bytes, four lanes a block), 4
-// where they are fp32 (one 16-byte access each).
-template <bool Mx>
-constexpr int kLaneElems = Mx ? 8 : 4;
-template <bool Mx>
-constexpr uint32_t kTileElems = kLanes * kLaneElems<Mx>;
+// Elements a lane takes at once: 4 where some stream is fp32 (one 16-byte access each), 8 where the moments are bytes and
+// the rest 16-bit.
+template <class T, class G, bool Mx, bool Master>
+constexpr int kLaneElems = Mx && !Master && T::kSize == 2 && G::kSize == 2 ? 8 : 4;
 
 // The step is not taken (clip says that a gradient is not finite): outputs that are not the inputs get copies.
 template <class T, bool Mx, bool Master, int E>
@@ -256,8 +290,8 @@ __device__ __forceinline__ void keep_tile(const AdamArgs& a, uint32_t i, uint64_
   if (!live) return;
   if constexpr (Mx) {
     const uint64_t blk = idx / kMxBlock;
-    if (a.out.m != a.in.m) *reinterpret_cast<u32x2*>(a.out.m + idx) = *reinterpret_cast<const u32x2*>(a.in.m + idx);
-    if (a.out.v != a.in.v) *reinterpret_cast<u32x2*>(a.out.v + idx) = *reinterpret_cast<const u32x2*>(a.in.v + idx);
+    if (a.out.m != a.in.m) store_codes<E>(a.out.m + idx, load_codes<E>(a.in.m + idx));
+    if (a.out.v != a.in.v) store_codes<E>(a.out.v + idx, load_codes<E>(a.in.v + idx));
     if (a.out.ms != a.in.ms) a.out.ms[blk] = a.in.ms[blk];
     if (a.out.vs != a.in.vs) a.out.vs[blk] = a.in.vs[blk];
   } else {
@@ -266,12 +300,21 @@ __device__ __forceinline__ void keep_tile(const AdamArgs& a, uint32_t i, uint64_
   }
 }
 
+// The tile of workgroup b of n.  Workgroups are dealt to the eight XCDs in turn; runs of 128 tiles that follow one
+// another go to one XCD, so each streams long stretches of every buffer (28M elements, 8-bit moments: 52.5 us in plain
+// order, 50.1 in runs of 16 to 128; 130M fp32: 640, 596 to 622).
+__device__ __forceinline__ uint32_t tile_of(uint32_t b, uint32_t n) {
+  constexpr uint32_t kRun = 128, kDeal = 8 * kRun;
+  return b < n / kDeal * kDeal ? b / kDeal * kDeal + b % 8 * kRun + b % kDeal / 8 : b;
+}
+
 // One tile per workgroup.  Every byte is touched once; loads and stores are non-temporal.
 template <class T, class G, bool Mx, bool Master>
 __global__ __launch_bounds__(kLanes) void adamw(AdamArgs a) {
-  constexpr int E = kLaneElems<Mx>;
-  const uint32_t i = TensorTable<kAdamTensors>(a.tile_prefix, a.P).find(blockIdx.x);
-  const uint64_t e = static_cast<uint64_t>(blockIdx.x - a.tile_prefix[i]) * kTileElems<Mx> + threadIdx.x * E;
+  constexpr int E = kLaneElems<T, G, Mx, Master>;
+  const uint32_t tile = tile_of(blockIdx.x, gridDim.x);
+  const uint32_t i = TensorTable<kAdamTensors>(a.tile_prefix, a.P).find(tile);
+  const uint64_t e = static_cast<uint64_t>(tile - a.tile_prefix[i]) * (kLanes * E) + threadIdx.x * E;
   const uint64_t n = a.n[i];
   const int cnt = e >= n ? 0 : n - e < E ? static_cast<int>(n - e) : E;
   const bool live = e < ((n + (kMxBlock - 1)) & ~uint64_t{kMxBlock - 1});  // in a block of the tensor's state
@@ -284,7 +327,7 @@ __global__ __launch_bounds__(kLanes) void adamw(AdamArgs a) {
       return;
     }
   }
-  float p[E], g[E], m[E], v[E], r[E];
+  float p[E], g[E], m[E], v[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) p[j] = m[j] = v[j] = 0.0f;
   if (live) {
@@ -293,41 +336,50 @@ __global__ __launch_bounds__(kLanes) void adamw(AdamArgs a) {
     else
       widen(load_part<T, E, true>(a.p[i] + e * T::kSize, cnt), p);
     if constexpr (Mx) {
-      mx_load(a.in.m + idx, a.in.ms[idx / kMxBlock], m);
-      mx_load(a.in.v + idx, a.in.vs[idx / kMxBlock], v);
-#pragma unroll
-      for (int j = 0; j < E; ++j) v[j] *= v[j];
+      mx_decode(load_codes<E>(a.in.m + idx), mx_scale(a.in.ms[idx / kMxBlock]) * a.b1, m);
+      mx_decode(load_codes<E>(a.in.v + idx), mx_scale(a.in.vs[idx / kMxBlock]) * a.root_b2, v);
     } else {
       widen(load_raw<EFp32, E, true>(a.in.m + 4 * idx), m);
       widen(load_raw<EFp32, E, true>(a.in.v + 4 * idx), v);
     }
   }
   widen(load_part<G, E, true>(a.g[i] + e * G::kSize, cnt), g);
+  if constexpr (Mx) {
+    // The decays ride on the blocks' scales: m holds b1*m, v holds sqrt(b2) times the stored root times 2^kUp.
+    const float gm = factor * a.c1, gv = factor * a.root_c2;
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const float gj = g[j] * factor;
-    m[j] = m[j] * a.b1 + gj * a.c1;
-    v[j] = v[j] * a.b2 + gj * gj * a.c2;
-    r[j] = root(v[j]);
-    const float u = m[j] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[j], a.inv_sqrt_bc2, a.eps));
-    p[j] = p[j] * a.keep - u * a.lr_t;
+    for (int j = 0; j < E; ++j) {
+      m[j] = __builtin_fmaf(g[j], gm, m[j]);
+      const float x = g[j] * gv;
+      v[j] = __builtin_amdgcn_sqrtf(__builtin_fmaf(x, x, v[j] * v[j]));
+      const float u = m[j] * __builtin_amdgcn_rcpf(__builtin_fmaf(v[j], a.inv_sqrt_bc2, a.eps));
+      p[j] = __builtin_fmaf(-u, a.lr_t, p[j] * a.keep);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const float gj = g[j] * factor;
+      m[j] = m[j] * a.b1 + gj * a.c1;
+      v[j] = v[j] * a.b2 + gj * gj * a.c2;
+      const float u = m[j] * __builtin_amdgcn_rcpf(__builtin_fmaf(root(v[j]), a.inv_sqrt_bc2, a.eps));
+      p[j] = p[j] * a.keep - u * a.lr_t;
+    }
   }
   if (cnt < E) {  // elements between tensors are kept at zero
 #pragma unroll
     for (int j = 0; j < E; ++j)
-      if (j >= cnt) p[j] = m[j] = v[j] = r[j] = 0.0f;
+      if (j >= cnt) p[j] = m[j] = v[j] = 0.0f;
   }
   if (cnt) store_part<T, E, true>(a.po[i] + e * T::kSize, p, cnt);
   if constexpr (Mx) {  // all lanes: the block's scale is the largest of four lanes' values
     uint32_t bits[E], mb, vb;
-#pragma unroll
-    for (int j = 0; j < E; ++j) bits[j] = random_bits(a.key, idx + j);
-    const u32x2 mw = mx_encode<false>(m, bits, &mb);
-    const u32x2 vw = mx_encode<true>(r, bits, &vb);
+    random_bits(a.key, idx, bits);
+    const Codes<E> mw = mx_encode<false, 0>(m, bits, &mb);
+    const Codes<E> vw = mx_encode<true, kAdamUp>(v, bits, &vb);
     if (live) {
-      __builtin_nontemporal_store(mw, reinterpret_cast<u32x2*>(a.out.m + idx));
-      __builtin_nontemporal_store(vw, reinterpret_cast<u32x2*>(a.out.v + idx));
-      if ((threadIdx.x & 3) == 0) {
+      store_codes<E>(a.out.m + idx, mw);
+      store_codes<E>(a.out.v + idx, vw);
+      if (threadIdx.x % (kMxBlock / E) == 0) {
         a.out.ms[idx / kMxBlock] = static_cast<uint8_t>(mb);
         a.out.vs[idx / kMxBlock] = static_cast<uint8_t>(vb);
       }
@@ -372,8 +424,9 @@ hipError_t launch_grad_norm(const GradNormArgs& a, mr_dtype dt, hipStream_t st) 
   return hipGetLastError();
 }
 
-uint32_t adam_tile_elems(mr_dtype, mr_dtype, mr_state_format fmt, bool) {
-  return fmt == MR_STATE_MXFP8 ? kTileElems<true> : kTileElems<false>;
+uint32_t adam_tile_elems(mr_dtype dt, mr_dtype gdt, mr_state_format fmt, bool master) {
+  return kLanes * (fmt == MR_STATE_MXFP8 && !master && dt != MR_FP32 && gdt != MR_FP32 ? kLaneElems<EBf16, EBf16, true, false>
+                                                                                       : kLaneElems<EFp32, EFp32, false, false>);
 }
 
 hipError_t launch_adam(const AdamArgs& a, mr_dtype dt, mr_dtype gdt, mr_state_format fmt, hipStream_t st) {
