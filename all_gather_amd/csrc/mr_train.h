@@ -43,14 +43,8 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, mr_dtype dt, mr_dtype wdt, hipS
 
 // --------------------------------------------------------------------------------- gradient norm, AdamW
 constexpr int kNormTensors = 128;           // tensors per launch (their table rides in the kernel arguments)
-#ifndef MR_GN_TILE
-#define MR_GN_TILE 16384
-#endif
-#ifndef MR_GN_GROUPS
-#define MR_GN_GROUPS 512
-#endif
-constexpr uint32_t kNormTileBytes = MR_GN_TILE;  // of one tensor
-constexpr uint32_t kNormMaxGroups = MR_GN_GROUPS;    // workgroups, and so partial sums, per launch: two to a compute unit
+constexpr uint32_t kNormTileBytes = 16384;  // of one tensor
+constexpr uint32_t kNormMaxGroups = 512;    // workgroups, and so partial sums, per launch: two to a compute unit
 constexpr uint32_t kNormSets = 8;           // arrivals are counted in sets, then sets: one address takes 11.6 ns an arrival
 struct GradNormArgs {
   const char* g[kNormTensors];

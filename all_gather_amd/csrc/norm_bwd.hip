@@ -124,7 +124,8 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
     store_raw<T, kV, true>(a.dx + (at + c.at[k]) * T::kSize, narrow<T, kV>(dx));
   };
   const size_t stride = static_cast<size_t>(gridDim.x) * set;
-  size_t base = static_cast<size_t>(blockIdx.x) * set;
+  const uint32_t group = group_of(blockIdx.x, gridDim.x);
+  size_t base = static_cast<size_t>(group) * set;
   Row next;
   if (kAhead) next = fetch(base);
   for (; base + set <= a.rows; base += stride) {
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
       for (int k = 0; k < K; ++k) store(r, k, at, c1, c2);
   }
   if (!a.part) return;
-  float* out = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.cols;
+  float* out = a.part + static_cast<size_t>(group) * 2 * a.cols;
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll

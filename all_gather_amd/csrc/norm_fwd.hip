@@ -12,9 +12,6 @@
 namespace mr {
 namespace {
 
-#ifndef MR_NF_AV
-#define MR_NF_AV 8
-#endif
 constexpr int kFwdLanes = 256;  // lanes of a workgroup whose rows take a wave or less each
 
 // Row held in registers.  Workgroups walk rows b, b + grid, ...: gamma and beta are loaded once, and with one input the
@@ -26,7 +23,7 @@ template <class T, class WT, int B, int K, bool Sum>
 __global__ __launch_bounds__(1024, K == 1 ? 8 : 4) void norm_fwd_row(NormFwdArgs a) {
   constexpr int kV = kPack<T>;
   constexpr bool kHold = K == 1;                 // gamma and beta stay in registers
-  constexpr bool kAhead = !Sum && K * kV <= MR_NF_AV;   // the next row's packs are loaded ahead
+  constexpr bool kAhead = !Sum && K * kV <= 16;   // the next row's packs are loaded ahead
   __shared__ WaveWords lds[2][B == kWaves ? 4 : 1];  // rows of 1 wave need none, of more at most 4 fit a workgroup
   const int lanes = B == kWaves ? a.waves * 64 : B;
   const int lane = threadIdx.x % lanes;
@@ -60,7 +57,7 @@ __global__ __launch_bounds__(1024, K == 1 ? 8 : 4) void norm_fwd_row(NormFwdArgs
     }
   }
   const size_t stride = static_cast<size_t>(gridDim.x) * set;
-  size_t base = static_cast<size_t>(blockIdx.x) * set;
+  size_t base = static_cast<size_t>(group_of(blockIdx.x, gridDim.x)) * set;
   struct Row {
     Raw<T, kV> x[K];
   };
