@@ -363,23 +363,33 @@ def _weights_dtype(ref, *weights):
     return ref.dtype if wdt is None else wdt
 
 
+_ptr_arrays: dict = {}
+
+
 def _ptr_array(ptrs):
-    return (ctypes.c_void_p * max(len(ptrs), 1))(*ptrs)
+    n = len(ptrs) or 1
+    t = _ptr_arrays.get(n)
+    if t is None:
+        t = _ptr_arrays[n] = ctypes.c_void_p * n
+    return t(*ptrs)
+
+
+def _layer_norm_forward_args(bufs, gamma, beta, y, eps, residual, x_out, mean, rstd, stream):
+    _dev_tensor(y, "y")
+    n, cols = y.numel(), y.shape[-1] if y.dim() else 1
+    rows, f32 = n // cols if cols else 0, (_torch().float32,)
+    same, wdt = (y.dtype,), _weights_dtype(y, gamma, beta)
+    dt = DTYPE_CODE[dtype_name(y)]
+    return (_ptr_array([_opt(b, "rank buffer", same, n) for b in bufs]), len(bufs), _opt(residual, "residual", same, n),
+            _opt(gamma, "gamma", (wdt,), cols), _opt(beta, "beta", (wdt,), cols), rows, cols, dt,
+            dt if wdt == y.dtype else DTYPE_CODE["fp32"], eps, _opt(x_out, "x_out", same, n), y.data_ptr(),
+            _opt(mean, "mean", f32, rows), _opt(rstd, "rstd", f32, rows), _stream_handle(stream))
 
 
 def prepare_layer_norm_forward(bufs: Sequence, gamma, beta, y, eps: float = 1e-5, residual=None, x_out=None, mean=None,
                                rstd=None, stream=None):
     """Pre-marshalled mr_layer_norm_forward over the last dimension of ``y``."""
-    _dev_tensor(y, "y")
-    n, cols = y.numel(), y.shape[-1] if y.dim() else 1
-    rows, f32 = n // cols if cols else 0, (_torch().float32,)
-    same, wdt = (y.dtype,), _weights_dtype(y, gamma, beta)
-    ptrs = _ptr_array([_opt(b, "rank buffer", same, n) for b in bufs])
-    dt = DTYPE_CODE[dtype_name(y)]
-    args = (ptrs, len(bufs), _opt(residual, "residual", same, n), _opt(gamma, "gamma", (wdt,), cols),
-            _opt(beta, "beta", (wdt,), cols), rows, cols, dt, dt if wdt == y.dtype else DTYPE_CODE["fp32"], eps,
-            _opt(x_out, "x_out", same, n), y.data_ptr(), _opt(mean, "mean", f32, rows), _opt(rstd, "rstd", f32, rows),
-            _stream_handle(stream))
+    args = _layer_norm_forward_args(bufs, gamma, beta, y, eps, residual, x_out, mean, rstd, stream)
     return _prepared("mr_layer_norm_forward", lib().mr_layer_norm_forward, args,
                      (list(bufs), gamma, beta, y, residual, x_out, mean, rstd))
 
@@ -391,12 +401,12 @@ def layer_norm_forward(bufs: Sequence, gamma, beta, y, eps: float = 1e-5, residu
     ``bufs`` with one tensor and no residual is a plain layer norm; with W tensors it is what follows a
     tensor-parallel all-reduce.  ``gamma`` / ``beta`` may be None (ones / zeros).  ``x_out`` receives x (the residual
     stream, and the backward pass's input); ``mean`` and ``rstd`` (fp32, one per row) the statistics."""
-    prepare_layer_norm_forward(bufs, gamma, beta, y, eps, residual, x_out, mean, rstd, stream)()
+    _check(lib().mr_layer_norm_forward(*_layer_norm_forward_args(bufs, gamma, beta, y, eps, residual, x_out, mean, rstd, stream)),
+           "mr_layer_norm_forward")
     return y
 
 
-def prepare_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None, stream=None):
-    """Pre-marshalled mr_layer_norm_backward."""
+def _layer_norm_backward_args(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres, stream):
     _dev_tensor(dy, "dy")
     n, cols = dy.numel(), dy.shape[-1] if dy.dim() else 1
     rows, f32 = n // cols if cols else 0, (_torch().float32,)
@@ -404,10 +414,15 @@ def prepare_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta
     if x is None or mean is None or rstd is None:
         raise ValueError("x, mean and rstd are needed")
     dt = DTYPE_CODE[dtype_name(dy)]
-    args = (dy.data_ptr(), _opt(x, "x", same, n), _opt(gamma, "gamma", (wdt,), cols), _opt(mean, "mean", f32, rows),
+    return (dy.data_ptr(), _opt(x, "x", same, n), _opt(gamma, "gamma", (wdt,), cols), _opt(mean, "mean", f32, rows),
             _opt(rstd, "rstd", f32, rows), _opt(dres, "dres", same, n), rows, cols, dt,
             dt if wdt == dy.dtype else DTYPE_CODE["fp32"], _opt(dx, "dx", same, n), _opt(dgamma, "dgamma", (wdt,), cols),
             _opt(dbeta, "dbeta", (wdt,), cols), _stream_handle(stream))
+
+
+def prepare_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None, stream=None):
+    """Pre-marshalled mr_layer_norm_backward."""
+    args = _layer_norm_backward_args(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres, stream)
     return _prepared("mr_layer_norm_backward", lib().mr_layer_norm_backward, args,
                      (dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres))
 
@@ -415,7 +430,8 @@ def prepare_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta
 def layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None, stream=None):
     """Gradients of layer_norm_forward: ``dx`` (of every rank buffer and the residual alike; plus ``dres``, the gradient
     that reaches x beside the norm), ``dgamma`` and ``dbeta`` (sums over the rows).  Any of the three may be None."""
-    prepare_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres, stream)()
+    _check(lib().mr_layer_norm_backward(*_layer_norm_backward_args(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres, stream)),
+           "mr_layer_norm_backward")
     return dx
 
 

@@ -13,16 +13,17 @@
 namespace mr {
 namespace {
 
-constexpr int kBwdLanes = 1024;  // most lanes of a workgroup
+constexpr int kBwdLanes = 1024;  // most lanes of a workgroup; with 768 a lane has 168 registers, not 128
 
 // Workgroup b of `groups` takes row sets b, b + groups, ...; a set is as many rows as the workgroup holds.  The next set's
 // x and dy are loaded before this set's sums where registers allow; as in the forward pass every full round issues the same
 // loads and stores on every path.
-template <class T, class WT, int B, int K, bool Dres>
-__global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
+template <class T, class WT, int B, int K, bool Dres, int Lanes>
+__global__ __launch_bounds__(Lanes) void norm_bwd_row(NormBwdArgs a) {
   constexpr int kV = kPack<T>;
-  constexpr bool kAhead = K * kV <= 8;
-  constexpr bool kHold = K == 1;  // gamma stays in registers
+  constexpr bool kAhead = K * kV <= 8 || (Lanes < 1024 && (T::kSize == 2 || !Dres));
+  // gamma stays in registers (its loads would otherwise wait for the next set's, issued before them)
+  constexpr bool kHold = kAhead;
   __shared__ WaveWords lds[2][2][B == kWaves ? 8 : 1];  // rows of several waves: at most 8 fit a workgroup
   __shared__ float part[K == 1 ? kBwdLanes / 2 * kV : 1];
   const int lanes = B == kWaves ? a.waves * 64 : B;
@@ -38,8 +39,10 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
   }
   const float inv = 1.0f / static_cast<float>(a.cols);
   float dg[K][kV], db[K][kV];
-  Raw<WT, kV> gamma;
-  if (kHold) gamma = load_weights<WT, kV>(a.gamma, c.at[0], 1.0f);
+  Raw<WT, kV> gamma[kHold ? K : 1];
+  if (kHold)
+#pragma unroll
+    for (int k = 0; k < K; ++k) gamma[k] = load_weights<WT, kV>(a.gamma, c.at[k], 1.0f);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -67,7 +70,7 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
     float xf[kV], df[kV], gf[kV];
     widen(r.x[k], xf);
     widen(r.dy[k], df);
-    widen(kHold ? gamma : load_weights<WT, kV>(a.gamma, c.at[k], 1.0f), gf);
+    widen(kHold ? gamma[kHold ? k : 0] : load_weights<WT, kV>(a.gamma, c.at[k], 1.0f), gf);
     auto add = [&](int i) {
       const float xh = (xf[i] - r.mean) * r.rstd;
       const float gd = gf[i] * df[i];
@@ -110,7 +113,7 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
     float xf[kV], gf[kV], df[kV], dx[kV];
     widen(r.x[k], xf);
     widen(r.dy[k], df);
-    widen(kHold ? gamma : load_weights<WT, kV>(a.gamma, c.at[k], 1.0f), gf);
+    widen(kHold ? gamma[kHold ? k : 0] : load_weights<WT, kV>(a.gamma, c.at[k], 1.0f), gf);
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       const float xh = (xf[i] - r.mean) * r.rstd;
@@ -124,8 +127,7 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
     store_raw<T, kV, true>(a.dx + (at + c.at[k]) * T::kSize, narrow<T, kV>(dx));
   };
   const size_t stride = static_cast<size_t>(gridDim.x) * set;
-  const uint32_t group = group_of(blockIdx.x, gridDim.x);
-  size_t base = static_cast<size_t>(group) * set;
+  size_t base = static_cast<size_t>(blockIdx.x) * set;
   Row next;
   if (kAhead) next = fetch(base);
   for (; base + set <= a.rows; base += stride) {
@@ -152,7 +154,7 @@ __global__ __launch_bounds__(kBwdLanes) void norm_bwd_row(NormBwdArgs a) {
       for (int k = 0; k < K; ++k) store(r, k, at, c1, c2);
   }
   if (!a.part) return;
-  float* out = a.part + static_cast<size_t>(group) * 2 * a.cols;
+  float* out = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.cols;
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -302,10 +304,18 @@ template <class T, class WT, int B, int K>
 void bwd_row(NormBwdArgs a, const Held& h, hipStream_t st) {
   a.waves = h.waves;
   const dim3 grid(a.groups), block(set_of(h) * (B == kWaves ? h.waves * 64 : B));
-  if (a.dres)
-    hipLaunchKernelGGL((norm_bwd_row<T, WT, B, K, true>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((norm_bwd_row<T, WT, B, K, false>), grid, block, 0, st, a);
+  if (K > 1 && block.x <= 768) {
+    if constexpr (K > 1) {
+      if (a.dres)
+        hipLaunchKernelGGL((norm_bwd_row<T, WT, B, K, true, 768>), grid, block, 0, st, a);
+      else
+        hipLaunchKernelGGL((norm_bwd_row<T, WT, B, K, false, 768>), grid, block, 0, st, a);
+    }
+  } else if (a.dres) {
+    hipLaunchKernelGGL((norm_bwd_row<T, WT, B, K, true, 1024>), grid, block, 0, st, a);
+  } else {
+    hipLaunchKernelGGL((norm_bwd_row<T, WT, B, K, false, 1024>), grid, block, 0, st, a);
+  }
 }
 
 template <class T, class WT, int B>

@@ -75,14 +75,6 @@ __device__ __forceinline__ float workgroup_sum(float x, WaveWords& l) {
   return words_sum(l, B / 64);
 }
 
-#ifndef MR_N_RUN
-#define MR_N_RUN 1
-#endif
-__device__ __forceinline__ uint32_t group_of(uint32_t b, uint32_t n) {
-  constexpr uint32_t kRun = MR_N_RUN, kDeal = 8 * kRun;
-  return b < n / kDeal * kDeal ? b / kDeal * kDeal + b % 8 * kRun + b % kDeal / 8 : b;
-}
-
 // A launch holds less than 2^32 lanes; kernels loop over the rows past their grid.
 inline uint32_t norm_grid(size_t groups) { return static_cast<uint32_t>(groups < (size_t{1} << 20) ? groups : size_t{1} << 20); }
 

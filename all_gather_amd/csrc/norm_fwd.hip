@@ -7,6 +7,8 @@
 // statistics are two passes over the registers, the second on deviations from the mean, which cancels
 // nothing.  Rows too long for that are read again from the caches.  All sums are fp32 in a fixed order.
 
+#include <type_traits>
+
 #include "norm_common.h"
 
 namespace mr {
@@ -14,16 +16,25 @@ namespace {
 
 constexpr int kFwdLanes = 256;  // lanes of a workgroup whose rows take a wave or less each
 
+// The row set of workgroup b of n: workgroups are dealt to the eight XCDs in turn, and runs of 16 sets that follow one another
+// go to one XCD (2048 rows of 4096, W = 8 with a residual: 33.3 us in plain order, 31.8 in runs of 4 to 16).
+__device__ __forceinline__ uint32_t group_of(uint32_t b, uint32_t n) {
+  constexpr uint32_t kRun = 16, kDeal = 8 * kRun;
+  return b < n / kDeal * kDeal ? b / kDeal * kDeal + b % 8 * kRun + b % kDeal / 8 : b;
+}
+
 // Row held in registers.  Workgroups walk rows b, b + grid, ...: gamma and beta are loaded once, and with one input the
 // next row's packs are loaded before this row's sums.  Loads and stores leave through one counter that a wait can only
 // count back on, so every full round issues the same ones on every path: lanes past the row's end store its last pack
 // once more, and the row's statistics collect in registers until a wave's lanes are full.  (With predicated stores a
 // round waited for the last one's stores to reach memory: 16384 x 8192 bf16 took 95 to 129 us.)
-template <class T, class WT, int B, int K, bool Sum>
-__global__ __launch_bounds__(1024, K == 1 ? 8 : 4) void norm_fwd_row(NormFwdArgs a) {
+template <class T, class WT, int B, int K, bool Sum, int Lanes>
+__global__ __launch_bounds__(Lanes, K == 1 ? 8 : Lanes == 768 ? 3 : 4) void norm_fwd_row(NormFwdArgs a) {
   constexpr int kV = kPack<T>;
-  constexpr bool kHold = K == 1;                 // gamma and beta stay in registers
-  constexpr bool kAhead = !Sum && K * kV <= 16;   // the next row's packs are loaded ahead
+  // gamma and beta stay in registers (their loads would otherwise wait for the next row's, issued before them)
+  constexpr bool kHold = K * kV <= 16 && !(Sum && Lanes == 1024 && K > 1);
+  constexpr bool kAhead = !Sum && kHold;       // the next rows' packs are loaded ahead,
+  constexpr int kDepth = Lanes < 1024 ? 2 : 1;  // so many rows
   __shared__ WaveWords lds[2][B == kWaves ? 4 : 1];  // rows of 1 wave need none, of more at most 4 fit a workgroup
   const int lanes = B == kWaves ? a.waves * 64 : B;
   const int lane = threadIdx.x % lanes;
@@ -157,16 +168,22 @@ __global__ __launch_bounds__(1024, K == 1 ? 8 : 4) void norm_fwd_row(NormFwdArgs
     }
     if (++kept == kKeep) flush();
   };
-  Row next;
-  if (kAhead) next = fetch(base);
+  Row next[kDepth];
+  if (kAhead)
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) next[d] = fetch(base + d * stride);
   for (; base + set <= a.rows; base += stride) {
     const size_t at = (base + sub) * a.cols;
     float x[K][kV], mean, rstd;
     if constexpr (Sum) {
       sum_inputs(at, x);
     } else {
-      const Row r = kAhead ? next : fetch(base);
-      if (kAhead) next = fetch(base + stride);
+      const Row r = kAhead ? next[0] : fetch(base);
+      if (kAhead) {
+#pragma unroll
+        for (int d = 1; d < kDepth; ++d) next[d - 1] = next[d];
+        next[kDepth - 1] = fetch(base + kDepth * stride);
+      }
 #pragma unroll
       for (int k = 0; k < K; ++k) widen(r.x[k], x[k]);
     }
@@ -256,11 +273,17 @@ void fwd_row(NormFwdArgs a, int waves, hipStream_t st) {
   const int lanes = B == kWaves ? waves * 64 : B;
   const int block = lanes < kFwdLanes ? kFwdLanes / lanes * lanes : lanes;  // up to 4 rows of a wave or more
   const size_t groups = (a.rows + block / lanes - 1) / (block / lanes);
-  if (a.terms > 1 || a.x_out)
-    hipLaunchKernelGGL((norm_fwd_row<T, WT, B, K, true>), dim3(norm_grid(groups)), dim3(block), 0, st, a);
-  else
-    hipLaunchKernelGGL((norm_fwd_row<T, WT, B, K, false>), dim3(resident_grid<norm_fwd_row<T, WT, B, K, false>>(block, groups)),
-                       dim3(block), 0, st, a);
+  auto launch = [&](auto most) {
+    constexpr int kLanes = decltype(most)::value;
+    if (a.terms > 1 || a.x_out)
+      hipLaunchKernelGGL((norm_fwd_row<T, WT, B, K, true, kLanes>), dim3(norm_grid(groups)), dim3(block), 0, st, a);
+    else
+      hipLaunchKernelGGL((norm_fwd_row<T, WT, B, K, false, kLanes>),
+                         dim3(resident_grid<norm_fwd_row<T, WT, B, K, false, kLanes>>(block, groups)), dim3(block), 0, st, a);
+  };
+  if constexpr (K > 1)
+    if (block <= 768) return launch(std::integral_constant<int, 768>());  // 168 registers a lane, not 128
+  launch(std::integral_constant<int, 1024>());
 }
 
 template <class T, class WT>
