@@ -35,6 +35,8 @@ struct NormBwdArgs {
   size_t rows, cols;
   uint32_t groups;
   int waves;          // waves to a row (set by the launch)
+  uint32_t* arrived;  // zero between launches
+  int one_launch;     // 1: the workgroup that arrives last adds `part` up (set by the launch)
 };
 // Row groups of the backward pass of this shape: each sums its rows' part of the weight gradients in
 // registers and writes one row of `part`.  A function of the shape alone, so results do not depend on the device.

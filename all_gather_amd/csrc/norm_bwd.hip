@@ -15,6 +15,13 @@ namespace {
 
 constexpr int kBwdLanes = 1024;  // most lanes of a workgroup; with 768 a lane has 168 registers, not 128
 
+// Column c of dgamma and then dbeta.
+template <class WT>
+__device__ __forceinline__ void write_weight(const NormBwdArgs& a, size_t c, float s) {
+  char* out = c < a.cols ? a.dgamma : a.dbeta;
+  if (out) store1<WT>(out + (c < a.cols ? c : c - a.cols) * WT::kSize, s);
+}
+
 // Workgroup b of `groups` takes row sets b, b + groups, ...; a set is as many rows as the workgroup holds.  The next set's
 // x and dy are loaded before this set's sums where registers allow; as in the forward pass every full round issues the same
 // loads and stores on every path.
@@ -176,7 +183,15 @@ __global__ __launch_bounds__(Lanes) void norm_bwd_row(NormBwdArgs a) {
         }
       if (sub == 0) {
         float* o = out + h * a.cols + c.at[k];
-        if (c.lo[k] == 0) {
+        if (a.groups == 1) {
+#pragma unroll
+          for (int i = 0; i < kV; ++i)
+            if (i >= c.lo[k]) write_weight<WT>(a, h * a.cols + c.at[k] + i, f[i]);
+        } else if (a.one_launch) {  // write-through, for a reader in this launch
+#pragma unroll
+          for (int i = 0; i < kV; ++i)
+            if (i >= c.lo[k]) __hip_atomic_store(o + i, f[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        } else if (c.lo[k] == 0) {
           store_raw<EFp32, kV, false>(reinterpret_cast<char*>(o), narrow<EFp32, kV>(f));
         } else {
 #pragma unroll
@@ -185,6 +200,41 @@ __global__ __launch_bounds__(Lanes) void norm_bwd_row(NormBwdArgs a) {
         }
       }
     }
+  if (!a.one_launch || a.groups == 1) return;
+  // Every lane's stores are acknowledged before the workgroup's arrival is counted; the last one's loads follow the count.
+  __shared__ bool last;
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = __hip_atomic_fetch_add(a.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    if (last) __hip_atomic_store(a.arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!last) return;
+  // `slices` lanes share a column where there are few; device-scope loads are slow, so eight of a lane's are in flight.
+  const uint32_t n = 2 * static_cast<uint32_t>(a.cols);
+  const uint32_t slices = n < blockDim.x ? blockDim.x / n : 1;
+  const uint32_t slice = threadIdx.x / n;
+  for (uint32_t j = slices > 1 ? threadIdx.x % n : threadIdx.x; j < n; j += blockDim.x) {
+    float s = 0.0f;
+    if (slices == 1 || slice < slices) {
+#pragma unroll 8
+      for (uint32_t g = slices > 1 ? slice : 0; g < a.groups; g += slices)
+        s += __hip_atomic_load(a.part + static_cast<size_t>(g) * n + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (slices == 1) {
+      write_weight<WT>(a, j, s);
+      continue;
+    }
+    if (slice < slices) part[slice * n + j] = s;
+    __syncthreads();
+    if (threadIdx.x < n) {
+      s = 0.0f;
+      for (uint32_t i = 0; i < slices; ++i) s += part[i * n + threadIdx.x];
+      write_weight<WT>(a, threadIdx.x, s);
+    }
+    break;
+  }
 }
 
 // Rows of any length: dx with two sweeps over the row, the second from the caches.  A lane reads a pack's inputs
@@ -282,8 +332,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_finish(NormBwdArgs a) {
   s = 0.0f;
 #pragma unroll
   for (int i = 0; i < kParts; ++i) s += lds[i][threadIdx.x];
-  char* out = c < a.cols ? a.dgamma : a.dbeta;
-  if (out) store1<WT>(out + (c < a.cols ? c : c - a.cols) * WT::kSize, s);
+  write_weight<WT>(a, c, s);
 }
 
 // The shape of a row that is held in registers: lanes (B, waves) and packs a lane; K = 0 if it is not.
@@ -325,12 +374,18 @@ void bwd_any(const NormBwdArgs& a, size_t packs, hipStream_t st) {
   if (a.dx) hipLaunchKernelGGL((norm_bwd_any_dx<T, WT, B>), dim3(norm_grid(a.rows)), dim3(B), 0, st, a);
 }
 
+// Most bytes of partial sums that the launch's last workgroup adds up by itself, sparing the second launch: a pass of
+// 1000 x 100 fp32 or 64 x 512 bf16 takes 8.2 us from the host with it and 11.3 without; at 256 KiB (256 x 1024 bf16) the one
+// workgroup's device-scope loads take longer than the launch, 25 us with and 11.3 without.
+constexpr size_t kOneLaunch = 128 << 10;
+
 template <class T, class WT>
-hipError_t bwd(const NormBwdArgs& a, hipStream_t st) {
+hipError_t bwd(NormBwdArgs a, hipStream_t st) {
   constexpr int kV = kPack<T>;
   const size_t packs = (a.cols + kV - 1) / kV;
   if (a.rows) {
     const Held h = held(a.cols, kV);
+    a.one_launch = h.K && a.dx && a.part && size_t{a.groups} * 2 * a.cols * 4 <= kOneLaunch;
     if (a.cols < kV)
       bwd_any<T, WT, 64>(a, packs, st);
     else if (h.K == 0 || !a.dx)
@@ -350,19 +405,16 @@ hipError_t bwd(const NormBwdArgs& a, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.dgamma || a.dbeta)
+  if (a.part && !a.one_launch)
     hipLaunchKernelGGL((norm_bwd_finish<WT>), dim3(static_cast<uint32_t>((2 * a.cols + 31) / 32)), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-#ifndef MR_NB_GROUPS
-#define MR_NB_GROUPS 256
-#endif
 uint32_t norm_bwd_groups(size_t rows, size_t cols, mr_dtype dt) {
   const Held h = held(cols, 16 / elem_size(dt));
-  const size_t set = h.K ? set_of(h) : 1, most = h.K ? MR_NB_GROUPS : 64;
+  const size_t set = h.K ? set_of(h) : 1, most = h.K ? 256 : cols < 8 ? 4096 : 64;
   const size_t want = (rows + set - 1) / set;
   return static_cast<uint32_t>(want < most ? want : most);
 }

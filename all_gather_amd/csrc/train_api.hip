@@ -176,6 +176,7 @@ mr_status layer_norm_backward(const void* dy, const void* x, const void* gamma, 
     s = mr::stream_workspace(st, size_t{a.groups} * 2 * cols * 4, &ctrl, &data);
     if (s != MR_OK) return s;
     a.part = reinterpret_cast<float*>(data);
+    a.arrived = &ctrl->arrived[0][0];
   }
   if (mr::trace_on())
     std::fprintf(stderr, "[mr] layer_norm backward rows=%zu cols=%zu dtype=%d groups=%u\n", rows, cols,
