@@ -374,10 +374,16 @@ void bwd_any(const NormBwdArgs& a, size_t packs, hipStream_t st) {
   if (a.dx) hipLaunchKernelGGL((norm_bwd_any_dx<T, WT, B>), dim3(norm_grid(a.rows)), dim3(B), 0, st, a);
 }
 
-// Most bytes of partial sums that the launch's last workgroup adds up by itself, sparing the second launch: a pass of
-// 1000 x 100 fp32 or 64 x 512 bf16 takes 8.2 us from the host with it and 11.3 without; at 256 KiB (256 x 1024 bf16) the one
-// workgroup's device-scope loads take longer than the launch, 25 us with and 11.3 without.
-constexpr size_t kOneLaunch = 128 << 10;
+// Does the launch's last workgroup add the partial sums up by itself, sparing the second launch?  Where its lanes need at
+// most two rounds of loads: a pass of 1000 x 100 fp32, 64 x 512 or 16 x 1024 bf16 takes 8.2 us from the host with it and 11.3
+// without.  Device-scope loads make a round 2 to 3 us: 256 x 1024 bf16 (8 rounds) took 25 us with and 11.3 without.
+bool one_launch(const NormBwdArgs& a, const Held& h) {
+  if (!h.K || !a.dx || !a.part) return false;
+  if (a.groups == 1) return true;  // no partial sums at all
+  const size_t n = 2 * a.cols, lanes = set_of(h) * (h.B == kWaves ? h.waves * 64 : h.B);
+  const size_t loads = n < lanes ? (a.groups + lanes / n - 1) / (lanes / n) : a.groups;  // of a lane, for one column
+  return (n + lanes - 1) / lanes * ((loads + 7) / 8) <= 2;
+}
 
 template <class T, class WT>
 hipError_t bwd(NormBwdArgs a, hipStream_t st) {
@@ -385,7 +391,7 @@ hipError_t bwd(NormBwdArgs a, hipStream_t st) {
   const size_t packs = (a.cols + kV - 1) / kV;
   if (a.rows) {
     const Held h = held(a.cols, kV);
-    a.one_launch = h.K && a.dx && a.part && size_t{a.groups} * 2 * a.cols * 4 <= kOneLaunch;
+    a.one_launch = one_launch(a, h);
     if (a.cols < kV)
       bwd_any<T, WT, 64>(a, packs, st);
     else if (h.K == 0 || !a.dx)
