@@ -33,8 +33,7 @@ __global__ __launch_bounds__(Lanes, K == 1 ? 8 : Lanes == 768 ? 3 : 4) void norm
   constexpr int kV = kPack<T>;
   // gamma and beta stay in registers (their loads would otherwise wait for the next row's, issued before them)
   constexpr bool kHold = K * kV <= 16 && !(Sum && Lanes == 1024 && K > 1);
-  constexpr bool kAhead = !Sum && kHold;       // the next rows' packs are loaded ahead,
-  constexpr int kDepth = Lanes < 1024 ? 2 : 1;  // so many rows
+  constexpr bool kAhead = !Sum && kHold;  // the next row's packs are loaded ahead
   __shared__ WaveWords lds[2][B == kWaves ? 4 : 1];  // rows of 1 wave need none, of more at most 4 fit a workgroup
   const int lanes = B == kWaves ? a.waves * 64 : B;
   const int lane = threadIdx.x % lanes;
@@ -168,22 +167,16 @@ __global__ __launch_bounds__(Lanes, K == 1 ? 8 : Lanes == 768 ? 3 : 4) void norm
     }
     if (++kept == kKeep) flush();
   };
-  Row next[kDepth];
-  if (kAhead)
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) next[d] = fetch(base + d * stride);
+  Row next;
+  if (kAhead) next = fetch(base);
   for (; base + set <= a.rows; base += stride) {
     const size_t at = (base + sub) * a.cols;
     float x[K][kV], mean, rstd;
     if constexpr (Sum) {
       sum_inputs(at, x);
     } else {
-      const Row r = kAhead ? next[0] : fetch(base);
-      if (kAhead) {
-#pragma unroll
-        for (int d = 1; d < kDepth; ++d) next[d - 1] = next[d];
-        next[kDepth - 1] = fetch(base + kDepth * stride);
-      }
+      const Row r = kAhead ? next : fetch(base);
+      if (kAhead) next = fetch(base + stride);
 #pragma unroll
       for (int k = 0; k < K; ++k) widen(r.x[k], x[k]);
     }
@@ -293,6 +286,10 @@ hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
   const int waves = static_cast<int>((packs + 63) / 64);  // with one pack a lane
   if (a.cols < kV)
     hipLaunchKernelGGL((norm_fwd_any<T, WT, 64>), dim3(norm_grid(a.rows)), dim3(64), 0, st, a);
+  else if (kV == 8 && a.terms == 1 && !a.x_out && packs % 128 == 0 && packs <= 1024)
+    // two packs a lane where they fill their waves: a row's sums cost each lane some 90 operations whatever it holds
+    // (65536 x 1024 bf16 50.8 -> 46.8 us, 16384 x 4096 50.1 -> 48.6; fp32 and part-filled waves measured slower)
+    fwd_row<T, WT, kWaves, 2>(a, static_cast<int>(packs / 128), st);
   else if (packs <= 8)
     fwd_row<T, WT, 8, 1>(a, 1, st);
   else if (packs <= 16)
