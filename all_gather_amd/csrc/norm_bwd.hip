@@ -23,9 +23,8 @@ __device__ __forceinline__ void write_weight(const NormBwdArgs& a, size_t c, flo
 }
 
 // Workgroup b of `groups` takes row sets b, b + groups, ...; a set is as many rows as the workgroup holds (one with more
-// than a pack a lane).  The next set's
-// x and dy are loaded before this set's sums where registers allow; as in the forward pass every full round issues the same
-// loads and stores on every path.
+// than a pack a lane).  The next set's x and dy are loaded before this set's sums where registers allow; as in the
+// forward pass every full round issues the same loads and stores on every path.
 template <class T, class WT, int B, int K, bool Dres, int Lanes>
 __global__ __launch_bounds__(Lanes) void norm_bwd_row(NormBwdArgs a) {
   constexpr int kV = kPack<T>;
@@ -98,7 +97,8 @@ __global__ __launch_bounds__(Lanes) void norm_bwd_row(NormBwdArgs a) {
   };
   int flip = 0;
   auto row_sums = [&](const Row& r, float* c1, float* c2) {
-    float x = lanes_sum<B>(*c1), y = lanes_sum<B>(*c2);
+    const bool alone = K == 1 && (B != kWaves || a.waves == 1);  // no wave waits for another
+    float x = alone ? wave_sum<B>(*c1) : lanes_sum<B>(*c1), y = alone ? wave_sum<B>(*c2) : lanes_sum<B>(*c2);
     if (Dres)  // has arrived before the barrier: dx may take its place, and a short last pack reads a neighbour's elements
 #pragma unroll
       for (int k = 0; k < K; ++k)

@@ -16,9 +16,9 @@ constexpr int kPack = 16 / T::kSize;
 constexpr int kWaves = 64;
 
 // A lane's packs of V elements of a row of `cols` >= V elements on `lanes` lanes.  The row's last pack, if short, is read as
-// the row's last V elements, of which the first `lo` belong to the neighbouring pack: every access is one whole pack, and both
-// lanes store the same bits where they overlap (predicated single elements instead took a 200003 x 509 fp16
-// backward pass 16% longer).  A pack past the row's end has lo = V: read as that last pack, never stored.
+// the row's last V elements, of which the first `lo` belong to the neighbouring pack: every access is one whole pack, with
+// no lane predicated by element, and both lanes store the same bits where they overlap.  A pack past the row's end has
+// lo = V: it is read, and stored, as that last pack, and adds nothing to a sum.
 template <int V, int K>
 struct RowPacks {
   uint32_t at[K];

@@ -175,7 +175,9 @@ __device__ __forceinline__ void store_part(char* p, const float (&f)[N], int cnt
 
 // Sum over the B neighbouring lanes (8, 16, 32 or 64) that hold a row, in every one of them, in a fixed order.  Moves within 16
 // lanes ride on the adds as DPP operands (quads by 1 and 2, then the mirrored half row and row); the four rows of a
-// wave are read into scalar registers.  A butterfly of LDS-routed shuffles took the backward pass 3% longer.
+// wave are read into scalar registers.  A butterfly of LDS-routed shuffles (wave_sum) measured slower where the waves of
+// a workgroup wait for one another: forward 16384 x 8192 89.1 -> 90.4 us, backward 60003 x 1025 84 -> 87.  Where they do
+// not it leaves the vector units free: backward 200003 x 512 109.7 -> 103.4 us.
 template <int Ctrl>
 __device__ __forceinline__ float dpp(float x) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), Ctrl, 0xf, 0xf, true));
@@ -196,10 +198,11 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
-// Sum over the 64 lanes of a wave, in every lane (a butterfly: the order is fixed).
-__device__ __forceinline__ double wave_sum(double x) {
+// The same sum as a butterfly of shuffles (B lanes), in every lane.
+template <int B = 64, class F>
+__device__ __forceinline__ F wave_sum(F x) {
 #pragma unroll
-  for (int m = 32; m; m >>= 1) x += __shfl_xor(x, m);
+  for (int m = B / 2; m; m >>= 1) x += __shfl_xor(x, m);
   return x;
 }
 
