@@ -304,7 +304,8 @@ mr_status mr_grad_norm(const void* const* grads, const uint64_t* counts, int P, 
  *     finite, the whole block reads as NaN).  Values are rounded to one of their two neighbours, up with
  *     probability (distance to the lower) / (spacing), by 16 bits of a hash of (seed, t, element): calls with the same
  *     arguments give the same bits.  A second moment that is not zero is never rounded to zero.  A state of zero bytes is
- *     the start.  The step itself uses m' and v' before they are rounded.
+ *     the start.  The step itself uses m' and v' before they are rounded.  Gradients (times f) below 2^47 in magnitude; the
+ *     block of a larger one becomes not finite.
  * master: floats, or NULL.  With it, p is read from master and written to both; `params` is not read (and may be NULL
  *     if params_out is given).  Only for 16-bit parameters.
  *
@@ -448,7 +449,8 @@ mr_status mr_get_option(mr_option opt, int64_t* value);
  * mr_allgather_param_contig_sdma, mr_sdma_engines and MR_ERR_ENGINE; 1.04 added
  * mr_allreduce_sum_noalloc and the last-arriver hand-off on XCD-local units (the default up to 32 MiB
  * per rank buffer); 1.05 added MR_OPT_SDMA_CU_BELOW (small parameters of the SDMA gather on the
- * compute units). */
+ * compute units).  The training-step entry points (mr_layer_norm_forward and the four after it) came later
+ * under the same number: they add symbols and change none. */
 int mr_version(void);
 
 #ifdef __cplusplus

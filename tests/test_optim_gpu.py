@@ -229,6 +229,23 @@ def test_not_finite_gradient_without_clip():
             assert torch.isfinite(p.cpu()[ok]).all() and torch.isnan(p.cpu()[~ok]).all(), (bits, bad)
 
 
+@pytest.mark.parametrize("bits,low", [(32, -55), (8, -70)])
+def test_gradients_of_every_size(bits, low):
+    """With eps = 0 the first step moves a parameter by lr whatever the gradient's size: no over- or underflow on the way to the
+    quotient, from 2^low (where the fp32 v of the 32-bit form is still normal) to 2^46.  A tolerance of 24 u of the step, 2 u of p."""
+    e = torch.arange(low, 47)
+    g = torch.ldexp(torch.ones(len(e)), e).repeat_interleave(32).to(device())
+    for sign in (1.0, -1.0):
+        p, st = torch.ones_like(g), mr.adamw_init([g], bits)
+        mr.adamw_step([p], [sign * g], st, 0.125, 1, weight_decay=0.0, eps=0.0)
+        assert float((p.double() - (1 - sign * 0.125)).abs().max()) <= 24 * U * 0.125 + 2 * U
+        m, v = st.moments()
+        # the 8-bit form's roots as they are stored: their squares leave fp32's range
+        r = v.sqrt() if bits == 32 else (st.v.float().view(-1, 32) * st.v_scale.float().view(-1, 1)).view(-1)
+        assert float((m / (sign * 0.1 * g) - 1).abs().max()) <= (1 / 8 if bits == 8 else 8 * U)
+        assert float((r / (0.001 ** 0.5 * g) - 1).abs().max()) <= (1 / 8 if bits == 8 else 16 * U)
+
+
 def test_zero_state_and_zero_gradient():
     for bits in (32, 8):
         p, g = torch.ones(100, device=device()), torch.zeros(100, device=device())
