@@ -242,10 +242,59 @@ __global__ __launch_bounds__(Lanes) void norm_bwd_row(NormBwdArgs a) {
   }
 }
 
+// Rows shorter than a pack: a lane to a row, `groups` waves; each writes its rows' part of the weight gradients.
+template <class T, class WT>
+__global__ __launch_bounds__(64) void norm_bwd_tiny(NormBwdArgs a) {
+  constexpr int kMost = kPack<T> - 1;
+  const int cols = static_cast<int>(a.cols);
+  const float inv = 1.0f / static_cast<float>(cols);
+  float dg[kMost], db[kMost];
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) dg[i] = db[i] = 0.0f;
+  for (size_t row = static_cast<size_t>(blockIdx.x) * 64 + threadIdx.x; row < a.rows; row += static_cast<size_t>(gridDim.x) * 64) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float xh[kMost], gd[kMost], c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (i >= cols) break;
+      const size_t at = (row * cols + i) * T::kSize;
+      xh[i] = (load1<T>(a.x + at) - mean) * rstd;
+      const float dy = load1<T>(a.dy + at);
+      gd[i] = a.gamma ? load1<WT>(a.gamma + i * WT::kSize) * dy : dy;
+      c1 += gd[i];
+      c2 = __builtin_fmaf(gd[i], xh[i], c2);
+      dg[i] = __builtin_fmaf(dy, xh[i], dg[i]);
+      db[i] += dy;
+    }
+    c1 *= inv;
+    c2 *= inv;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (i >= cols || !a.dx) break;
+      const size_t at = (row * cols + i) * T::kSize;
+      float dx = rstd * (gd[i] - __builtin_fmaf(xh[i], c2, c1));
+      if (a.dres) dx += load1<T>(a.dres + at);
+      store1<T>(a.dx + at, dx);
+    }
+  }
+  if (!a.part) return;
+  float* out = a.part + static_cast<size_t>(blockIdx.x) * 2 * cols;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    if (i >= cols) break;
+    const float g = wave_sum(dg[i]), b = wave_sum(db[i]);
+    if (threadIdx.x == 0) {
+      out[i] = g;
+      out[cols + i] = b;
+    }
+  }
+}
+
 // Rows of any length: dx with two sweeps over the row, the second from the caches.  A lane reads a pack's inputs
 // before it writes that pack, so dx may take the place of one of them.
-template <class T, class WT, int B>
-__global__ __launch_bounds__(B) void norm_bwd_any_dx(NormBwdArgs a) {
+template <class T, class WT>
+__global__ __launch_bounds__(1024) void norm_bwd_any_dx(NormBwdArgs a) {
+  constexpr int B = 1024;
   __shared__ WaveWords lds[2];
   constexpr int kV = kPack<T>;
   const float inv = 1.0f / static_cast<float>(a.cols);
@@ -373,11 +422,11 @@ void bwd_row(NormBwdArgs a, const Held& h, hipStream_t st) {
   }
 }
 
-template <class T, class WT, int B>
+template <class T, class WT>
 void bwd_any(const NormBwdArgs& a, size_t packs, hipStream_t st) {
   if (a.part)  // first: dx may take the place of x or dy
     hipLaunchKernelGGL((norm_bwd_any_weights<T>), dim3(static_cast<uint32_t>((packs + 63) / 64), a.groups), dim3(64), 0, st, a);
-  if (a.dx) hipLaunchKernelGGL((norm_bwd_any_dx<T, WT, B>), dim3(norm_grid(a.rows)), dim3(B), 0, st, a);
+  if (a.dx) hipLaunchKernelGGL((norm_bwd_any_dx<T, WT>), dim3(norm_grid(a.rows)), dim3(1024), 0, st, a);
 }
 
 // Does the launch's last workgroup add the partial sums up by itself, sparing the second launch?  Where its lanes need at
@@ -399,9 +448,9 @@ hipError_t bwd(NormBwdArgs a, hipStream_t st) {
     const Held h = held(a.cols, kV);
     a.one_launch = one_launch(a, h);
     if (a.cols < kV)
-      bwd_any<T, WT, 64>(a, packs, st);
+      hipLaunchKernelGGL((norm_bwd_tiny<T, WT>), dim3(a.groups), dim3(64), 0, st, a);
     else if (h.K == 0 || !a.dx)
-      bwd_any<T, WT, 1024>(a, packs, st);
+      bwd_any<T, WT>(a, packs, st);
     else if (h.B == 8)
       bwd_row<T, WT, 8, 1>(a, h, st);
     else if (h.B == 16)
@@ -426,7 +475,8 @@ hipError_t bwd(NormBwdArgs a, hipStream_t st) {
 
 uint32_t norm_bwd_groups(size_t rows, size_t cols, mr_dtype dt) {
   const Held h = held(cols, 16 / elem_size(dt));
-  const size_t set = h.K ? set_of(h) : 1, most = h.K ? 256 : cols < 8 ? 4096 : 64;
+  const bool tiny = cols < static_cast<size_t>(16 / elem_size(dt));
+  const size_t set = h.K ? set_of(h) : tiny ? 64 : 1, most = h.K ? 256 : tiny ? 1024 : 64;
   const size_t want = (rows + set - 1) / set;
   return static_cast<uint32_t>(want < most ? want : most);
 }

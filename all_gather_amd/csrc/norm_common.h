@@ -65,11 +65,10 @@ __device__ __forceinline__ float words_sum(const WaveWords& l, int waves) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// Sum over a workgroup of B lanes, in every one of them.
+// Sum over a workgroup of B lanes (several waves), in every one of them.
 template <int B>
 __device__ __forceinline__ float workgroup_sum(float x, WaveWords& l) {
   x = lanes_sum<64>(x);
-  if (B == 64) return x;
   if ((threadIdx.x & 63) == 0) l.w[threadIdx.x >> 6] = x;
   __syncthreads();
   return words_sum(l, B / 64);

@@ -205,10 +205,47 @@ __global__ __launch_bounds__(Lanes, K == 1 ? 8 : Lanes == 768 ? 3 : 4) void norm
   flush();
 }
 
+// Rows shorter than a pack: a lane to a row.
+template <class T, class WT>
+__global__ __launch_bounds__(256) void norm_fwd_tiny(NormFwdArgs a) {
+  constexpr int kMost = kPack<T> - 1;
+  const int cols = static_cast<int>(a.cols);
+  const float inv = 1.0f / static_cast<float>(cols);
+  for (size_t row = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; row < a.rows; row += static_cast<size_t>(gridDim.x) * 256) {
+    float x[kMost];
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (i >= cols) break;
+      const size_t at = (row * cols + i) * T::kSize;
+      x[i] = load1<T>(a.in[0] + at);
+      for (int r = 1; r < a.terms; ++r) x[i] += load1<T>(a.in[r] + at);
+      s += x[i];
+    }
+    const float mean = s * inv;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i)
+      if (i < cols) s = __builtin_fmaf(x[i] - mean, x[i] - mean, s);
+    const float rstd = 1.0f / __builtin_sqrtf(s * inv + a.eps);
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (i >= cols) break;
+      const size_t at = (row * cols + i) * T::kSize;
+      if (a.x_out) store1<T>(a.x_out + at, x[i]);
+      const float g = a.gamma ? load1<WT>(a.gamma + i * WT::kSize) : 1.0f, b = a.beta ? load1<WT>(a.beta + i * WT::kSize) : 0.0f;
+      store1<T>(a.y + at, __builtin_fmaf((x[i] - mean) * rstd, g, b));
+    }
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+}
+
 // Rows of any length: three sweeps over the row, the later two from the caches.  A lane reads every input
 // of a pack before it writes that pack, so outputs may replace inputs exactly.
-template <class T, class WT, int B>
-__global__ __launch_bounds__(B) void norm_fwd_any(NormFwdArgs a) {
+template <class T, class WT>
+__global__ __launch_bounds__(1024) void norm_fwd_any(NormFwdArgs a) {
+  constexpr int B = 1024;
   __shared__ WaveWords lds[2];
   constexpr int kV = kPack<T>;
   const float inv = 1.0f / static_cast<float>(a.cols);
@@ -288,7 +325,7 @@ hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
   const size_t packs = (a.cols + kV - 1) / kV;
   const int waves = static_cast<int>((packs + 63) / 64);  // with one pack a lane
   if (a.cols < kV)
-    hipLaunchKernelGGL((norm_fwd_any<T, WT, 64>), dim3(norm_grid(a.rows)), dim3(64), 0, st, a);
+    hipLaunchKernelGGL((norm_fwd_tiny<T, WT>), dim3(norm_grid((a.rows + 255) / 256)), dim3(256), 0, st, a);
   else if (kV == 8 && a.terms == 1 && !a.x_out && packs % 128 == 0 && packs <= 1024)
     // two packs a lane where they fill their waves: a row's sums cost each lane some 90 operations whatever it holds
     // (65536 x 1024 bf16 50.8 -> 46.8 us, 16384 x 4096 50.1 -> 48.6; fp32 and part-filled waves measured slower)
@@ -306,7 +343,7 @@ hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
   else if (waves <= 64)
     fwd_row<T, WT, kWaves, 4>(a, (waves + 3) / 4, st);
   else
-    hipLaunchKernelGGL((norm_fwd_any<T, WT, 1024>), dim3(norm_grid(a.rows)), dim3(1024), 0, st, a);
+    hipLaunchKernelGGL((norm_fwd_any<T, WT>), dim3(norm_grid(a.rows)), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 

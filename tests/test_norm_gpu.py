@@ -181,6 +181,16 @@ def test_backward_shapes(rows, cols, dtype, wdtype):
     check_backward(rows, cols, dtype, wdtype, dres=(rows + cols) % 2 == 0)
 
 
+def test_rows_shorter_than_a_pack():
+    for cols in (1, 2, 3, 5, 7):
+        for dtype, wdtype in (("bf16", "fp32"), ("fp16", "same"), ("fp32", "same")):
+            check_forward(1000, cols, dtype, wdtype, W=2, res=True)
+            if cols > 2:  # two elements' gradient is nothing but cancellation
+                check_backward(70001, cols, dtype, wdtype, dres=True)
+    check_backward(300, 3, "fp32", want=("dgamma", "dbeta"))
+    check_backward(300, 3, "fp32", place="dy")
+
+
 def test_backward_many_rows():
     check_backward(20011, 96, "fp32", dres=True)
     check_backward(5000, 1500, "bf16", "fp32")
