@@ -77,37 +77,51 @@ struct Raw {
   uint32_t w[kWords];
 };
 
-// Nt: non-temporal, for bytes that this launch touches once.
-template <bool Nt, class V>
-__device__ __forceinline__ auto load_v(const V* p) {
-  if constexpr (Nt)
-    return __builtin_nontemporal_load(p);
-  else
-    return *p;
+// Accesses of 8 and 16 bytes at addresses that are multiples of A (2 or 4).  The vector type of reduced alignment is named
+// where memory is touched: as a template argument it would lose that attribute.  Nt: non-temporal, for bytes that
+// this launch touches once.
+template <int A, bool Nt>
+__device__ __forceinline__ u32x4 load16(const char* p) {
+  if constexpr (A == 2) {
+    const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p);
+    if constexpr (Nt) return __builtin_nontemporal_load(q); else return *q;
+  } else {
+    const u32x4_a4* q = reinterpret_cast<const u32x4_a4*>(p);
+    if constexpr (Nt) return __builtin_nontemporal_load(q); else return *q;
+  }
 }
-template <bool Nt, class V, class U>
-__device__ __forceinline__ void store_v(U v, V* p) {
-  if constexpr (Nt)
-    __builtin_nontemporal_store(v, p);
-  else
-    *p = v;
+template <int A, bool Nt>
+__device__ __forceinline__ void store16(char* p, u32x4 v) {
+  if constexpr (A == 2) {
+    u32x4_a2* q = reinterpret_cast<u32x4_a2*>(p);
+    if constexpr (Nt) __builtin_nontemporal_store(v, q); else *q = v;
+  } else {
+    u32x4_a4* q = reinterpret_cast<u32x4_a4*>(p);
+    if constexpr (Nt) __builtin_nontemporal_store(v, q); else *q = v;
+  }
+}
+template <bool Nt>
+__device__ __forceinline__ u32x2 load8(const char* p) {
+  const u32x2_a2* q = reinterpret_cast<const u32x2_a2*>(p);
+  if constexpr (Nt) return __builtin_nontemporal_load(q); else return *q;
+}
+template <bool Nt>
+__device__ __forceinline__ void store8(char* p, u32x2 v) {
+  u32x2_a2* q = reinterpret_cast<u32x2_a2*>(p);
+  if constexpr (Nt) __builtin_nontemporal_store(v, q); else *q = v;
 }
 
 template <class T, int N, bool Nt>
 __device__ __forceinline__ Raw<T, N> load_raw(const char* p) {
   Raw<T, N> r;
   if constexpr (Raw<T, N>::kWords == 2) {
-    const u32x2 v = load_v<Nt>(reinterpret_cast<const u32x2_a2*>(p));
+    const u32x2 v = load8<Nt>(p);
     r.w[0] = v[0];
     r.w[1] = v[1];
   } else {
 #pragma unroll
     for (int i = 0; i < Raw<T, N>::kWords; i += 4) {
-      u32x4 v;
-      if constexpr (T::kSize == 2)
-        v = load_v<Nt>(reinterpret_cast<const u32x4_a2*>(p + 4 * i));
-      else
-        v = load_v<Nt>(reinterpret_cast<const u32x4_a4*>(p + 4 * i));
+      const u32x4 v = load16<T::kSize, Nt>(p + 4 * i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) r.w[i + j] = v[j];
     }
@@ -117,16 +131,11 @@ __device__ __forceinline__ Raw<T, N> load_raw(const char* p) {
 template <class T, int N, bool Nt>
 __device__ __forceinline__ void store_raw(char* p, const Raw<T, N>& r) {
   if constexpr (Raw<T, N>::kWords == 2) {
-    store_v<Nt>(u32x2{r.w[0], r.w[1]}, reinterpret_cast<u32x2_a2*>(p));
+    store8<Nt>(p, u32x2{r.w[0], r.w[1]});
   } else {
 #pragma unroll
-    for (int i = 0; i < Raw<T, N>::kWords; i += 4) {
-      const u32x4 v = {r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]};
-      if constexpr (T::kSize == 2)
-        store_v<Nt>(v, reinterpret_cast<u32x4_a2*>(p + 4 * i));
-      else
-        store_v<Nt>(v, reinterpret_cast<u32x4_a4*>(p + 4 * i));
-    }
+    for (int i = 0; i < Raw<T, N>::kWords; i += 4)
+      store16<T::kSize, Nt>(p + 4 * i, u32x4{r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]});
   }
 }
 
