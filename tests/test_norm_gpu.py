@@ -351,3 +351,31 @@ def test_offsets_past_32_bits():
     mag = (part.double().abs() * (part.double().abs() + m[at].double()[:, None].abs()) * r[at].double()[:, None]).sum(0)
     assert bool(((dg.double() - want).abs() <= 128 * U * mag).all())
     assert np.isclose(float(db.double().mean()), 0.5 * (rows - len(at)) + float(part.double().sum(0).mean()), rtol=(4096 + 64) * U)
+
+
+def test_prepared_calls_and_a_bound_workspace():
+    """Prepared calls give the plain calls' bits; a caller's workspace is used, and refused when it is too small."""
+    rows, cols = 900, 1600
+    gen = torch.Generator().manual_seed(10)
+    x, dy = rand(gen, rows, cols, "bf16"), rand(gen, rows, cols, "bf16")
+    g, b = (torch.randn(cols, generator=gen).to(torch.bfloat16).to(device()) for _ in range(2))
+    m, r = torch.empty(rows, device=device()), torch.empty(rows, device=device())
+    want, got = ([torch.empty_like(x), torch.empty_like(x), torch.empty_like(g), torch.empty_like(g)] for _ in range(2))
+    mr.layer_norm_forward([x], g, b, want[0], mean=m, rstd=r)
+    mr.layer_norm_backward(dy, x, g, m, r, want[1], dgamma=want[2], dbeta=want[3])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    small, large = (torch.empty(n, dtype=torch.uint8, device=device()) for n in (1 << 18, 1 << 22))
+    torch.cuda.synchronize()
+    mr.prepare_layer_norm_forward([x], g, b, got[0], mean=m, rstd=r, stream=s)()
+    backward = mr.prepare_layer_norm_backward(dy, x, g, m, r, got[1], dgamma=got[2], dbeta=got[3], stream=s)
+    mr.set_workspace(small, stream=s)
+    with pytest.raises(mr.MRError) as e:
+        backward()
+    assert e.value.status == -4
+    mr.set_workspace(large, stream=s)
+    backward()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    mr.set_workspace(None, stream=s)
+    torch.cuda.synchronize()
