@@ -367,26 +367,30 @@ __global__ __launch_bounds__(64) void norm_bwd_any_weights(NormBwdArgs a) {
   store_part<EFp32, kV, false>(reinterpret_cast<char*>(out + a.cols), db, cnt);
 }
 
-// dgamma and dbeta: the sum of the groups' rows of `part`.  A workgroup takes 32 of the 2*cols columns; its 32
+// dgamma and dbeta: the sum of the groups' rows of `part`.  A workgroup takes 32 of the 2*cols columns at a time; its 32
 // half waves each add up every 32nd group (8 loads of 256 groups, all in flight), and the first adds the 32 sums.
 template <class WT>
 __global__ __launch_bounds__(1024) void norm_bwd_finish(NormBwdArgs a) {
   constexpr int kCols = 32, kParts = 1024 / kCols;
   __shared__ float lds[kParts][kCols];
-  const size_t c = static_cast<size_t>(blockIdx.x) * kCols + threadIdx.x % kCols;
   const uint32_t w = threadIdx.x / kCols;
-  float s = 0.0f;
-  if (c < 2 * a.cols) {
+  const size_t first = static_cast<size_t>(blockIdx.x) * kCols, n = 2 * a.cols;
+  for (size_t block = first; block < n; block += static_cast<size_t>(gridDim.x) * kCols) {
+    if (block != first) __syncthreads();  // the last columns' sums have been read
+    const size_t c = block + threadIdx.x % kCols;
+    float s = 0.0f;
+    if (c < n) {
 #pragma unroll 8
-    for (uint32_t g = w; g < a.groups; g += kParts) s += a.part[static_cast<size_t>(g) * 2 * a.cols + c];
-  }
-  lds[w][threadIdx.x % kCols] = s;
-  __syncthreads();
-  if (w || c >= 2 * a.cols) return;
-  s = 0.0f;
+      for (uint32_t g = w; g < a.groups; g += kParts) s += a.part[g * n + c];
+    }
+    lds[w][threadIdx.x % kCols] = s;
+    __syncthreads();
+    if (w || c >= n) continue;
+    s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kParts; ++i) s += lds[i][threadIdx.x];
-  write_weight<WT>(a, c, s);
+    for (int i = 0; i < kParts; ++i) s += lds[i][threadIdx.x];
+    write_weight<WT>(a, c, s);
+  }
 }
 
 // The shape of a row that is held in registers: lanes (B, waves) and packs a lane; K = 0 if it is not.
@@ -467,7 +471,7 @@ hipError_t bwd(NormBwdArgs a, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   if (a.part && !a.one_launch)
-    hipLaunchKernelGGL((norm_bwd_finish<WT>), dim3(static_cast<uint32_t>((2 * a.cols + 31) / 32)), dim3(1024), 0, st, a);
+    hipLaunchKernelGGL((norm_bwd_finish<WT>), dim3(norm_grid((2 * a.cols + 31) / 32)), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 

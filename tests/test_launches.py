@@ -1,0 +1,95 @@
+"""What the host code launches, without a GPU: the library's objects linked with a HIP runtime that only writes launches
+down (fake_hip.cpp)."""
+import ctypes
+import os
+import shutil
+import subprocess
+import threading
+import time
+from concurrent.futures import ThreadPoolExecutor
+
+import pytest
+
+import all_gather_amd as mr
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "all_gather_amd", "csrc")
+CLANG = "/opt/rocm/llvm/bin/clang++"
+BF16, FP16, FP32 = 0, 1, 2
+A = [(i + 1) << 40 for i in range(12)]  # far apart, never dereferenced
+MOST_COLS = 2 ** 31 - 1
+
+pytestmark = pytest.mark.skipif(not (os.path.exists(CLANG) and os.path.exists("/opt/rocm/bin/hipcc")),
+                                reason="ROCm toolchain not present")
+
+
+@pytest.fixture(scope="module")
+def fake(tmp_path_factory):
+    from all_gather_amd import _build
+
+    tmp = tmp_path_factory.mktemp("fake")
+    headers = max(os.path.getmtime(os.path.join(CSRC, h)) for h in os.listdir(CSRC) if h.endswith(".h"))
+
+    def compiled(src):
+        path, built = os.path.join(CSRC, src), os.path.join(_build.OBJ, os.path.splitext(src)[0] + ".o")
+        # a file whose interface headers are newer than its object is compiled here; the reduce and gather kernels' is not
+        own = headers if src in ("api.hip", "train_api.hip", "norm_fwd.hip", "norm_bwd.hip", "optim_kernels.hip") else 0
+        if os.path.exists(built) and os.path.getmtime(built) >= max(os.path.getmtime(path), own):
+            return built
+        obj = str(tmp / (src + ".o"))
+        r = subprocess.run([_build.hipcc(), *_build.CFLAGS, "-c", path, "-o", obj], capture_output=True, text=True, timeout=900)
+        assert r.returncode == 0, r.stderr[-2000:]
+        return obj
+
+    with ThreadPoolExecutor(4) as ex:
+        objs = list(ex.map(compiled, _build.SOURCES))
+    lib = str(tmp / "libmr_fake.so")
+    r = subprocess.run([CLANG, "-std=c++17", "-O1", "-g", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
+                        "-Wl,-Bsymbolic", "-Wl,--no-undefined", os.path.join(ROOT, "tests", "fake_hip.cpp"), *objs, "-lpthread",
+                        "-o", lib], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    L = ctypes.CDLL(lib)
+    for name, (res, args) in mr._SIGS.items():
+        f = getattr(L, name)
+        f.restype, f.argtypes = res, args
+    L.fake_allocated.restype = ctypes.c_uint64
+    yield L
+    shutil.rmtree(tmp, ignore_errors=True)
+
+
+def launches(L):
+    out, name, v = [], ctypes.create_string_buffer(400), (ctypes.c_uint64 * 9)()
+    for i in range(L.fake_launches()):
+        assert L.fake_launch(i, name, 400, v) == 0
+        out.append(dict(name=name.value.decode(), stream=v[0], thread=v[1], grid=tuple(v[2:5]), block=tuple(v[5:8]), refused=v[8]))
+    return out
+
+
+def ptrs(*p):
+    return (ctypes.c_void_p * max(len(p), 1))(*p)
+
+
+def counts(*c):
+    return (ctypes.c_uint64 * max(len(c), 1))(*c)
+
+
+def backward(L, rows, cols, dt=BF16, wdt=FP32, dx=A[5], dgamma=A[6], dbeta=A[7], stream=None):
+    return L.mr_layer_norm_backward(A[0], A[1], A[2], A[3], A[4], None, rows, cols, dt, wdt, dx, dgamma, dbeta, stream)
+
+
+def forward(L, rows, cols, dt=BF16, wdt=FP32, W=1, stream=None):
+    return L.mr_layer_norm_forward(ptrs(*A[5:5 + W]), W, None, A[2], A[3], rows, cols, dt, wdt, 1e-5, None, A[0], A[4], A[1], stream)
+
+
+@pytest.mark.parametrize("dt", [BF16, FP16, FP32])
+@pytest.mark.parametrize("rows,cols", [(1, MOST_COLS), (3, 2 ** 26), (1, 2 ** 26 - 1), (1, 2 ** 27 + 5), (2 ** 38, 1), (2 ** 26, 4096),
+                                       (2 ** 24, 8191), (2 ** 20, 40000), (1, 1)])
+def test_every_norm_launch_fits_the_device(fake, dt, rows, cols):
+    """The whole range of rows and columns that the header allows: a call launches all of its kernels or none."""
+    for parts in ({}, dict(dx=None), dict(dgamma=None, dbeta=None)):
+        fake.fake_reset(0)
+        assert backward(fake, rows, cols, dt, **parts) == 0, parts
+        assert fake.fake_launches() >= 1 and not any(x["refused"] for x in launches(fake))
+    fake.fake_reset(0)
+    assert forward(fake, rows, cols, dt) == 0
+    assert fake.fake_launches() == 1 and not any(x["refused"] for x in launches(fake))

@@ -379,3 +379,24 @@ def test_prepared_calls_and_a_bound_workspace():
     assert all(torch.equal(p, q) for p, q in zip(want, got))
     mr.set_workspace(None, stream=s)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("cols", [(1 << 25) + 3, (1 << 26) + 37])
+def test_backward_of_the_widest_rows(cols):
+    """More columns than the launch that finishes the weight gradients has workgroups for: each takes several blocks of them.
+    The tolerances are check_backward's, where a lane adds up cols / 1024 elements of a row."""
+    print(f"[case] norm backward 2x{cols} bf16/fp32", flush=True)
+    gen = torch.Generator(device=device()).manual_seed(12)
+    x, dy = (torch.randn(2, cols, generator=gen, device=device()).to(torch.bfloat16) for _ in range(2))
+    m, r = torch.tensor([0.25, -0.5], device=device()), torch.tensor([1.0, 0.75], device=device())
+    dx, dg, db = torch.empty_like(x), torch.full((cols,), float("nan"), device=device()), torch.full((cols,), float("nan"), device=device())
+    mr.layer_norm_backward(dy, x, None, m, r, dx, dgamma=dg, dbeta=db)
+    dy64, xh = dy.double(), (x.double() - m.double()[:, None]) * r.double()[:, None]
+    big = xh.abs() + (x.double().abs() + m.double().abs()[:, None]) * r.double()[:, None]
+    assert bool(((dg.double() - (dy64 * xh).sum(0)).abs() <= 66 * U * (dy64.abs() * big).sum(0)).all())
+    assert bool(((db.double() - dy64.sum(0)).abs() <= 66 * U * dy64.abs().sum(0)).all())
+    chain = (cols // 1024 + 128) * U
+    want = r.double()[:, None] * (dy64 - dy64.mean(1, keepdim=True) - xh * (dy64 * xh).mean(1, keepdim=True))
+    tol = UO["bf16"] * want.abs() + chain * r.double()[:, None] * (
+        dy64.abs() + dy64.abs().mean(1, keepdim=True) + big * (dy64.abs() * big).mean(1, keepdim=True))
+    assert bool(((dx.double() - want).abs() <= tol + TINY["bf16"]).all())
