@@ -85,6 +85,16 @@ std::map<WsKey, Workspace> g_ws;
 // the caller unbinds the stream's workspace (mr_set_workspace).  Growth at least doubles, so they total
 // less than the live one.
 std::map<std::pair<int, hipStream_t>, std::vector<char*>> g_retired;
+// A call holds its stream's lock from the lookup of the workspace to its last launch: the kernels of one call hand
+// partial sums over in the workspace, and those of another host thread's call must not come between them.
+std::map<std::pair<int, hipStream_t>, std::mutex> g_ws_use;  // entries stay, so their addresses do
+
+std::unique_lock<std::mutex> use_stream(int dev, hipStream_t st) {
+  std::unique_lock<std::mutex> lk(g_ws_mu);
+  std::mutex& m = g_ws_use[{dev, st}];
+  lk.unlock();
+  return std::unique_lock<std::mutex>(m);
+}
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -106,8 +116,9 @@ hipError_t ws_clear(char* base, size_t bytes, hipStream_t st) {
 }
 
 // Returns the workspace of (current device, stream) able to hold a two-shot call of n elements
-// needing `flags` producer flags, allocating or growing a library-owned one.
-mr_status get_workspace(hipStream_t st, size_t n, int esize, size_t flags, Workspace* out) {
+// needing `flags` producer flags, allocating or growing a library-owned one.  `use` holds the stream's lock
+// afterwards; the caller keeps it until the call's last launch.
+mr_status get_workspace(hipStream_t st, size_t n, int esize, size_t flags, Workspace* out, std::unique_lock<std::mutex>* use) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return hip_fail(e);
@@ -116,6 +127,7 @@ mr_status get_workspace(hipStream_t st, size_t n, int esize, size_t flags, Works
   e = hipStreamGetCaptureInfo(st, &cs, &capture);
   if (e != hipSuccess) return hip_fail(e);
   if (cs != hipStreamCaptureStatusActive) capture = 0;
+  *use = use_stream(dev, st);
   std::lock_guard<std::mutex> lk(g_ws_mu);
   if (capture) {  // caller-owned memory bound to the stream is used for captured calls too
     auto own = g_ws.find(WsKey{dev, st, 0});
@@ -227,11 +239,12 @@ mr_status reduce_launch(const char* const* ins, int W, size_t n, mr_dtype dtype,
     if (mr::twoshot_grid(pl) >= (1ull << 24)) return MR_ERR_INVALID_ARG;
     const size_t flags_needed = mr::twoshot_flag_words(pl);
     Workspace ws;
+    std::unique_lock<std::mutex> use;
     if (fixed) {
       if (!ws_fits(fixed->bytes, n, es, flags_needed)) return MR_ERR_WORKSPACE;
       ws = *fixed;
     } else {
-      mr_status s = get_workspace(st, n, es, flags_needed, &ws);
+      mr_status s = get_workspace(st, n, es, flags_needed, &ws, &use);
       if (s != MR_OK) return s;
     }
     // The stage shares out's 16-byte phase, so its body is 16-byte aligned too, and the body starts on a
@@ -413,9 +426,9 @@ size_t workspace_bytes_for(size_t n, int esize) { return ws_bytes_for(n, esize);
 
 hipError_t clear_workspace_words(char* base, size_t bytes, hipStream_t st) { return ws_clear(base, bytes, st); }
 
-mr_status stream_workspace(hipStream_t st, size_t bytes, Ctrl** ctrl, char** data) {
+mr_status stream_workspace(hipStream_t st, size_t bytes, Ctrl** ctrl, char** data, std::unique_lock<std::mutex>* use) {
   Workspace ws;
-  const mr_status s = get_workspace(st, bytes, 1, 0, &ws);
+  const mr_status s = get_workspace(st, bytes, 1, 0, &ws, use);
   if (s != MR_OK) return s;
   *ctrl = reinterpret_cast<Ctrl*>(ws.base);
   *data = ws.base + ws_stage_offset(ws.bytes);
@@ -779,6 +792,7 @@ mr_status mr_set_workspace(mr_stream stream, void* dev_ptr, size_t bytes) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return hip_fail(e);
+  const std::unique_lock<std::mutex> use = use_stream(dev, st);
   std::lock_guard<std::mutex> lk(g_ws_mu);
   // every library-owned buffer of this stream: its own workspace, those of captures made on it, and
   // the ones growth replaced
@@ -823,6 +837,7 @@ mr_status mr_workspace_check(mr_stream stream, uint32_t* flags) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return hip_fail(e);
+  const std::unique_lock<std::mutex> use = use_stream(dev, st);
   std::vector<Workspace> ws;  // the stream's own workspace and those of captures made on it
   {
     std::lock_guard<std::mutex> lk(g_ws_mu);

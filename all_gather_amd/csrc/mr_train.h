@@ -1,6 +1,8 @@
 // Launch interface of the training-step operators, shared by train_api.hip and the kernel files.
 #pragma once
 
+#include <mutex>
+
 #include "mr_internal.h"
 
 namespace mr {
@@ -90,9 +92,10 @@ constexpr int kAdamUp = 16;
 uint32_t adam_tile_elems(mr_dtype dt, mr_dtype gdt, mr_state_format fmt, bool master);
 hipError_t launch_adam(const AdamArgs& a, mr_dtype dt, mr_dtype gdt, mr_state_format fmt, hipStream_t st);
 
-// Helpers of api.hip.  stream_workspace: the stream's library workspace (or the one of the capture under way), with room for `bytes`: its Ctrl words
-// and its data area, which earlier work on the stream has finished with when a later launch runs.
+// Helpers of api.hip.  stream_workspace: the stream's library workspace (or the one of the capture under way), with room
+// for `bytes`: its Ctrl words and its data area.  Earlier work on the stream has finished with both when a later launch
+// runs, and no other thread's call uses them between this call's launches while `use` is held.
 bool trace_on();  // MR_TRACE=1
-mr_status stream_workspace(hipStream_t st, size_t bytes, Ctrl** ctrl, char** data);
+mr_status stream_workspace(hipStream_t st, size_t bytes, Ctrl** ctrl, char** data, std::unique_lock<std::mutex>* use);
 
 }  // namespace mr

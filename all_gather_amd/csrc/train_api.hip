@@ -170,10 +170,11 @@ mr_status layer_norm_backward(const void* dy, const void* x, const void* gamma, 
   a.rows = rows;
   a.cols = cols;
   a.groups = mr::norm_bwd_groups(rows, cols, dtype);
+  std::unique_lock<std::mutex> use;  // to the last launch
   if (dgamma || dbeta) {
     mr::Ctrl* ctrl = nullptr;
     char* data = nullptr;
-    s = mr::stream_workspace(st, size_t{a.groups} * 2 * cols * 4, &ctrl, &data);
+    s = mr::stream_workspace(st, size_t{a.groups} * 2 * cols * 4, &ctrl, &data, &use);
     if (s != MR_OK) return s;
     a.part = reinterpret_cast<float*>(data);
     a.arrived = &ctrl->arrived[0][0];
@@ -229,7 +230,8 @@ mr_status grad_norm(const void* const* grads, const uint64_t* counts, int P, mr_
   if (a.P || launches.empty()) emit();
   mr::Ctrl* ctrl = nullptr;
   char* data = nullptr;
-  const mr_status s = mr::stream_workspace(st, groups * sizeof(double), &ctrl, &data);
+  std::unique_lock<std::mutex> use;  // to the last launch
+  const mr_status s = mr::stream_workspace(st, groups * sizeof(double), &ctrl, &data, &use);
   if (s != MR_OK) return s;
   for (size_t k = 0; k < launches.size(); ++k) {
     mr::GradNormArgs& l = launches[k];

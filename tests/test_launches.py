@@ -93,3 +93,52 @@ def test_every_norm_launch_fits_the_device(fake, dt, rows, cols):
     fake.fake_reset(0)
     assert forward(fake, rows, cols, dt) == 0
     assert fake.fake_launches() == 1 and not any(x["refused"] for x in launches(fake))
+
+
+def grad_norm(L, tensors, stream=None):
+    g = [A[0] + 4096 * i for i in range(tensors)]
+    return L.mr_grad_norm(ptrs(*g), counts(*[64] * tensors), tensors, FP32, 1.0, 1.0, A[3], stream)
+
+
+def two_shot(L, stream=None):
+    return L.mr_allreduce_sum(ptrs(A[0], A[1]), 2, 4096, FP32, A[2], 1, stream)
+
+
+CALLS = {"grad_norm": lambda L, st: grad_norm(L, 300, st), "backward": lambda L, st: backward(L, 5000, 1500, stream=st),
+         "two_shot": two_shot}
+
+
+def at_once(L, first, second, streams):
+    """The launches of two calls from two threads; the second call starts once the first's first kernel is launched, and every
+    launch keeps its thread for 40 ms."""
+    for name, st in zip((first, second), streams):  # workspaces are there
+        assert CALLS[name](L, st) == 0
+    L.fake_reset(40)
+    status = []
+    a = threading.Thread(target=lambda: status.append(CALLS[first](L, streams[0])))
+    b = threading.Thread(target=lambda: status.append(CALLS[second](L, streams[1])))
+    a.start()
+    end = time.monotonic() + 10
+    while not L.fake_launches() and time.monotonic() < end:
+        time.sleep(0.001)
+    b.start()
+    a.join()
+    b.join()
+    assert status == [0, 0]
+    return launches(L)
+
+
+@pytest.mark.parametrize("second", ["grad_norm", "backward", "two_shot"])
+@pytest.mark.parametrize("first", ["grad_norm", "backward"])
+def test_a_call_s_launches_stay_together_on_a_stream(fake, first, second):
+    """The kernels of one call hand partial sums over in the stream's workspace: a call from another host thread that uses the same
+    workspace must not come between them."""
+    got = [x["thread"] for x in at_once(fake, first, second, (0x50, 0x50))]
+    n = {"grad_norm": 3, "backward": 2, "two_shot": 1}
+    assert len(got) == n[first] + n[second]
+    assert len(set(got[:n[first]])) == 1 and len(set(got[n[first]:])) == 1, got
+
+
+def test_streams_do_not_wait_for_one_another(fake):
+    got = [x["stream"] for x in at_once(fake, "grad_norm", "backward", (0x50, 0x60))]
+    assert sorted(got) == [0x50] * 3 + [0x60] * 2 and got != [0x50] * 3 + [0x60] * 2
