@@ -108,6 +108,14 @@ __global__ __launch_bounds__(Lanes) void norm_bwd_row(NormBwdArgs a) {
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < Raw<T, kV>::kWords; ++i) asm volatile("" ::"v"(r.dres[k].w[i]));
+    // With several packs a lane a wave may lie past the row's end with one of them, which it reads and stores as the row's last
+    // pack and adds to no sum: it too has x and dy (a pack is one load) before the barrier, after which dx may be in their place.
+    if (K > 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        constexpr int kLast = Raw<T, kV>::kWords - 1;
+        asm volatile("" ::"v"(r.x[k].w[kLast]), "v"(r.dy[k].w[kLast]));
+      }
     if (B == kWaves && a.waves > 1) {  // two sets of words in turn: one barrier a round
       if ((threadIdx.x & 63) == 0) {
         lds[flip][0][sub].w[wave] = x;

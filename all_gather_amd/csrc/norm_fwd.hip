@@ -119,6 +119,11 @@ __global__ __launch_bounds__(Lanes, K == 1 ? 8 : Lanes == 768 ? 3 : 4) void norm
         for (int i = 0; i < kV; ++i) s += i >= c.lo[k] ? x[k][i] : 0.0f;
       }
     }
+    // With several packs a lane a wave may lie past the row's end with one of them, which it reads and stores as the row's last
+    // pack and adds to no sum: it too has x (a pack is one load) before the barrier, after which y may be in its place.
+    if (K > 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) asm volatile("" ::"v"(x[k][kV - 1]));
     const float m = row_sum(s, lds[0]) * inv;
     s = 0.0f;
 #pragma unroll

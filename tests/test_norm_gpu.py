@@ -400,3 +400,45 @@ def test_backward_of_the_widest_rows(cols):
     tol = UO["bf16"] * want.abs() + chain * r.double()[:, None] * (
         dy64.abs() + dy64.abs().mean(1, keepdim=True) + big * (dy64.abs() * big).mean(1, keepdim=True))
     assert bool(((dx.double() - want).abs() <= tol + TINY["bf16"]).all())
+
+
+# rows past one round of the grid, with a ragged last set: lanes of 16, waves, two and four packs a lane (of which the last wave's
+# second or fourth lies past the row's end), and rows past the registers
+@pytest.mark.parametrize("rows,cols,dtype", [(20011, 96, "bf16"), (5001, 1500, "fp16"), (601, 8700, "bf16"), (601, 8700, "fp16"),
+                                             (700, 14337, "bf16"), (601, 4100, "fp32"), (601, 12300, "fp32"), (601, 16383, "fp32"),
+                                             (301, 20000, "bf16")])
+def test_backward_in_place_over_many_rounds(rows, cols, dtype):
+    gen = torch.Generator().manual_seed(13)
+    x, dy, dr = (rand(gen, rows, cols, dtype) for _ in range(3))
+    g = (1 + 0.2 * torch.randn(cols, generator=gen)).to(device())
+    m, r = x.float().mean(1), torch.rsqrt(x.float().var(1) + EPS)
+    for res, places in ((None, ("dy", "x")), (dr, ("dy", "x", "dres"))):
+        want = torch.empty_like(x), torch.empty(cols, device=device()), torch.empty(cols, device=device())
+        mr.layer_norm_backward(dy, x, g, m, r, want[0], dgamma=want[1], dbeta=want[2], dres=res)
+        for place in places:
+            print(f"[case] norm backward in place {rows}x{cols} {dtype} dres={res is not None} place={place}", flush=True)
+            ins = {"dy": dy, "x": x, "dres": res}
+            ins[place] = ins[place].clone()
+            got = ins[place], torch.empty_like(want[1]), torch.empty_like(want[2])
+            mr.layer_norm_backward(ins["dy"], ins["x"], g, m, r, got[0], dgamma=got[1], dbeta=got[2], dres=ins["dres"])
+            assert all(torch.equal(a, b) for a, b in zip(want, got)), (res is not None, place)
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(100003, 96, "bf16"), (5001, 1500, "fp16"), (9001, 1024, "bf16"), (3001, 8192, "bf16"),
+                                             (3001, 8700, "bf16"), (3001, 8700, "fp16"), (2001, 17000, "fp16"), (3001, 4100, "fp32"),
+                                             (2001, 12300, "fp32"), (601, 33000, "bf16")])
+def test_forward_in_place_over_many_rounds(rows, cols, dtype):
+    gen = torch.Generator().manual_seed(14)
+    bufs = [rand(gen, rows, cols, dtype) for _ in range(3)]
+    g, b = (torch.randn(cols, generator=gen).to(device()) for _ in range(2))
+    for W in (1, 2):
+        res = bufs[2] if W > 1 else None
+        for x_out in (False, True):
+            print(f"[case] norm forward in place {rows}x{cols} {dtype} W={W} x_out={x_out}", flush=True)
+            want = [torch.empty_like(bufs[0]), torch.empty_like(bufs[0]) if x_out else None]
+            mr.layer_norm_forward(bufs[:W], g, b, want[0], residual=res, x_out=want[1])
+            ins, r = [t.clone() for t in bufs[:W]], None if res is None else res.clone()
+            # y over the first buffer, x over the residual; with one buffer x over it and y apart
+            got = [ins[0], r] if W > 1 else [torch.empty_like(ins[0]), ins[0]] if x_out else [ins[0], None]
+            mr.layer_norm_forward(ins, g, b, got[0], residual=r, x_out=got[1] if x_out else None)
+            assert all(torch.equal(p, q) for p, q in zip(want, got) if p is not None)
