@@ -86,7 +86,7 @@ struct AdamArgs {
   AdamState in, out;
   const float* clip;                        // {norm, factor, all finite} or null
   float b1, c1, b2, c2, eps, keep, lr_t, inv_sqrt_bc2;  // keep = 1 - lr*wd, lr_t = lr / (1 - b1^t)
-  float root_b2, root_c2;  // 8-bit moments: sqrt(b2), sqrt(c2) times 2^kAdamUp, and inv_sqrt_bc2 over it
+  float root_b2, root_c2;  // 8-bit moments: sqrt(b2), sqrt(c2) times 2^kAdamUp, with eps and lr_t times it too
 };
 constexpr int kAdamUp = 16;
 uint32_t adam_tile_elems(mr_dtype dt, mr_dtype gdt, mr_state_format fmt, bool master);

@@ -328,11 +328,11 @@ mr_status adamw_step(const void* const* params, const void* const* grads, const 
   a.c1 = static_cast<float>(1.0 - h->beta1);
   a.b2 = static_cast<float>(h->beta2);
   a.c2 = static_cast<float>(1.0 - h->beta2);
-  a.eps = static_cast<float>(h->eps);
-  a.keep = static_cast<float>(1.0 - h->lr * h->weight_decay);
-  a.lr_t = static_cast<float>(h->lr / (1.0 - std::pow(h->beta1, static_cast<double>(h->step))));
   const double up = mx ? std::ldexp(1.0, mr::kAdamUp) : 1.0;
-  a.inv_sqrt_bc2 = static_cast<float>(1.0 / (std::sqrt(1.0 - std::pow(h->beta2, static_cast<double>(h->step))) * up));
+  a.eps = static_cast<float>(h->eps * up);
+  a.keep = static_cast<float>(1.0 - h->lr * h->weight_decay);
+  a.lr_t = static_cast<float>(h->lr / (1.0 - std::pow(h->beta1, static_cast<double>(h->step))) * up);
+  a.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(h->beta2, static_cast<double>(h->step))));
   a.root_b2 = static_cast<float>(std::sqrt(h->beta2) * up);
   a.root_c2 = static_cast<float>(std::sqrt(1.0 - h->beta2) * up);
   const uint32_t tile = mr::adam_tile_elems(dtype, gdtype, fmt, master);

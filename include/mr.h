@@ -303,8 +303,8 @@ mr_status mr_grad_norm(const void* const* grads, const uint64_t* counts, int P, 
  *     moment.  The scale is the smallest that brings the block's largest magnitude to 448 or less (b = 255: not
  *     finite, the whole block reads as NaN).  Values are rounded to one of their two neighbours, up with
  *     probability (distance to the lower) / (spacing), by 16 bits of a hash of (seed, t, element): calls with the same
- *     arguments give the same bits.  A second moment that is not zero is never rounded to zero.  A state of zero bytes is
- *     the start.  The step itself uses m' and v' before they are rounded.  Gradients (times f) below 2^47 in magnitude; the
+ *     arguments give the same bits.  A second moment whose root is 2^-149 or more is never rounded to zero.  A state of zero
+ *     bytes is the start.  The step itself uses m' and v' before they are rounded.  Gradients (times f) below 2^47 in magnitude; the
  *     block of a larger one becomes not finite.
  * master: floats, or NULL.  With it, p is read from master and written to both; `params` is not read (and may be NULL
  *     if params_out is given).  Only for 16-bit parameters.

@@ -392,3 +392,37 @@ def test_offsets_past_32_bits():
     m = st.m[-64:].float() * torch.repeat_interleave(st.m_scale[-2:].float(), 32)
     tail = n % 32
     assert abs(float(m[32 + tail - 1]) / (0.1 * 2.0 ** -4) - 1) <= 1 / 8 and not bool(m[32 + tail:].any())
+
+
+@pytest.mark.parametrize("low,high", [(-133, -80), (-90, -60), (-149, -120)])
+def test_eight_bit_second_moments_of_the_smallest_sizes(low, high):
+    """Second moments far below fp32's squares: the root of a gradient of 2^low and more is kept, a zero gradient leaves it decayed, and
+    none becomes zero.  fp32 gradients below 2^-126 have fewer bits, which the tolerance of one E4M3 spacing covers."""
+    e = torch.arange(low, high)
+    g = torch.ldexp(torch.ones(len(e), dtype=torch.float64), e).float().repeat_interleave(32).to(device())
+    st = mr.adamw_init([g], 8)
+    p = torch.ones_like(g)
+    mr.adamw_step([p], [g], st, 0.125, 1, weight_decay=0.0, eps=1e-8, betas=(0.5, 0.75))
+
+    def root():
+        return st.v.cpu().double() * torch.exp2(st.v_scale.view(torch.uint8).cpu().double() - 127).repeat_interleave(32)
+
+    want = 0.5 * g.double().cpu()
+    # the smallest number of the format is 2^-9 * 2^-127: below it a root is raised to it
+    tol = torch.maximum(want / 8, torch.tensor(2.0 ** -136, dtype=torch.float64))
+    assert bool((root() > 0).all()) and bool(((root() - want).abs() <= tol).all())
+    before = root()
+    mr.adamw_step([p], [torch.zeros_like(g)], st, 0.125, 2, weight_decay=0.0, eps=1e-8, betas=(0.5, 0.75))
+    want = before * 0.75 ** 0.5
+    tol = torch.maximum(want / 8, torch.tensor(2.0 ** -136, dtype=torch.float64))
+    assert bool((root() > 0).all()) and bool(((root() - want).abs() <= tol).all())
+
+
+def test_eight_bit_step_without_eps_at_the_smallest_sizes():
+    """With eps = 0 the first step moves a parameter by lr at every gradient down to 2^-120: neither the second moment nor the
+    quotient leaves fp32's range on the way.  The tolerance is test_gradients_of_every_size's."""
+    e = torch.arange(-120, -60)
+    g = torch.ldexp(torch.ones(len(e), dtype=torch.float64), e).float().repeat_interleave(32).to(device())
+    p, st = torch.ones_like(g), mr.adamw_init([g], 8)
+    mr.adamw_step([p], [g], st, 0.125, 1, weight_decay=0.0, eps=0.0)
+    assert float((p.double() - 0.875).abs().max()) <= 24 * U * 0.125 + 2 * U
