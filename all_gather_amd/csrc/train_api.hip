@@ -96,7 +96,8 @@ mr_status check_norm(size_t rows, size_t cols, mr_dtype dtype, mr_dtype wdtype) 
 mr_status layer_norm_forward(const void* const* bufs, int W, const void* residual, const void* gamma, const void* beta,
                              size_t rows, size_t cols, mr_dtype dtype, mr_dtype wdtype, double eps, void* x_out, void* y,
                              float* mean, float* rstd, hipStream_t st) {
-  if (W < 1 || W > MR_MAX_W || !(eps >= 0.0) || !std::isfinite(eps)) return MR_ERR_INVALID_ARG;
+  const float eps32 = static_cast<float>(eps);
+  if (W < 1 || W > MR_MAX_W || !(eps >= 0.0) || !std::isfinite(eps32) || (eps > 0.0 && eps32 == 0.0f)) return MR_ERR_INVALID_ARG;
   const mr_status s = check_norm(rows, cols, dtype, wdtype);
   if (s != MR_OK) return s;
   if (rows == 0 || cols == 0) return MR_OK;
@@ -130,7 +131,7 @@ mr_status layer_norm_forward(const void* const* bufs, int W, const void* residua
   a.rstd = rstd;
   a.rows = rows;
   a.cols = cols;
-  a.eps = static_cast<float>(eps);
+  a.eps = eps32;
   if (mr::trace_on())
     std::fprintf(stderr, "[mr] layer_norm forward W=%d rows=%zu cols=%zu dtype=%d\n", W, rows, cols, static_cast<int>(dtype));
   const hipError_t e = mr::launch_norm_fwd(a, dtype, wdtype, st);
@@ -187,6 +188,7 @@ mr_status layer_norm_backward(const void* dy, const void* x, const void* gamma, 
 }
 
 constexpr uint64_t kMaxCount = uint64_t{1} << 33;  // elements of one tensor
+constexpr double kLeastEps = 0x1p-126;             // fp32's smallest normal number: the reciprocal takes smaller ones as zero
 constexpr uint32_t kMaxTiles = 1u << 23;           // tiles of one launch (256 lanes each, below 2^32 lanes)
 
 mr_status grad_norm(const void* const* grads, const uint64_t* counts, int P, mr_dtype dtype, double scale, double max_norm,
@@ -274,7 +276,7 @@ mr_status adamw_step(const void* const* params, const void* const* grads, const 
   if (s != MR_OK) return s;
   if (P < 0 || (fmt != MR_STATE_FP32 && fmt != MR_STATE_MXFP8) || !h) return MR_ERR_INVALID_ARG;
   if (!std::isfinite(h->lr) || !std::isfinite(h->weight_decay) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
-      !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps >= 0.0) || !std::isfinite(h->eps) || h->step < 1)
+      !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps == 0.0 || h->eps >= kLeastEps) || !std::isfinite(h->eps) || h->step < 1)
     return MR_ERR_INVALID_ARG;
   uint64_t total = 0;
   s = state_elems(counts, P, &total);

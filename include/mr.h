@@ -242,7 +242,7 @@ mr_status mr_allgather_param_contig_shards(const void* const* shards, int W, int
  *  x_out and y may each be one of the bufs or the residual exactly; any other overlap of an output with an
  *  input or another output -> MR_ERR_ALIAS.  Pointers are multiples of their element size (else
  *  MR_ERR_INVALID_ARG); rows need not start on any larger grid.  rows == 0 or cols == 0 is a no-op.
- *  cols < 2^31, eps finite and >= 0.  Infinities and NaN give what the formula gives, in their row only.
+ *  cols < 2^31, eps >= 0 and within fp32's range (0, or 2^-149 to 2^128).  Infinities and NaN give what the formula gives, in their row only.
  */
 mr_status mr_layer_norm_forward(const void* const* bufs, int W, const void* residual, const void* gamma, const void* beta,
                                 size_t rows, size_t cols, mr_dtype dtype, mr_dtype wdtype, double eps, void* x_out, void* y,
@@ -314,7 +314,7 @@ mr_status mr_grad_norm(const void* const* grads, const uint64_t* counts, int P, 
  *  state    host struct of device pointers, 256-byte aligned (scales: any).
  *  params_out, state_out  where results go; NULL: in place.  Each output may be its own input exactly; any
  *           other overlap -> MR_ERR_ALIAS.
- *  hyper    host struct; beta1, beta2 in [0, 1), eps >= 0, lr and weight_decay finite, t >= 1.
+ *  hyper    host struct; beta1, beta2 in [0, 1), eps 0 or at least 2^-126, lr, weight_decay and eps finite, t >= 1.
  *  clip     device, mr_grad_norm's 3 floats, or NULL.  Where clip[2] is 0 the step is not taken: outputs
  *           are the inputs (params_out the rounded master, with one).
  *  Up to 80 tensors go in one launch; counts[i] == 0 is allowed, counts[i] <= 2^33.

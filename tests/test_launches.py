@@ -142,3 +142,29 @@ def test_a_call_s_launches_stay_together_on_a_stream(fake, first, second):
 def test_streams_do_not_wait_for_one_another(fake):
     got = [x["stream"] for x in at_once(fake, "grad_norm", "backward", (0x50, 0x60))]
     assert sorted(got) == [0x50] * 3 + [0x60] * 2 and got != [0x50] * 3 + [0x60] * 2
+
+
+def adamw(L, eps, fmt=0):
+    h = mr._AdamWHyperC(1e-3, 0.9, 0.999, eps, 0.0, 1, 0)
+    st = mr._AdamWStateC(A[4], A[5], A[6] if fmt else None, A[7] if fmt else None, None)
+    return L.mr_adamw_step(ptrs(A[0]), ptrs(A[1]), counts(100), 1, FP32, FP32, fmt, ctypes.byref(st), None, None, ctypes.byref(h), None, None)
+
+
+def test_eps_outside_the_range_of_the_arithmetic(fake):
+    """AdamW divides by a number that is at least eps, with an instruction that takes subnormal numbers as zero; layer norm takes the
+    root of one.  An eps that is lost on the way would turn 0 / eps into NaN."""
+    for fmt in (0, 1):
+        for eps in (0.0, 2.0 ** -126, 1e-8, 1e30):
+            assert adamw(fake, eps, fmt) == 0, eps
+        for eps in (2.0 ** -127, 1e-39, 1e-45, 1e-300, 5e-324):
+            fake.fake_reset(0)
+            assert adamw(fake, eps, fmt) == -1 and fake.fake_launches() == 0, eps
+
+    def norm(eps):
+        return fake.mr_layer_norm_forward(ptrs(A[5]), 1, None, None, None, 4, 64, BF16, BF16, eps, None, A[0], None, None, None)
+
+    for eps in (0.0, 2.0 ** -149, 1e-40, 1e-5, 3e38):
+        assert norm(eps) == 0, eps
+    for eps in (2.0 ** -151, 1e-300, 5e-324, 1e39, 1e300):
+        fake.fake_reset(0)
+        assert norm(eps) == -1 and fake.fake_launches() == 0, eps
