@@ -564,6 +564,8 @@ def prepare_adamw(params: Sequence, grads: Sequence, state: AdamWState, params_o
     f = lib().mr_adamw_step
 
     def call(lr: float, step: int) -> None:
+        if not 0 < step < 1 << 64:
+            raise ValueError("step must count from 1")
         hyper.lr, hyper.step = lr, step
         st = f(*args)
         if st != MR_OK:

@@ -185,3 +185,48 @@ def test_refusals_under_asan_and_ubsan(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300, env=env)
     assert r.returncode == 0 and "c abi ok" in r.stdout, (r.stdout + r.stderr)[-3000:]
     shutil.rmtree(tmp_path, ignore_errors=True)
+
+
+class _OnDevice:
+    """What the binding reads of a device tensor."""
+
+    def __init__(self, n, dtype, at):
+        self.n, self.dtype, self.at, self.is_cuda = n, dtype, at, True
+
+    def numel(self):
+        return self.n
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.at
+
+
+def test_binding_refuses_steps_that_do_not_count_from_one(monkeypatch):
+    """A step of -1 would reach the library as 2^64 - 1, whose bias corrections are 1."""
+    import torch
+
+    calls, real = [], mr.lib()
+
+    class Library:
+        mr_adamw_state_elems = real.mr_adamw_state_elems
+
+        @staticmethod
+        def mr_adamw_step(*args):
+            calls.append(args)
+            return OK
+
+    class Stream:
+        cuda_stream = 0x50
+
+    monkeypatch.setattr(mr, "lib", lambda: Library)
+    t = [_OnDevice(32, torch.float32, a) for a in A[:4]]
+    call = mr.prepare_adamw([t[0]], [t[1]], mr.AdamWState(t[2], t[3]), stream=Stream())
+    call(1e-3, 1)
+    call(1e-3, 2 ** 64 - 1)
+    assert len(calls) == 2
+    for step in (0, -1, -2 ** 63, 2 ** 64, 2 ** 64 + 1):
+        with pytest.raises(ValueError):
+            call(1e-3, step)
+    assert len(calls) == 2
