@@ -262,8 +262,9 @@ mr_status mr_layer_norm_forward(const void* const* bufs, int W, const void* resi
  *  dres      device, rows*cols elements: the gradient that reaches x beside the norm; or NULL.
  *  dx        device, rows*cols elements, or NULL; may be dy, x or dres exactly.
  *  dgamma, dbeta  device, cols elements of `wdtype`, or NULL.  With rows == 0 they become zeros.
- *  Other overlaps, types and alignments as above.  Takes up to 16 MiB for cols <= 8192 (more for wider rows) of the
- *  stream's library workspace (see mr_set_workspace) for the weight gradients.
+ *  Other overlaps, types and alignments as above.  The weight gradients' partial sums take up to 2 KiB a column of the
+ *  stream's library workspace (see mr_set_workspace); one that the caller binds is large enough for any number of rows
+ *  with mr_workspace_bytes(1, 512 * max(cols, 32), MR_FP32) bytes.
  */
 mr_status mr_layer_norm_backward(const void* dy, const void* x, const void* gamma, const float* mean, const float* rstd,
                                  const void* dres, size_t rows, size_t cols, mr_dtype dtype, mr_dtype wdtype, void* dx,
@@ -282,7 +283,8 @@ mr_status mr_layer_norm_backward(const void* dy, const void* x, const void* gamm
  *          multiples of the element size; counts[i] == 0 allowed (its pointer is not read), and P == 0.
  *  scale   finite and > 0: e.g. 1 / the loss scale.  max_norm: finite.
  *  out     device, 3 floats; overlap with a gradient -> MR_ERR_ALIAS.
- *  Takes a few KiB of the stream's library workspace.
+ *  Takes 4 KiB of the stream's library workspace for every 128 tensors; one that the caller binds is large enough with
+ *  mr_workspace_bytes(1, 8 * P + 1024, MR_FP32) bytes.
  */
 mr_status mr_grad_norm(const void* const* grads, const uint64_t* counts, int P, mr_dtype dtype, double scale,
                        double max_norm, float* out, mr_stream stream);
@@ -361,7 +363,8 @@ mr_status mr_adamw_step(const void* const* params, const void* const* grads, con
  * Every launch returns its barrier words and flags to zero before it ends, also when a bounded wait
  * gave up (the call that timed out has invalid output; later calls are unaffected).
  *
- * mr_workspace_bytes: bytes a caller-owned workspace needs for a two-shot call of this shape.
+ * mr_workspace_bytes: bytes a caller-owned workspace needs for a two-shot call of this shape (and, as described there,
+ *                     for mr_layer_norm_backward and mr_grad_norm).
  * mr_set_workspace:   bind caller-owned device memory (256-byte aligned) as the workspace of `stream`
  *                     on the current device, replacing any library-owned one; the barrier words and
  *                     flags are cleared on `stream` here.  Memory too small to hold them plus some

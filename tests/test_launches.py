@@ -168,3 +168,32 @@ def test_eps_outside_the_range_of_the_arithmetic(fake):
     for eps in (2.0 ** -151, 1e-300, 5e-324, 1e39, 1e300):
         fake.fake_reset(0)
         assert norm(eps) == -1 and fake.fake_launches() == 0, eps
+
+
+@pytest.mark.parametrize("cols", [1, 7, 8, 31, 32, 100, 4096, 8192, 16384, 16385, 40000, 10 ** 6])
+def test_a_caller_s_workspace_of_the_documented_size(fake, cols):
+    """mr_workspace_bytes(1, 512 * max(cols, 32), MR_FP32) is enough for the backward pass of any number of rows."""
+    bytes_ = fake.mr_workspace_bytes(1, 512 * max(cols, 32), FP32)
+    assert fake.mr_set_workspace(0x70, A[8], bytes_) == 0
+    before = fake.fake_allocated()
+    for rows in (1, 255, 257, 3000, min(10 ** 6, 2 ** 37 // cols)):  # buffers lie 2^40 bytes apart
+        for dt in (BF16, FP32):
+            for parts in ({}, dict(dx=None)):
+                assert backward(fake, rows, cols, dt, stream=0x70, **parts) == 0, (rows, dt, parts)
+    assert fake.fake_allocated() == before
+    assert fake.mr_set_workspace(0x70, None, 0) == 0
+
+
+def test_a_caller_s_workspace_for_the_gradient_norm(fake):
+    for tensors in (0, 1, 128, 129, 5000):
+        g = [A[0] + (i << 24) for i in range(tensors)]
+        bytes_ = fake.mr_workspace_bytes(1, 8 * tensors + 1024, FP32)
+        assert fake.mr_set_workspace(0x70, A[8], bytes_) == 0
+        before = fake.fake_allocated()
+        assert fake.mr_grad_norm(ptrs(*g), counts(*[1 << 22] * tensors), tensors, FP32, 1.0, 1.0, A[7] + 4, 0x70) == 0
+        assert fake.fake_allocated() == before
+    small = fake.mr_workspace_bytes(1, 16, FP32)
+    assert fake.mr_set_workspace(0x70, A[8], small) == 0
+    assert fake.mr_grad_norm(ptrs(*g), counts(*[1 << 22] * 5000), 5000, FP32, 1.0, 1.0, A[7] + 4, 0x70) == -4
+    assert backward(fake, 3000, 4096, stream=0x70) == -4
+    assert fake.mr_set_workspace(0x70, None, 0) == 0
