@@ -197,3 +197,21 @@ def test_a_caller_s_workspace_for_the_gradient_norm(fake):
     assert fake.mr_grad_norm(ptrs(*g), counts(*[1 << 22] * 5000), 5000, FP32, 1.0, 1.0, A[7] + 4, 0x70) == -4
     assert backward(fake, 3000, 4096, stream=0x70) == -4
     assert fake.mr_set_workspace(0x70, None, 0) == 0
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("gdt", [BF16, FP32])
+def test_the_largest_lists_fit_the_device(fake, gdt, fmt):
+    """Tensors of up to 2^33 elements: a launch takes a tensor more than fills it, and still holds less than 2^32 lanes."""
+    c = [2 ** 33 - 1024, 2 ** 33, 5, 2 ** 32 + 1, 2 ** 33 - 2048 * 8, 2 ** 33]
+    at = [i << 36 for i in range(len(c))]
+    h = mr._AdamWHyperC(1e-3, 0.9, 0.999, 1e-8, 0.0, 1, 0)
+    st = mr._AdamWStateC(A[4], A[5], A[6] if fmt else None, A[7] if fmt else None, None)
+    fake.fake_reset(0)
+    assert fake.mr_adamw_step(ptrs(*[A[0] + a for a in at]), ptrs(*[A[2] + a for a in at]), counts(*c), len(c), gdt, gdt, fmt,
+                              ctypes.byref(st), None, None, ctypes.byref(h), None, None) == 0
+    got = launches(fake)
+    assert len(got) >= 2 and not any(x["refused"] for x in got)
+    fake.fake_reset(0)
+    assert fake.mr_grad_norm(ptrs(*[A[2] + a for a in at]), counts(*c), len(c), gdt, 1.0, 1.0, A[8], None) == 0
+    assert fake.fake_launches() >= 1 and not any(x["refused"] for x in launches(fake))
