@@ -184,7 +184,8 @@ def _prepared(name: str, f, args, keep):
 # Each prepare_* checks that every tensor is a contiguous device tensor of the sizes the call implies
 # (the library takes raw pointers and cannot check extents) and marshals the arguments once; the
 # returned no-argument callable enqueues that same call (tight timing loops, graph capture).  The
-# plain functions are one prepared call.
+# stream is marshalled too: without a ``stream`` it is the one that is current at preparation, not at
+# the call.  The plain functions are one prepared call.
 
 def prepare_allreduce(bufs: Sequence, out, mode: str = "oneshot", stream=None):
     """Pre-marshalled mr_allreduce_sum: out = elementwise fp32 sum (rank order) of the tensors ``bufs``."""
@@ -388,7 +389,7 @@ def _layer_norm_forward_args(bufs, gamma, beta, y, eps, residual, x_out, mean, r
 
 def prepare_layer_norm_forward(bufs: Sequence, gamma, beta, y, eps: float = 1e-5, residual=None, x_out=None, mean=None,
                                rstd=None, stream=None):
-    """Pre-marshalled mr_layer_norm_forward over the last dimension of ``y``."""
+    """Pre-marshalled mr_layer_norm_forward over the last dimension of ``y``, on ``stream`` or the one current now."""
     args = _layer_norm_forward_args(bufs, gamma, beta, y, eps, residual, x_out, mean, rstd, stream)
     return _prepared("mr_layer_norm_forward", lib().mr_layer_norm_forward, args,
                      (list(bufs), gamma, beta, y, residual, x_out, mean, rstd))
@@ -421,7 +422,7 @@ def _layer_norm_backward_args(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres,
 
 
 def prepare_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None, stream=None):
-    """Pre-marshalled mr_layer_norm_backward."""
+    """Pre-marshalled mr_layer_norm_backward, on ``stream`` or the one current now."""
     args = _layer_norm_backward_args(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres, stream)
     return _prepared("mr_layer_norm_backward", lib().mr_layer_norm_backward, args,
                      (dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres))
@@ -448,7 +449,8 @@ def _tensor_list(tensors, what: str, counts=None):
 
 
 def prepare_grad_norm(grads: Sequence, out, max_norm: float = 0.0, scale: float = 1.0, stream=None):
-    """Pre-marshalled mr_grad_norm."""
+    """Pre-marshalled mr_grad_norm for gradients that stay where they are, on ``stream`` or the one current now.  ``max_norm``
+    and ``scale`` are fixed with it: a loss scale that changes takes grad_norm, or another preparation."""
     grads = list(grads)
     _opt(out, "out", (_torch().float32,), 3)
     _dev_tensor(out, "out")
@@ -541,7 +543,9 @@ def _state_c(st: AdamWState, n: int) -> _AdamWStateC:
 def prepare_adamw(params: Sequence, grads: Sequence, state: AdamWState, params_out=None, state_out: AdamWState | None = None,
                   betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01, clip=None, seed: int = 0, stream=None):
     """Pre-marshalled mr_adamw_step for tensors that stay where they are: the returned ``call(lr, step)`` takes step
-    ``step`` (from 1).  Results go in place, or to ``params_out`` / ``state_out``."""
+    ``step`` (from 1), on ``stream`` or the one that is current at preparation.  Results go in place, or to ``params_out`` /
+    ``state_out``.  A HIP graph that captures the call repeats its ``lr`` and ``step``, and with them the bias corrections and
+    the 8-bit state's random bits: capture each step anew, or keep the call outside."""
     params, grads = list(params), list(grads)
     counts = [p.numel() for p in params]
     _, n = adamw_offsets(counts)

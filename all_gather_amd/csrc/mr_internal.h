@@ -33,7 +33,8 @@ struct Ctrl {
   uint32_t err[64];              // bit 0: a wait gave up after the spin limit (that call's output is not
                                  // valid); bits 1 and 2: the XCD-local two-shot recomputed units after a
                                  // wait gave up / whose producer ran on another XCD (output valid)
-  uint32_t arrived[9][64];       // gradient norm: workgroups that have written their sums, in 8 sets, and complete sets
+  uint32_t arrived[9][64];       // workgroups that have written their sums (gradient norm: in 8 sets, and complete
+                                 // sets; layer norm's backward pass of few rows: the first word)
 };
 static_assert(sizeof(Ctrl) <= kCtrlBytes, "ctrl layout");
 

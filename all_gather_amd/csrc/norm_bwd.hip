@@ -28,7 +28,8 @@ __device__ __forceinline__ void write_weight(const NormBwdArgs& a, size_t c, flo
 
 // Workgroup b of `groups` takes row sets b, b + groups, ...; a set is as many rows as the workgroup holds (one with more
 // than a pack a lane).  The next set's x and dy are loaded before this set's sums where registers allow; as in the
-// forward pass every full round issues the same loads and stores on every path.
+// forward pass every full round issues the same loads and stores on every path, and as built the waits count past the last
+// round's stores, but for fp16 rows without dres on one pack a lane, which wait for all of them at the loop's top.
 template <class T, class WT, int B, int K, bool Dres, int Lanes>
 __global__ __launch_bounds__(Lanes) void norm_bwd_row(NormBwdArgs a) {
   constexpr int kV = kPack<T>;

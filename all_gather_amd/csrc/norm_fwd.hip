@@ -31,6 +31,8 @@ __device__ __forceinline__ uint32_t group_of(uint32_t b, uint32_t n) {
 // count back on, so every full round issues the same ones on every path: lanes past the row's end store its last pack
 // once more, and the row's statistics collect in registers until a wave's lanes are full.  (With predicated stores a
 // round waited for the last one's stores to reach memory: 60003 x 1025 bf16 57.8 -> 54.5 us, its backward pass 92.6 -> 81.9.)
+// The waits are the compiler's.  As built, rows on whole waves with one pack a lane count past the last round's stores (fp32
+// rows, and 16-bit rows with weights of their type); the other single-input builds still wait for all of them at the loop's top.
 template <class T, class WT, int B, int K, bool Sum, int Lanes>
 __global__ __launch_bounds__(Lanes, K == 1 ? 8 : Lanes == 768 ? 3 : 4) void norm_fwd_row(NormFwdArgs a) {
   constexpr int kV = kPack<T>;

@@ -1,7 +1,7 @@
 // The norm of a list of gradients with its clip factor, and the AdamW step over a list of tensors, for gfx950.
 //
 // Both walk the tensors of one launch as one list of tiles: the kernel arguments hold the tensors' pointers
-// and a prefix of their tile counts, and a workgroup finds its tile's tensor with a scalar binary search.
+// and a prefix of their tile counts, and a workgroup finds its tile's tensor by comparing its number with the whole prefix.
 //
 //   norm    N = scale * sqrt(sum of all g^2), factor = scale * min(1, max_norm / (N + 1e-6))
 //   AdamW   g' = factor * g,  m' = b1*m + (1-b1)*g',  v' = b2*v + (1-b2)*g'^2,
@@ -176,7 +176,9 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
 }
 
 // 32 random bits for each of the elements idx .. idx + E - 1 of the flat state (idx a multiple of E): a Weyl step on the
-// key of (seed, step) and one multiply-xorshift round.
+// key of (seed, step) and one multiply-xorshift round.  The step is the prime next to 2^32 over the golden ratio (Knuth's
+// multiplicative hashing); the round's multiplier and shifts come from Wellons' published search for 32-bit mixers of low
+// bias, and the odd multiplier of the index's upper half from Collet's published hash constants.
 template <int E>
 __device__ __forceinline__ void random_bits(uint32_t key, uint64_t idx, uint32_t (&r)[E]) {
   const uint32_t first = key + static_cast<uint32_t>(idx) * 0x9E3779B1u + static_cast<uint32_t>(idx >> 32) * 0x85EBCA77u;

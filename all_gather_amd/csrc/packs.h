@@ -1,5 +1,5 @@
 // Packs of consecutive elements between memory and fp32 registers, and wave64 reductions, for the
-// training-step kernels (norm_kernels.hip, optim_kernels.hip).
+// training-step kernels (norm_fwd.hip, norm_bwd.hip, optim_kernels.hip).
 //
 // Rows and tensors of odd sizes start anywhere on the element grid, so a pack may start off its own
 // 16-byte grid.  Global memory on gfx950 takes multi-dword accesses at any byte address (the compiler's

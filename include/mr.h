@@ -320,6 +320,8 @@ mr_status mr_grad_norm(const void* const* grads, const uint64_t* counts, int P, 
  *  clip     device, mr_grad_norm's 3 floats, or NULL.  Where clip[2] is 0 the step is not taken: outputs
  *           are the inputs (params_out the rounded master, with one).
  *  Up to 80 tensors go in one launch; counts[i] == 0 is allowed, counts[i] <= 2^33.
+ *  hyper is read on the host: a HIP graph that captured the call repeats the same lr, t and seed at every replay, so its
+ *  bias corrections stand still and 8-bit moments meet the same random bits, whose roundings then no longer average out.
  */
 typedef enum mr_state_format { MR_STATE_FP32 = 0, MR_STATE_MXFP8 = 1 } mr_state_format;
 typedef struct mr_adamw_state {
