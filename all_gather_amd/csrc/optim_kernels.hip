@@ -15,10 +15,10 @@
 // (spacing) keeps the average.  A second moment that is not zero is never stored as zero, so that no later
 // step divides by eps alone.
 //
-// The norm and the 32-bit step are bound by the bytes they move: 537M bf16 gradients 154 us (6.9 TB/s, reads only), 134M
-// fp32 elements 623 to 654 us (5.7 to 6.0 TB/s over 4 read and 3 written streams, by where the buffers lie).  The 8-bit
-// step is near both bounds: 41 vector operations an element at 10.1 bytes, 28M bf16 elements 49.5 us (5.7 TB/s), 130M
-// 204 us (6.4 TB/s).
+// The norm and the 32-bit step are bound by the bytes they move: 537M bf16 gradients 155 us (6.9 TB/s, reads only), 134M
+// fp32 elements 617 to 654 us (5.7 to 6.1 TB/s over 4 read and 3 written streams, by where the buffers lie).  The 8-bit
+// step is near both bounds: 42 vector operations an element at 10.1 bytes, 28M bf16 elements 49.9 us (5.7 TB/s), 130M
+// 205 to 209 us (6.3 to 6.4 TB/s).
 
 #include <type_traits>
 
