@@ -351,7 +351,7 @@ mr_status mr_adamw_step(const void* const* params, const void* const* grads, con
  * mr_set_workspace on that stream.  One workspace per (device, stream): eager two-shot calls on
  * different streams never share barrier words.  The layer norm's backward pass and the gradient norm keep their partial
  * sums there too.  Calls on one stream from several host threads are safe: each enqueues its kernels together.
- * (hipStreamPerThread is one handle and a stream of each thread: use it from one thread only.)
+ * (hipStreamPerThread is one handle and a stream of each thread: make such calls on it from one thread only.)
  *
  * A two-shot call made while its stream is being captured into a HIP graph uses a library-owned
  * workspace of that capture (device, stream, capture id), allocated during the capture with this

@@ -108,12 +108,12 @@ CALLS = {"grad_norm": lambda L, st: grad_norm(L, 300, st), "backward": lambda L,
          "two_shot": two_shot}
 
 
-def at_once(L, first, second, streams):
+def at_once(L, first, second, streams, hold_ms=40):
     """The launches of two calls from two threads; the second call starts once the first's first kernel is launched, and every
-    launch keeps its thread for 40 ms."""
+    launch keeps its thread for hold_ms."""
     for name, st in zip((first, second), streams):  # workspaces are there
         assert CALLS[name](L, st) == 0
-    L.fake_reset(40)
+    L.fake_reset(hold_ms)
     status = []
     a = threading.Thread(target=lambda: status.append(CALLS[first](L, streams[0])))
     b = threading.Thread(target=lambda: status.append(CALLS[second](L, streams[1])))
@@ -140,7 +140,7 @@ def test_a_call_s_launches_stay_together_on_a_stream(fake, first, second):
 
 
 def test_streams_do_not_wait_for_one_another(fake):
-    got = [x["stream"] for x in at_once(fake, "grad_norm", "backward", (0x50, 0x60))]
+    got = [x["stream"] for x in at_once(fake, "grad_norm", "backward", (0x50, 0x60), 200)]
     assert sorted(got) == [0x50] * 3 + [0x60] * 2 and got != [0x50] * 3 + [0x60] * 2
 
 
