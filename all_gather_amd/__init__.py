@@ -1,5 +1,5 @@
 """Python binding of libmr, the MI355X W-way sum-reduce and param-contiguous gather library, with the operators of
-a training step around them (layer norm, gradient norm, AdamW).
+a training step around them (layer norm, losses on logits, gradient norm, AdamW).
 
 A thin ctypes layer over the C ABI declared in include/mr.h: it turns torch tensors into device
 pointers, sizes and the current HIP stream, calls the entry point of the same name and raises on a
@@ -48,6 +48,14 @@ class _AdamWHyperC(ctypes.Structure):
         ("step", ctypes.c_uint64), ("seed", ctypes.c_uint64)]
 
 
+class _PolicyHyperC(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("temperature", "clip_low", "clip_high", "kl_coef", "grad_scale")]
+
+
+class _PreferenceHyperC(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("beta", "smoothing", "loss_scale", "grad_scale")]
+
+
 # Exported symbols of include/mr.h, with ctypes signatures.
 _SIGS = {
     "mr_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -90,6 +98,14 @@ _SIGS = {
                                      ctypes.POINTER(ctypes.c_uint64)] + [ctypes.c_int] * 4 +
                       [ctypes.POINTER(_AdamWStateC), ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(_AdamWStateC),
                        ctypes.POINTER(_AdamWHyperC), ctypes.c_void_p, ctypes.c_void_p]),
+    "mr_token_logprob_forward": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_size_t] * 3 + [ctypes.c_int, ctypes.c_void_p,
+                                                ctypes.c_double] + [ctypes.c_void_p] * 3),
+    "mr_token_logprob_backward": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_size_t] * 3 + [ctypes.c_int, ctypes.c_void_p,
+                                                 ctypes.c_double] + [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "mr_policy_loss": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_size_t] * 3 + [ctypes.c_int] + [ctypes.c_void_p] * 5 +
+                       [ctypes.POINTER(_PolicyHyperC)] + [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "mr_preference_loss": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_size_t, ctypes.c_void_p, ctypes.c_size_t,
+                                          ctypes.POINTER(_PreferenceHyperC)] + [ctypes.c_void_p] * 4),
     "mr_set_option": (ctypes.c_int, [ctypes.c_int, ctypes.c_int64]),
     "mr_get_option": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_int64)]),
 }
@@ -434,6 +450,99 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, d
     _check(lib().mr_layer_norm_backward(*_layer_norm_backward_args(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dres, stream)),
            "mr_layer_norm_backward")
     return dx
+
+
+def _rows2d(t, what: str, ref=None):
+    """(rows, cols, row stride) of logits: any contiguous tensor, or a matrix of contiguous rows, like ``ref`` if given."""
+    if not t.is_cuda or (ref is not None and (t.dtype != ref.dtype or t.shape != ref.shape)):
+        raise ValueError(f"{what} must be a device tensor" + (f" of {ref.dtype}, shaped like the logits" if ref is not None else ""))
+    cols = t.shape[-1] if t.dim() else 1
+    rows = t.numel() // cols if cols else (t.shape[0] if t.dim() > 1 else 0)
+    if t.is_contiguous() or rows <= 1 and (cols <= 1 or t.stride(-1) == 1):
+        return rows, cols, cols
+    if t.dim() == 2 and (t.stride(1) == 1 or cols == 1) and t.stride(0) >= cols:
+        return rows, cols, t.stride(0)
+    raise ValueError(f"{what} must be contiguous, or a matrix whose rows are")
+
+
+def _targets(t, rows: int):
+    return _need(t, "targets", _torch().int64, rows)
+
+
+def _need(t, what: str, dtype, numel: int):
+    if t is None or not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() == numel):
+        raise ValueError(f"{what} must be a contiguous device tensor of {numel} elements of {dtype}")
+    return t.data_ptr()
+
+
+def token_logprob_forward(logits, targets, logp, stats=None, temperature: float = 1.0, stream=None):
+    """logp[i] = the log-probability of token ``targets[i]`` (int64) under row i of ``logits`` / ``temperature``, in fp32; 0 where
+    the target lies outside the vocabulary (-100: prompts, padding).  ``stats`` (fp32, two per row) receives what
+    token_logprob_backward takes.  ``logits``: bf16, fp16 or fp32, contiguous, or a matrix whose rows are (logits[:, :vocab])."""
+    rows, cols, stride = _rows2d(logits, "logits")
+    f32 = (_torch().float32,)
+    _check(lib().mr_token_logprob_forward(logits.data_ptr(), rows, cols, stride, DTYPE_CODE[dtype_name(logits)], _targets(targets, rows),
+                                          temperature, _opt(logp, "logp", f32, rows), _opt(stats, "stats", f32, 2 * rows),
+                                          _stream_handle(stream)), "mr_token_logprob_forward")
+    return logp
+
+
+def token_logprob_backward(logits, targets, stats, dlogp, dlogits, temperature: float = 1.0, stream=None):
+    """dlogits = the gradient of the logits, where ``dlogp`` (fp32, one per row) is that of token_logprob_forward's logp.
+    ``dlogits`` is shaped like the logits, and may be them."""
+    rows, cols, stride = _rows2d(logits, "logits")
+    _, _, dstride = _rows2d(dlogits, "dlogits", logits)
+    f32 = _torch().float32
+    _check(lib().mr_token_logprob_backward(logits.data_ptr(), rows, cols, stride, DTYPE_CODE[dtype_name(logits)],
+                                           _targets(targets, rows), temperature, _need(stats, "stats", f32, 2 * rows),
+                                           _need(dlogp, "dlogp", f32, rows), dlogits.data_ptr(), dstride, _stream_handle(stream)),
+           "mr_token_logprob_backward")
+    return dlogits
+
+
+def policy_loss(logits, targets, advantages, record, old_logp=None, ref_logp=None, weights=None, logp=None, dlogits=None,
+                clip=(0.2, 0.2), kl: float = 0.0, temperature: float = 1.0, grad_scale: float = 1.0, stream=None):
+    """The clipped policy loss with a KL term, and its gradient, in one pass over the logits.
+
+    Each token's loss is max(-A r, -A min(max(r, 1 - clip[0]), 1 + clip[1])) + kl * (exp(d) - d - 1), where r = exp(logp - old_logp)
+    and d = ref_logp - logp (old_logp None: r = 1; ref_logp None: no KL term).  ``record`` (4 floats) receives the sums over the
+    tokens of weight * loss, weight * (exp(d) - d - 1), weight * [clipped], and weight; ``weights`` None stands for ones, and rows of
+    weight 0 or a target outside the vocabulary are left out.  ``dlogits`` (the logits themselves, or shaped like them), if given,
+    receives the gradient of grad_scale * record[0]; ``logp`` the tokens' log-probabilities.  advantages, old_logp, ref_logp,
+    weights, logp: fp32, one per row."""
+    rows, cols, stride = _rows2d(logits, "logits")
+    f32 = _torch().float32
+    some = (f32,)
+    dstride = 0 if dlogits is None else _rows2d(dlogits, "dlogits", logits)[2]
+    hyper = _PolicyHyperC(temperature, clip[0], clip[1], kl, grad_scale)
+    _check(lib().mr_policy_loss(logits.data_ptr(), rows, cols, stride, DTYPE_CODE[dtype_name(logits)], _targets(targets, rows),
+                                _opt(old_logp, "old_logp", some, rows), _opt(ref_logp, "ref_logp", some, rows),
+                                _need(advantages, "advantages", f32, rows), _opt(weights, "weights", some, rows), ctypes.byref(hyper),
+                                _need(record, "record", f32, 4), _opt(logp, "logp", some, rows),
+                                None if dlogits is None else dlogits.data_ptr(), dstride, _stream_handle(stream)), "mr_policy_loss")
+    return record
+
+
+def preference_loss(logp, offsets, record, ref_logp=None, margins=None, dlogp=None, beta: float = 0.1, smoothing: float = 0.0,
+                    loss_scale: float | None = None, grad_scale: float = 1.0, stream=None):
+    """The preference loss over pairs of sequences, from their tokens' log-probabilities, and its gradient.
+
+    ``offsets`` (int64, 2 * pairs + 1, not decreasing): rows offsets[k] to offsets[k+1] are sequence k; pair p's chosen sequence
+    is 2p and its rejected one 2p + 1.  With s the sum of logp - ref_logp over a sequence (ref_logp None: 0) and h = beta * (s_chosen -
+    s_rejected), a pair's loss is -(1 - smoothing) ln sigmoid(h) - smoothing ln sigmoid(-h).  ``record`` (3 floats) receives
+    loss_scale (None: 1 / pairs) * the sum of the losses, the share of h > 0 and the mean of h; ``margins`` every h; ``dlogp`` (or
+    logp itself) the gradient of grad_scale * record[0]."""
+    f32 = _torch().float32
+    rows, n = logp.numel(), offsets.numel()
+    if n % 2 == 0:
+        raise ValueError("offsets must hold 2 * pairs + 1 elements")
+    pairs = n // 2
+    hyper = _PreferenceHyperC(beta, smoothing, (1.0 / pairs if pairs else 1.0) if loss_scale is None else loss_scale, grad_scale)
+    _check(lib().mr_preference_loss(_need(logp, "logp", f32, rows), _opt(ref_logp, "ref_logp", (f32,), rows), rows,
+                                    _need(offsets, "offsets", _torch().int64, n), pairs, ctypes.byref(hyper), _need(record, "record", f32, 3),
+                                    _opt(margins, "margins", (f32,), pairs), _opt(dlogp, "dlogp", (f32,), rows), _stream_handle(stream)),
+           "mr_preference_loss")
+    return record
 
 
 def _tensor_list(tensors, what: str, counts=None):

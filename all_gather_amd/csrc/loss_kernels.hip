@@ -1,0 +1,635 @@
+// Losses on logits for gfx950: log-probabilities of target tokens, their backward pass, the clipped policy loss with a
+// KL term, and the preference loss over pairs of sequences.
+//
+//   m = max z,  S = sum exp((z - m) / T),  logp = (z_t - m) / T - ln S,   d logp / d z_j = ([j = t] - exp((z_j - m) / T) / S) / T
+//
+// Row statistics are taken online, in one pass: a lane keeps the maximum and the sum of what it has seen, and scales the sum
+// down where the maximum rises.  Exponents are (z - m) * log2(e)/T, not z * log2(e)/T - m * log2(e)/T: the difference is
+// exact near the maximum, and a row whose every element is the type's lowest value stays a uniform distribution.
+//
+// The policy loss's gradient needs nothing but its own row, so a row that fits the registers of a workgroup is read once
+// and its gradient written straight from them (policy_held).  Longer rows, and calls of too few rows to fill the device, go over
+// the logits twice: row_stats, whose workgroups may share a row, and logit_grad.
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+
+#include "mr_train.h"
+#include "packs.h"
+
+namespace mr {
+namespace {
+
+constexpr float kNone = -__builtin_huge_valf();
+
+// Running maximum and sum of exp2((z - maximum) * c).
+struct Stat {
+  float m, s;
+};
+// What exponents are taken against: a row of -inf alone has sum 0, not NaN.
+__device__ __forceinline__ float base_of(float m) { return m == kNone ? 0.0f : m; }
+__device__ __forceinline__ float power(float z, float base, float c) { return __builtin_amdgcn_exp2f((z - base) * c); }
+
+template <int N>
+__device__ __forceinline__ void add_values(Stat& a, const float (&f)[N], float c) {
+  float m = a.m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmaxf(m, f[i]);
+  const float base = base_of(m);
+  float s0 = a.s * power(a.m, base, c), s1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    s0 += power(f[i], base, c);
+    s1 += power(f[i + 1], base, c);
+  }
+  a.m = m;
+  a.s = s0 + s1;
+}
+__device__ __forceinline__ Stat joined(const Stat& a, const Stat& b, float c) {
+  Stat r;
+  r.m = fmaxf(a.m, b.m);
+  const float base = base_of(r.m);
+  r.s = a.s * power(a.m, base, c) + b.s * power(b.m, base, c);
+  return r;
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+  x = fmaxf(x, dpp<0xB1>(x));   // quad lanes 1 0 3 2
+  x = fmaxf(x, dpp<0x4E>(x));   // quad lanes 2 3 0 1
+  x = fmaxf(x, dpp<0x141>(x));  // half row mirrored
+  x = fmaxf(x, dpp<0x140>(x));  // row mirrored
+  const int b = __float_as_int(x);
+  return fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 0)), __int_as_float(__builtin_amdgcn_readlane(b, 16))),
+               fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 32)), __int_as_float(__builtin_amdgcn_readlane(b, 48))));
+}
+__device__ __forceinline__ Stat wave_join(Stat a, float c) {
+  const float m = wave_max(a.m);
+  a.s = lanes_sum<64>(a.s * power(a.m, base_of(m), c));
+  a.m = m;
+  return a;
+}
+
+// ln S without the rounding of a large logarithm: S = f * 2^e with f around 1, so that ln 1 is 0.
+__device__ __forceinline__ double ln(float S) {
+  int e;
+  float f = frexpf(S, &e);
+  if (f < 0.70710678f) f *= 2.0f, e -= 1;
+  return static_cast<double>(e) * 0.6931471805599453 + static_cast<double>(logf(f));
+}
+__device__ __forceinline__ double logp_of(const LogitArgs& a, float m, float S, float zt) {
+  return (static_cast<double>(zt) - static_cast<double>(m)) * a.inv_temp - ln(S);
+}
+
+// A row that carries a loss: its target is one of the columns, and its weight is not zero.
+// (The same for every lane: read into scalar registers, so that rows' addresses are too.)
+__device__ __forceinline__ bool row_live(const LogitArgs& a, size_t row, uint32_t* t) {
+  const uint64_t x = static_cast<uint64_t>(a.targets[row]);
+  *t = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+  const uint32_t high = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
+  uint32_t weight = 1;
+  if (a.weights) weight = __builtin_amdgcn_readfirstlane(__float_as_uint(a.weights[row])) << 1;
+  return high == 0 && *t < static_cast<uint32_t>(a.cols) && weight != 0;
+}
+
+// exp(d) - d - 1, without the cancellation of its leading terms where d is small: there its power series, whose first
+// term left out, d^11 / 11!, is below 2^-24 of the sum for |d| <= 1.
+__device__ __forceinline__ float excess(float d) {
+  if (fabsf(d) > 1.0f) return expm1f(d) - d;
+  float p = 1.0f + d * (1.0f / 10.0f);
+#pragma unroll
+  for (int n = 9; n >= 3; --n) p = 1.0f + d * p * (1.0f / static_cast<float>(n));
+  return 0.5f * d * d * p;
+}
+
+// The policy loss of one row: the gradient of its log-probability (grad_scale in it), and its terms of the record.
+struct PolicyRow {
+  float g;
+  double loss, kl, held, w;
+};
+__device__ __forceinline__ PolicyRow policy_row(const LogitArgs& a, size_t row, double logp) {
+  const double w = a.weights ? static_cast<double>(a.weights[row]) : 1.0;
+  const double adv = static_cast<double>(a.adv[row]);
+  const double r = a.old_logp ? static_cast<double>(expf(static_cast<float>(logp - static_cast<double>(a.old_logp[row])))) : logp - logp + 1.0;
+  double near = r < 1.0 - a.clip_lo ? 1.0 - a.clip_lo : r;
+  near = near > 1.0 + a.clip_hi ? 1.0 + a.clip_hi : near;
+  const double free = -adv * r, held = -adv * near;
+  const bool cut = held > free;
+  PolicyRow p;
+  double g = cut ? 0.0 : free, k = 0.0;
+  if (a.ref_logp) {
+    const float d = static_cast<float>(static_cast<double>(a.ref_logp[row]) - logp);
+    g -= a.kl * static_cast<double>(expm1f(d));
+    k = static_cast<double>(excess(d));
+  }
+  p.g = static_cast<float>(a.grad_scale * w * g);
+  p.loss = w * ((cut ? held : free) + a.kl * k);
+  p.kl = w * k;
+  p.held = cut ? w : 0.0;
+  p.w = w;
+  return p;
+}
+
+// Workgroups' sums to the record: each leaves four through write-through stores, acknowledged before its arrival is counted,
+// and the one that arrives last adds them all up in their order.  Every lane of the workgroup calls this.
+__device__ __forceinline__ bool arrive_last(uint32_t (*arrived)[64], uint32_t groups) {
+  __shared__ bool last;
+  if (threadIdx.x == 0) {
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    const uint32_t sets = groups < 4 * kNormSets ? 1 : kNormSets, set = blockIdx.x % sets;
+    const uint32_t members = (groups - set + sets - 1) / sets;
+    last = __hip_atomic_fetch_add(&arrived[set][0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == members - 1;
+    if (last && sets > 1)
+      last = __hip_atomic_fetch_add(&arrived[kNormSets][0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == sets - 1;
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  }
+  __syncthreads();
+  return last;
+}
+// The first wave's sum over all workgroups of their four values; lane 0 to 3 has one each.
+__device__ __forceinline__ double total_of(const double* sums, uint32_t groups) {
+  const uint32_t j = threadIdx.x & 3;
+  double s = 0.0;
+  for (uint32_t i = threadIdx.x >> 2; i < groups; i += 16)
+    s += __hip_atomic_load(sums + size_t{i} * 4 + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int m = 32; m >= 4; m >>= 1) s += __shfl_xor(s, m);
+  return s;
+}
+__device__ __forceinline__ void finish_record(double v0, double v1, double v2, double v3, double* sums, uint32_t (*arrived)[64],
+                                              uint32_t groups, float* record, int words) {
+  if (threadIdx.x == 0) {
+    double* p = sums + size_t{blockIdx.x} * 4;
+    __hip_atomic_store(p, v0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(p + 1, v1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(p + 2, v2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(p + 3, v3, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (!arrive_last(arrived, groups) || threadIdx.x >= 64) return;
+  const double s = total_of(sums, groups);
+  if (threadIdx.x <= kNormSets) __hip_atomic_store(&arrived[threadIdx.x][0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (static_cast<int>(threadIdx.x) < words) record[threadIdx.x] = static_cast<float>(s);
+}
+
+constexpr int kMostWaves = 16;
+
+// --------------------------------------------------------------------------------- statistics of rows
+//
+// A workgroup takes one of `splits` parts of a row.  The parts' maxima and sums are joined, in their order, by the workgroup
+// that finishes its row last.  Bound by the reads.
+constexpr int kStatPacks = 4;  // packs a lane has in flight
+
+template <class T, bool Policy>
+__global__ __launch_bounds__(1024) void row_stats(LogitArgs a) {
+  constexpr int V = 16 / T::kSize;
+  __shared__ Stat waves[kMostWaves];
+  __shared__ float shared_zt;
+  __shared__ bool last;
+  const uint32_t lanes = blockDim.x, lane = threadIdx.x;
+  const size_t parts = a.rows * a.splits;
+  const size_t packs = (a.cols + V - 1) / V, per = (packs + a.splits - 1) / a.splits;
+  double loss = 0.0, kl = 0.0, cut = 0.0, weight = 0.0;
+  for (size_t part = blockIdx.x; part < parts; part += gridDim.x) {
+    const size_t row = part / a.splits;
+    const uint32_t split = static_cast<uint32_t>(part % a.splits);
+    uint32_t t;
+    if (!row_live(a, row, &t)) {  // the same for every lane, and for every part of the row
+      if (lane == 0 && split == 0) {
+        if (a.logp) a.logp[row] = 0.0f;
+        if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
+        if (Policy && a.dz) const_cast<float*>(a.dlogp)[row] = 0.0f;
+      }
+      continue;
+    }
+    const char* z = a.z + row * a.stride * T::kSize;
+    const size_t first = split * per, end = first + per < packs ? first + per : packs;
+    Stat st{kNone, 0.0f};
+    for (size_t p = first + lane; p < end; p += static_cast<size_t>(lanes) * kStatPacks) {
+      float f[kStatPacks * V];
+      Raw<T, V> raw[kStatPacks];
+      if (p + static_cast<size_t>(lanes) * (kStatPacks - 1) < end && (p + static_cast<size_t>(lanes) * (kStatPacks - 1) + 1) * V <= a.cols) {
+#pragma unroll
+        for (int k = 0; k < kStatPacks; ++k) raw[k] = load_raw<T, V, true>(z + (p + static_cast<size_t>(lanes) * k) * V * T::kSize);
+#pragma unroll
+        for (int k = 0; k < kStatPacks; ++k) widen(raw[k], reinterpret_cast<float(&)[V]>(f[k * V]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < kStatPacks; ++k) {
+          const size_t q = p + static_cast<size_t>(lanes) * k;
+          const int n = q >= end ? 0 : a.cols - q * V < V ? static_cast<int>(a.cols - q * V) : V;
+          float (&g)[V] = reinterpret_cast<float(&)[V]>(f[k * V]);
+          widen(load_part<T, V, true>(z + q * V * T::kSize, n), g);
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (i >= n) g[i] = kNone;
+        }
+      }
+      add_values(st, f, a.c);
+    }
+    st = wave_join(st, a.c);
+    __syncthreads();  // the last row's words have been read
+    if ((lane & 63) == 0) waves[lane >> 6] = st;
+    if (lane == 0) shared_zt = load1<T>(z + static_cast<size_t>(t) * T::kSize);
+    __syncthreads();
+    if (lane >= 64) {
+      if (a.splits == 1) continue;
+    } else {
+      st = waves[0];
+      for (uint32_t w = 1; w < lanes / 64; ++w) st = joined(st, waves[w], a.c);
+    }
+    if (a.splits > 1) {
+      if (lane == 0) {
+        float* at = a.part + part * 2;
+        __hip_atomic_store(at, st.m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(at + 1, st.s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        last = __hip_atomic_fetch_add(a.row_arrived + row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.splits - 1;
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        if (last) __hip_atomic_store(a.row_arrived + row, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
+      if (!last || lane >= 64) continue;
+      Stat mine{kNone, 0.0f};
+      if (lane < a.splits) {
+        const float* at = a.part + (row * a.splits + lane) * 2;
+        mine.m = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        mine.s = __hip_atomic_load(at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      st = wave_join(mine, a.c);
+    }
+    const double lp = logp_of(a, st.m, st.s, shared_zt);
+    if (lane == 0) {
+      if (a.logp) a.logp[row] = static_cast<float>(lp);
+      if (a.stats) {
+        a.stats[2 * row] = st.m;
+        a.stats[2 * row + 1] = st.s;
+      }
+      if constexpr (Policy) {
+        const PolicyRow p = policy_row(a, row, lp);
+        if (a.dz) const_cast<float*>(a.dlogp)[row] = p.g;
+        loss += p.loss, kl += p.kl, cut += p.held, weight += p.w;
+      }
+    }
+  }
+  if constexpr (Policy) finish_record(loss, kl, cut, weight, a.sums, a.arrived, gridDim.x, a.record, 4);
+}
+
+// ------------------------------------------------------------------------------ gradient of the logits
+//
+// dz_j = g/T ([j = t] - exp((z_j - m) / T) / S), element by element; a workgroup takes a run of packs of one row.
+constexpr int kGradPacks = 4;
+
+template <class T>
+__global__ __launch_bounds__(256) void logit_grad(LogitArgs a) {
+  constexpr int V = 16 / T::kSize;
+  const uint32_t lanes = blockDim.x, lane = threadIdx.x;
+  const size_t packs = (a.cols + V - 1) / V, run = static_cast<size_t>(lanes) * kGradPacks;
+  const size_t runs = (packs + run - 1) / run;
+  for (size_t item = blockIdx.x; item < a.rows * runs; item += gridDim.x) {
+    const size_t row = item / runs, p0 = item % runs * run + lane;
+    uint32_t t;
+    const bool live = row_live(a, row, &t);  // (the backward pass has no weights)
+    const char* z = a.z + row * a.stride * T::kSize;
+    char* dz = a.dz + row * a.dstride * T::kSize;
+    const bool whole = (p0 - lane + run) * V <= a.cols;
+    if (!live) {
+      const float none[V] = {};
+#pragma unroll
+      for (int k = 0; k < kGradPacks; ++k) {
+        const size_t q = p0 + static_cast<size_t>(lanes) * k;
+        const int n = whole ? V : q >= packs ? 0 : a.cols - q * V < V ? static_cast<int>(a.cols - q * V) : V;
+        if (n) store_part<T, V, true>(dz + q * V * T::kSize, none, n);
+      }
+      continue;
+    }
+    Raw<T, V> raw[kGradPacks];
+#pragma unroll
+    for (int k = 0; k < kGradPacks; ++k) {
+      const size_t q = p0 + static_cast<size_t>(lanes) * k;
+      if (whole)
+        raw[k] = load_raw<T, V, true>(z + q * V * T::kSize);
+      else if (q < packs)
+        raw[k] = load_part<T, V, true>(z + q * V * T::kSize, a.cols - q * V < V ? static_cast<int>(a.cols - q * V) : V);
+    }
+    const float base = base_of(a.stats[2 * row]), g = static_cast<float>(static_cast<double>(a.dlogp[row]) * a.inv_temp);
+    const float share = -g / a.stats[2 * row + 1];
+#pragma unroll
+    for (int k = 0; k < kGradPacks; ++k) {
+      const size_t q = p0 + static_cast<size_t>(lanes) * k;
+      if (!whole && q >= packs) continue;
+      float f[V];
+      widen(raw[k], f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = share * power(f[i], base, a.c);
+      const uint64_t at = static_cast<uint64_t>(t) - q * V;
+      if (at < V) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (at == static_cast<uint64_t>(i)) f[i] += g;
+      }
+      if (whole)
+        store_raw<T, V, true>(dz + q * V * T::kSize, narrow<T, V>(f));
+      else
+        store_part<T, V, true>(dz + q * V * T::kSize, f, a.cols - q * V < V ? static_cast<int>(a.cols - q * V) : V);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------- the policy loss in one pass
+//
+// A workgroup holds a row in registers, K packs a lane, and walks the rows.  As each pack's gradient leaves, the next row's
+// pack is loaded into its place, so that reads and writes flow together.  One barrier a row: its words are of alternating
+// sets.  Only the last two of the K strips of packs can pass the row's end (held_row).  Its last pack, if short, is read as the
+// row's last V elements (the first `lo` of which the neighbouring pack has too, so they add nothing to the sums; both store
+// the same bits), and packs past the end are read, and stored, as that one.
+template <class T, int K>
+__global__ __launch_bounds__(1024) void policy_held(LogitArgs a) {
+  constexpr int V = 16 / T::kSize, kEnd = K < 2 ? K : 2;
+  __shared__ Stat words[2][kMostWaves];
+  __shared__ double sums[4];  // the first lane's
+  const uint32_t lanes = blockDim.x, lane = threadIdx.x, nw = lanes / 64;
+  const uint32_t cols = static_cast<uint32_t>(a.cols);
+  uint32_t end_at[kEnd];  // the last strips' columns
+  int end_lo[kEnd];
+#pragma unroll
+  for (int i = 0; i < kEnd; ++i) {
+    const uint32_t col = ((K - kEnd + i) * lanes + lane) * V;
+    end_at[i] = col < cols - V ? col : cols - V;
+    end_lo[i] = static_cast<int>(col - end_at[i] < V ? col - end_at[i] : V);
+  }
+  // a lane's column in strip k, as a part of all lanes and its own: the first rides in scalar registers
+  auto strip = [&](int k) { return k < K - kEnd ? k * lanes * V : 0u; };
+  auto own = [&](int k) { return k < K - kEnd ? lane * V : end_at[k - (K - kEnd)]; };
+  if (lane == 0) sums[0] = sums[1] = sums[2] = sums[3] = 0.0;
+  Raw<T, V> raw[K];
+  // A row's packs; where there is no row to load, every lane reads one pack of this one.  Loads behind a branch would keep the
+  // packs that leave and those that come in registers of their own.
+  auto load = [&](const char* z, uint32_t some, int k) {
+    raw[k] = load_raw<T, V, true>(z + (size_t{strip(k)} & static_cast<int32_t>(some)) * T::kSize + (own(k) & some) * T::kSize);
+  };
+  const size_t step = gridDim.x;
+  uint32_t t_next = 0;
+  // The first row at or after r that carries a loss; those before it get their zeros.
+  auto advance = [&](size_t r) {
+    for (; r < a.rows && !row_live(a, r, &t_next); r += step) {
+      char* dz = a.dz + r * a.dstride * T::kSize;
+      if (lane == 0 && a.logp) a.logp[r] = 0.0f;
+      const float none[V] = {};
+#pragma unroll
+      for (int k = 0; k < K; ++k) store_raw<T, V, true>(dz + size_t{strip(k)} * T::kSize + own(k) * T::kSize, narrow<T, V>(none));
+    }
+    return r;
+  };
+  size_t row = advance(blockIdx.x), next = row;
+  uint32_t t = t_next;
+  float zt = 0.0f;
+  if (row < a.rows) zt = load1<T>(a.z + (row * a.stride + t) * T::kSize);
+#pragma unroll
+  for (int k = 0; k < K; ++k) load(a.z + (row < a.rows ? row : 0) * a.stride * T::kSize, row < a.rows ? ~0u : 0u, k);
+  for (uint32_t turn = 0; row < a.rows; row = next, ++turn) {
+    next = advance(row + step);
+    const uint32_t some = next < a.rows ? ~0u : 0u;
+    const char* z_next = a.z + (some ? next : row) * a.stride * T::kSize;
+    float zt_next = 0.0f;
+    if (some) zt_next = load1<T>(z_next + static_cast<size_t>(t_next) * T::kSize);
+    char* dz = a.dz + row * a.dstride * T::kSize;
+    Stat st{kNone, 0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      // packs in turn: their values are not held beside one another
+#pragma unroll
+      for (int i = 0; i < Raw<T, V>::kWords; ++i) asm volatile("" : "+v"(raw[k].w[i]), "+v"(st.m), "+v"(st.s));
+      float f[V];
+      widen(raw[k], f);
+      if (k >= K - kEnd) {
+        int lo = end_lo[k >= K - kEnd ? k - (K - kEnd) : 0];
+        asm volatile("" : "+v"(lo));  // compared anew: kept, the comparisons' masks would take 16 scalar registers a strip
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i < lo) f[i] = kNone;
+      }
+      add_values(st, f, a.c);
+    }
+    st = wave_join(st, a.c);
+    if ((lane & 63) == 0) words[turn & 1][lane >> 6] = st;
+    __syncthreads();
+    st = words[turn & 1][0];
+    for (uint32_t i = 1; i < nw; ++i) st = joined(st, words[turn & 1][i], a.c);
+    const double lp = logp_of(a, st.m, st.s, zt);
+    const PolicyRow p = policy_row(a, row, lp);
+    if (lane == 0) {
+      if (a.logp) a.logp[row] = static_cast<float>(lp);
+      sums[0] += p.loss, sums[1] += p.kl, sums[2] += p.held, sums[3] += p.w;
+    }
+    const float base = base_of(st.m), g = static_cast<float>(static_cast<double>(p.g) * a.inv_temp), share = -g / st.s;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      // widened anew: kept from the sums, the values would take twice the registers that hold the row
+#pragma unroll
+      for (int i = 0; i < Raw<T, V>::kWords; ++i) asm volatile("" : "+v"(raw[k].w[i]));
+      float f[V];
+      widen(raw[k], f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = share * power(f[i], base, a.c);
+      store_raw<T, V, true>(dz + size_t{strip(k)} * T::kSize + own(k) * T::kSize, narrow<T, V>(f));
+      load(z_next, some, k);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // The target's own element, by every lane that stored a pack with it, after that pack: one of them writes it last.
+    const uint32_t q = t / V;
+    bool mine = K > kEnd && q < (K - kEnd) * lanes && q % lanes == lane;
+#pragma unroll
+    for (int i = 0; i < kEnd; ++i) mine = mine || t - end_at[i] < V;
+    if (mine) store1<T>(dz + size_t{t} * T::kSize, share * power(zt, base, a.c) + g);
+    t = t_next;
+    zt = zt_next;
+  }
+  finish_record(sums[0], sums[1], sums[2], sums[3], a.sums, a.arrived, gridDim.x, a.record, 4);
+}
+
+// ------------------------------------------------------------------------------------- preference loss
+
+__device__ __forceinline__ double group_sum(double x, double* lds) {
+  x = wave_sum(x);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = 0.0;
+  for (uint32_t i = 0; i < blockDim.x / 64; ++i) x += lds[i];
+  return x;
+}
+
+// A workgroup takes a pair: the sums of both sequences' log ratios in fp64, then the gradient of each of their tokens.
+__global__ __launch_bounds__(1024) void preference(PreferenceArgs a) {
+  __shared__ double lds[kMostWaves];
+  const uint32_t lanes = blockDim.x, lane = threadIdx.x;
+  const int64_t rows = static_cast<int64_t>(a.rows);
+  auto bound = [&](size_t i) {
+    const int64_t o = a.offsets[i];
+    return o < 0 ? 0 : o > rows ? rows : o;
+  };
+  double loss = 0.0, right = 0.0, margin = 0.0;
+  for (size_t pair = blockIdx.x; pair < a.pairs; pair += gridDim.x) {
+    const int64_t from = bound(2 * pair), mid = bound(2 * pair + 1), to = bound(2 * pair + 2);
+    double s = 0.0;  // the chosen sequence's sum less the rejected one's
+#pragma unroll 4
+    for (int64_t i = from + lane; i < to; i += lanes) {
+      const double x = static_cast<double>(a.logp[i]) - (a.ref ? static_cast<double>(a.ref[i]) : 0.0);
+      s += i < mid ? x : -x;
+    }
+    const double h = a.beta * group_sum(s, lds);
+    const double e = exp(-fabs(h)), small = log1p(e);  // -ln sigmoid(x) = log1p(exp(-|x|)) + max(-x, 0)
+    const double below = e / (1.0 + e), sig_minus = h >= 0.0 ? below : 1.0 - below;  // sigmoid(-h)
+    if (lane == 0) {
+      loss += (1.0 - a.smoothing) * (small + fmax(-h, 0.0));
+      if (a.smoothing > 0.0) loss += a.smoothing * (small + fmax(h, 0.0));
+      right += h > 0.0 ? 1.0 : 0.0;
+      margin += h;
+      if (a.margins) a.margins[pair] = static_cast<float>(h);
+    }
+    if (a.dlogp) {
+      const float g = static_cast<float>(a.grad_scale * a.loss_scale * a.beta * (a.smoothing - sig_minus));
+      for (int64_t i = from + lane; i < to; i += lanes) a.dlogp[i] = i < mid ? g : -g;
+    }
+  }
+  if (a.dlogp) {  // rows of no sequence
+    const int64_t first = bound(0), end = bound(2 * a.pairs), step = static_cast<int64_t>(gridDim.x) * lanes;
+    const int64_t me = static_cast<int64_t>(blockIdx.x) * lanes + lane;
+    for (int64_t i = me; i < first; i += step) a.dlogp[i] = 0.0f;
+    for (int64_t i = (end > first ? end : first) + me; i < rows; i += step) a.dlogp[i] = 0.0f;
+  }
+  const double n = a.pairs ? 1.0 / static_cast<double>(a.pairs) : 0.0;
+  finish_record(loss * a.loss_scale, right * n, margin * n, 0.0, a.sums, a.arrived, gridDim.x, a.record, 3);
+}
+
+// ---------------------------------------------------------------------------------------------- launches
+
+constexpr size_t kMostGrid = size_t{1} << 20;  // below 2^32 lanes; kernels loop over what lies past their grid
+inline uint32_t grid_of(size_t n) { return static_cast<uint32_t>(n < kMostGrid ? n : kMostGrid); }
+
+inline uint32_t stat_lanes(size_t packs_of_part) {
+  return packs_of_part <= 256 ? 64 : packs_of_part <= 2048 ? 256 : 512;
+}
+
+// Rows in registers: lanes and packs a lane.
+struct Held {
+  uint32_t waves;
+  int K;
+};
+constexpr int kHeldMost = 16;
+Held held_row(size_t cols, int V) {
+  const size_t packs = (cols + V - 1) / V;
+  if (cols < static_cast<size_t>(V) || packs > size_t{64} * kMostWaves * kHeldMost) return {0, 0};
+  const uint32_t waves = static_cast<uint32_t>((packs + 64 * kHeldMost - 1) / (64 * kHeldMost));
+  const int need = static_cast<int>((packs + 64 * waves - 1) / (64 * waves));
+  return {waves, need <= 2 ? need : (need + 1) / 2 * 2};
+}
+
+constexpr uint32_t kCus = 256;
+
+template <class T, int K>
+void held(const LogitArgs& a, uint32_t waves, uint32_t groups, hipStream_t st) {
+  hipLaunchKernelGGL((policy_held<T, K>), dim3(groups), dim3(waves * 64), 0, st, a);
+}
+template <class T>
+void launch_held(const LogitArgs& a, uint32_t groups, hipStream_t st) {
+  const Held h = held_row(a.cols, 16 / T::kSize);
+  switch (h.K) {
+    case 1: held<T, 1>(a, h.waves, groups, st); break;
+    case 2: held<T, 2>(a, h.waves, groups, st); break;
+    case 4: held<T, 4>(a, h.waves, groups, st); break;
+    case 6: held<T, 6>(a, h.waves, groups, st); break;
+    case 8: held<T, 8>(a, h.waves, groups, st); break;
+    case 10: held<T, 10>(a, h.waves, groups, st); break;
+    case 12: held<T, 12>(a, h.waves, groups, st); break;
+    case 14: held<T, 14>(a, h.waves, groups, st); break;
+    default: held<T, 16>(a, h.waves, groups, st); break;
+  }
+}
+
+template <class T, bool Policy>
+void stats(const LogitArgs& a, uint32_t groups, hipStream_t st) {
+  constexpr size_t V = 16 / T::kSize;
+  const size_t packs = (a.cols + V - 1) / V;
+  hipLaunchKernelGGL((row_stats<T, Policy>), dim3(groups), dim3(stat_lanes((packs + a.splits - 1) / a.splits)), 0, st, a);
+}
+template <class T>
+void grad(const LogitArgs& a, hipStream_t st) {
+  constexpr size_t V = 16 / T::kSize;
+  const size_t packs = (a.cols + V - 1) / V;
+  const uint32_t lanes = packs <= 256 ? 64 : 256;
+  const size_t run = static_cast<size_t>(lanes) * kGradPacks, runs = (packs + run - 1) / run;
+  hipLaunchKernelGGL((logit_grad<T>), dim3(grid_of(a.rows * runs)), dim3(lanes), 0, st, a);
+}
+
+template <class F>
+void by_type(mr_dtype dt, F f) {
+  if (dt == MR_BF16)
+    f(EBf16{});
+  else if (dt == MR_FP16)
+    f(EFp16{});
+  else
+    f(EFp32{});
+}
+
+}  // namespace
+
+LogitPlan plan_logits(size_t rows, size_t cols, mr_dtype dt, bool gradient) {
+  const int V = 16 / elem_size(dt);
+  const size_t packs = (cols + V - 1) / V;
+  LogitPlan pl{};
+  const Held h = held_row(cols, V);
+  if (gradient && h.K && rows >= kCus / 2) {
+    pl.held = 1;
+    pl.splits = 1;
+    const size_t per_cu = 16 / h.waves;  // 128 registers a lane
+    const size_t most = kCus * (per_cu > 8 ? 8 : per_cu), rounds = (rows + most - 1) / most;
+    pl.groups = static_cast<uint32_t>((rows + rounds - 1) / rounds);
+    return pl;
+  }
+  size_t splits = 1;
+  if (rows && packs && rows < 4 * kCus) {  // too few rows for the device: each over several workgroups, of at least 64 lanes' loads
+    splits = (4 * kCus + rows - 1) / rows;
+    const size_t most = (packs + 64 * kStatPacks - 1) / (64 * kStatPacks);
+    splits = splits > most ? most : splits;
+    splits = splits > 64 ? 64 : splits;
+  }
+  pl.splits = static_cast<uint32_t>(splits);
+  const size_t parts = rows * splits, most = size_t{kCus} * 8;
+  pl.groups = static_cast<uint32_t>(parts < 1 ? 1 : parts < most ? parts : most);
+  return pl;
+}
+
+hipError_t launch_logprob(const LogitArgs& a, mr_dtype dt, hipStream_t st) {
+  by_type(dt, [&](auto t) { stats<decltype(t), false>(a, grid_of(a.rows * a.splits), st); });
+  return hipGetLastError();
+}
+
+hipError_t launch_logprob_bwd(const LogitArgs& a, mr_dtype dt, hipStream_t st) {
+  by_type(dt, [&](auto t) { grad<decltype(t)>(a, st); });
+  return hipGetLastError();
+}
+
+hipError_t launch_policy(const LogitArgs& a, const LogitPlan& pl, mr_dtype dt, hipStream_t st) {
+  if (pl.held) {
+    by_type(dt, [&](auto t) { launch_held<decltype(t)>(a, pl.groups, st); });
+    return hipGetLastError();
+  }
+  by_type(dt, [&](auto t) { stats<decltype(t), true>(a, pl.groups, st); });
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.dz) return e;
+  by_type(dt, [&](auto t) { grad<decltype(t)>(a, st); });
+  return hipGetLastError();
+}
+
+uint32_t preference_groups(size_t pairs) { return static_cast<uint32_t>(pairs < 1 ? 1 : pairs < 4 * kCus ? pairs : 4 * kCus); }
+
+hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st) {
+  const uint32_t groups = preference_groups(a.pairs);
+  const uint32_t lanes = a.rows / (a.pairs ? a.pairs : 1) > 4096 ? 1024 : 256;
+  hipLaunchKernelGGL(preference, dim3(groups), dim3(lanes), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace mr

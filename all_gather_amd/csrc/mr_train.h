@@ -92,6 +92,57 @@ constexpr int kAdamUp = 16;
 uint32_t adam_tile_elems(mr_dtype dt, mr_dtype gdt, mr_state_format fmt, bool master);
 hipError_t launch_adam(const AdamArgs& a, mr_dtype dt, mr_dtype gdt, mr_state_format fmt, hipStream_t st);
 
+// ------------------------------------------------------------------------------------ losses on logits
+struct LogitArgs {
+  const char* z;        // logits, rows of `stride` elements
+  char* dz;             // their gradient, rows of `dstride` elements; may be null, may be z
+  size_t rows, cols, stride, dstride;
+  const int64_t* targets;
+  float c;              // log2(e) / temperature
+  double inv_temp;
+  float* logp;          // may be null
+  float* stats;         // [rows][2]: the row's maximum and the sum of exp((z - maximum) / temperature); may be null
+  const float* dlogp;   // backward pass: gradient of each row's log-probability
+  // policy loss
+  const float* old_logp;  // null: the log-probabilities themselves
+  const float* ref_logp;  // null: no KL term
+  const float* adv;
+  const float* weights;   // null: ones
+  double clip_lo, clip_hi, kl, grad_scale;
+  float* record;
+  // workspace
+  float* part;            // [rows][splits][3]: maximum, sum, target's logit (or -inf) of a part of a row
+  uint32_t* row_arrived;  // [rows] parts that are done; zero between launches
+  double* sums;           // [workgroups][4] parts of the policy loss's record
+  uint32_t (*arrived)[64];
+  uint32_t splits;        // parts of a row (set by the plan)
+};
+// How a call over logits is launched: a function of its shape alone.
+struct LogitPlan {
+  int held;          // policy loss: rows in registers, one launch
+  uint32_t splits;   // else: parts of a row in the statistics pass
+  uint32_t groups;   // workgroups that add up the policy loss's record
+};
+LogitPlan plan_logits(size_t rows, size_t cols, mr_dtype dt, bool gradient);
+hipError_t launch_logprob(const LogitArgs& a, mr_dtype dt, hipStream_t st);
+hipError_t launch_logprob_bwd(const LogitArgs& a, mr_dtype dt, hipStream_t st);
+hipError_t launch_policy(const LogitArgs& a, const LogitPlan& pl, mr_dtype dt, hipStream_t st);
+
+struct PreferenceArgs {
+  const float* logp;
+  const float* ref;        // may be null
+  const int64_t* offsets;  // [2 * pairs + 1]
+  size_t rows, pairs;
+  double beta, smoothing, loss_scale, grad_scale;
+  float* margins;  // may be null
+  float* dlogp;    // may be null
+  float* record;
+  double* sums;    // [workgroups][4]
+  uint32_t (*arrived)[64];
+};
+uint32_t preference_groups(size_t pairs);
+hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st);
+
 // Helpers of api.hip.  stream_workspace: the stream's library workspace (or the one of the capture under way), with room
 // for `bytes`: its Ctrl words and its data area.  Earlier work on the stream has finished with both when a later launch
 // runs, and no other thread's call uses them between this call's launches while `use` is held.

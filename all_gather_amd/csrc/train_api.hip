@@ -187,6 +187,7 @@ mr_status layer_norm_backward(const void* dy, const void* x, const void* gamma, 
   return e == hipSuccess ? MR_OK : hip_fail(e);
 }
 
+constexpr double kLog2E = 1.4426950408889634;
 constexpr uint64_t kMaxCount = uint64_t{1} << 33;  // elements of one tensor
 constexpr double kLeastEps = 0x1p-126;             // fp32's smallest normal number: the reciprocal takes smaller ones as zero
 constexpr uint32_t kMaxTiles = 1u << 23;           // tiles of one launch (256 lanes each, below 2^32 lanes)
@@ -363,6 +364,181 @@ mr_status adamw_step(const void* const* params, const void* const* grads, const 
   return e == hipSuccess ? MR_OK : hip_fail(e);
 }
 
+// Rows of a call over logits: `stride` elements apart, `cols` of them used.
+mr_status check_logits(size_t rows, size_t cols, size_t stride, mr_dtype dtype, double temperature) {
+  if (!valid_dtype(dtype)) return MR_ERR_INVALID_ARG;
+  if (!is_float(dtype)) return MR_ERR_DTYPE;
+  if (cols > 0x7fffffffu || rows > (size_t{1} << 40) || stride > (size_t{1} << 40) || (rows > 1 && stride < cols)) return MR_ERR_INVALID_ARG;
+  if (rows && stride > (size_t{1} << 56) / rows) return MR_ERR_INVALID_ARG;
+  const float c = static_cast<float>(kLog2E / temperature);
+  if (!(temperature > 0.0) || !std::isfinite(temperature) || !std::isfinite(c) || c < 0x1p-126f) return MR_ERR_INVALID_ARG;
+  return MR_OK;
+}
+// Bytes that a call touches from the first element of the first row to the last of the last.
+size_t extent(size_t rows, size_t cols, size_t stride, size_t es) { return rows && cols ? ((rows - 1) * stride + cols) * es : 0; }
+
+mr::LogitArgs logit_args(const void* logits, size_t rows, size_t cols, size_t stride, const int64_t* targets, double temperature) {
+  mr::LogitArgs a{};
+  a.z = static_cast<const char*>(logits);
+  a.rows = rows;
+  a.cols = cols;
+  a.stride = stride;
+  a.targets = targets;
+  a.c = static_cast<float>(kLog2E / temperature);
+  a.inv_temp = 1.0 / temperature;
+  a.splits = 1;
+  return a;
+}
+
+// Arrival counters of `n` rows in the stream's workspace: the words after its control words, zero between calls.
+size_t row_words_bytes(size_t n) { return n << 8; }
+uint32_t* row_words(mr::Ctrl* ctrl) { return reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(ctrl) + mr::kCtrlBytes); }
+
+mr_status token_logprob_forward(const void* logits, size_t rows, size_t cols, size_t stride, mr_dtype dtype, const int64_t* targets,
+                                double temperature, float* logp, float* stats, hipStream_t st) {
+  mr_status s = check_logits(rows, cols, stride, dtype, temperature);
+  if (s != MR_OK) return s;
+  if (rows == 0 || (!logp && !stats)) return MR_OK;
+  if ((!logits && cols) || !targets) return MR_ERR_INVALID_ARG;
+  const size_t es = mr::elem_size(dtype), in = extent(rows, cols, stride, es);
+  if (!on_grid(logits, es) || !on_grid(targets, 8) || !on_grid(logp, 4) || !on_grid(stats, 4)) return MR_ERR_INVALID_ARG;
+  Outputs outs(&t_spans);
+  outs.add(logp, rows * 4, 0);
+  outs.add(stats, rows * 8, 0);
+  if (!outs.ok() || !outs.admits(logits, in) || !outs.admits(targets, rows * 8)) return MR_ERR_ALIAS;
+  mr::LogitArgs a = logit_args(logits, rows, cols, stride, targets, temperature);
+  a.logp = logp;
+  a.stats = stats;
+  a.splits = mr::plan_logits(rows, cols, dtype, false).splits;
+  std::unique_lock<std::mutex> use;  // to the last launch
+  if (a.splits > 1) {
+    mr::Ctrl* ctrl = nullptr;
+    char* data = nullptr;
+    s = mr::stream_workspace(st, std::max(rows * a.splits * 8, row_words_bytes(rows)), &ctrl, &data, &use);
+    if (s != MR_OK) return s;
+    a.part = reinterpret_cast<float*>(data);
+    a.row_arrived = row_words(ctrl);
+  }
+  if (mr::trace_on())
+    std::fprintf(stderr, "[mr] token_logprob forward rows=%zu cols=%zu dtype=%d splits=%u\n", rows, cols, static_cast<int>(dtype), a.splits);
+  const hipError_t e = mr::launch_logprob(a, dtype, st);
+  return e == hipSuccess ? MR_OK : hip_fail(e);
+}
+
+mr_status token_logprob_backward(const void* logits, size_t rows, size_t cols, size_t stride, mr_dtype dtype, const int64_t* targets,
+                                 double temperature, const float* stats, const float* dlogp, void* dlogits, size_t dstride,
+                                 hipStream_t st) {
+  mr_status s = check_logits(rows, cols, stride, dtype, temperature);
+  if (s == MR_OK) s = check_logits(rows, cols, dstride, dtype, temperature);
+  if (s != MR_OK) return s;
+  if (rows == 0 || cols == 0) return MR_OK;
+  if (!logits || !targets || !stats || !dlogp || !dlogits) return MR_ERR_INVALID_ARG;
+  const size_t es = mr::elem_size(dtype), in = extent(rows, cols, stride, es), out = extent(rows, cols, dstride, es);
+  if (!on_grid(logits, es) || !on_grid(dlogits, es) || !on_grid(targets, 8) || !on_grid(stats, 4) || !on_grid(dlogp, 4))
+    return MR_ERR_INVALID_ARG;
+  Outputs outs(&t_spans);
+  outs.add(dlogits, out, 1);
+  if (!outs.admits(logits, in, [](int id) { return id == 1; }) || !outs.admits(targets, rows * 8) || !outs.admits(stats, rows * 8) ||
+      !outs.admits(dlogp, rows * 4))
+    return MR_ERR_ALIAS;
+  mr::LogitArgs a = logit_args(logits, rows, cols, stride, targets, temperature);
+  a.stats = const_cast<float*>(stats);
+  a.dlogp = dlogp;
+  a.dz = static_cast<char*>(dlogits);
+  a.dstride = dstride;
+  if (mr::trace_on())
+    std::fprintf(stderr, "[mr] token_logprob backward rows=%zu cols=%zu dtype=%d\n", rows, cols, static_cast<int>(dtype));
+  const hipError_t e = mr::launch_logprob_bwd(a, dtype, st);
+  return e == hipSuccess ? MR_OK : hip_fail(e);
+}
+
+mr_status policy_loss(const void* logits, size_t rows, size_t cols, size_t stride, mr_dtype dtype, const int64_t* targets,
+                      const float* old_logp, const float* ref_logp, const float* advantages, const float* weights,
+                      const mr_policy_hyper* h, float* record, float* logp, void* dlogits, size_t dstride, hipStream_t st) {
+  if (!h) return MR_ERR_INVALID_ARG;
+  mr_status s = check_logits(rows, cols, stride, dtype, h->temperature);
+  if (s == MR_OK && dlogits) s = check_logits(rows, cols, dstride, dtype, h->temperature);
+  if (s != MR_OK) return s;
+  if (!(h->clip_low >= 0.0 && h->clip_low <= 1.0) || !(h->clip_high >= 0.0) || !std::isfinite(h->clip_high) || !std::isfinite(h->kl_coef) ||
+      !(h->grad_scale > 0.0) || !std::isfinite(h->grad_scale) || (h->kl_coef != 0.0 && !ref_logp))
+    return MR_ERR_INVALID_ARG;
+  if (!record || !on_grid(record, 4) || (rows && ((!logits && cols) || !targets || !advantages))) return MR_ERR_INVALID_ARG;
+  const size_t es = mr::elem_size(dtype), in = extent(rows, cols, stride, es), out = extent(rows, cols, dstride, es);
+  if (!on_grid(logits, es) || !on_grid(dlogits, es) || !on_grid(targets, 8) || !on_grid(old_logp, 4) || !on_grid(ref_logp, 4) ||
+      !on_grid(advantages, 4) || !on_grid(weights, 4) || !on_grid(logp, 4))
+    return MR_ERR_INVALID_ARG;
+  Outputs outs(&t_spans);
+  outs.add(dlogits, out, 1);
+  outs.add(record, 16, 0);
+  outs.add(logp, rows * 4, 0);
+  if (!outs.ok() || !outs.admits(logits, in, [](int id) { return id == 1; }) || !outs.admits(targets, rows * 8)) return MR_ERR_ALIAS;
+  for (const float* p : {old_logp, ref_logp, advantages, weights})
+    if (!outs.admits(p, rows * 4)) return MR_ERR_ALIAS;
+  mr::LogitArgs a = logit_args(logits, rows, cols, stride, targets, h->temperature);
+  a.old_logp = old_logp;
+  a.ref_logp = ref_logp;
+  a.adv = advantages;
+  a.weights = weights;
+  a.clip_lo = h->clip_low;
+  a.clip_hi = h->clip_high;
+  a.kl = h->kl_coef;
+  a.grad_scale = h->grad_scale;
+  a.record = record;
+  a.logp = logp;
+  a.dz = cols ? static_cast<char*>(dlogits) : nullptr;
+  a.dstride = dstride;
+  const mr::LogitPlan pl = mr::plan_logits(rows, cols, dtype, a.dz != nullptr);
+  a.splits = pl.splits;
+  // the workspace: workgroups' sums, then (on the path of two passes) rows' statistics, gradients and parts
+  const size_t sums = size_t{pl.groups} * 32, two = pl.held ? 0 : rows * 12 + rows * (pl.splits > 1 ? pl.splits * 8 : 0);
+  mr::Ctrl* ctrl = nullptr;
+  char* data = nullptr;
+  std::unique_lock<std::mutex> use;  // to the last launch
+  s = mr::stream_workspace(st, std::max(sums + two, pl.splits > 1 ? row_words_bytes(rows) : 0), &ctrl, &data, &use);
+  if (s != MR_OK) return s;
+  a.sums = reinterpret_cast<double*>(data);
+  a.arrived = ctrl->arrived;
+  if (!pl.held) {
+    a.stats = reinterpret_cast<float*>(data + sums);
+    a.dlogp = a.stats + 2 * rows;
+    a.part = a.stats + 3 * rows;
+    a.row_arrived = row_words(ctrl);
+  }
+  if (mr::trace_on())
+    std::fprintf(stderr, "[mr] policy_loss rows=%zu cols=%zu dtype=%d held=%d splits=%u groups=%u\n", rows, cols, static_cast<int>(dtype),
+                 pl.held, pl.splits, pl.groups);
+  const hipError_t e = mr::launch_policy(a, pl, dtype, st);
+  return e == hipSuccess ? MR_OK : hip_fail(e);
+}
+
+mr_status preference_loss(const float* logp, const float* ref_logp, size_t rows, const int64_t* offsets, size_t pairs,
+                          const mr_preference_hyper* h, float* record, float* margins, float* dlogp, hipStream_t st) {
+  if (!h || !std::isfinite(h->beta) || !(h->smoothing >= 0.0 && h->smoothing <= 0.5) || !std::isfinite(h->loss_scale) ||
+      !(h->grad_scale > 0.0) || !std::isfinite(h->grad_scale))
+    return MR_ERR_INVALID_ARG;
+  if (rows > (size_t{1} << 40) || pairs > (size_t{1} << 40) || !record || !offsets || (rows && !logp)) return MR_ERR_INVALID_ARG;
+  if (!on_grid(logp, 4) || !on_grid(ref_logp, 4) || !on_grid(offsets, 8) || !on_grid(record, 4) || !on_grid(margins, 4) || !on_grid(dlogp, 4))
+    return MR_ERR_INVALID_ARG;
+  Outputs outs(&t_spans);
+  outs.add(record, 12, 0);
+  outs.add(margins, pairs * 4, 0);
+  outs.add(dlogp, rows * 4, 1);
+  if (!outs.ok() || !outs.admits(logp, rows * 4, [](int id) { return id == 1; }) || !outs.admits(ref_logp, rows * 4) ||
+      !outs.admits(offsets, (2 * pairs + 1) * 8))
+    return MR_ERR_ALIAS;
+  mr::PreferenceArgs a{logp, ref_logp, offsets, rows, pairs, h->beta, h->smoothing, h->loss_scale, h->grad_scale, margins, dlogp, record, nullptr, nullptr};
+  mr::Ctrl* ctrl = nullptr;
+  char* data = nullptr;
+  std::unique_lock<std::mutex> use;  // to the last launch
+  const mr_status s = mr::stream_workspace(st, size_t{mr::preference_groups(pairs)} * 32, &ctrl, &data, &use);
+  if (s != MR_OK) return s;
+  a.sums = reinterpret_cast<double*>(data);
+  a.arrived = ctrl->arrived;
+  if (mr::trace_on()) std::fprintf(stderr, "[mr] preference_loss rows=%zu pairs=%zu\n", rows, pairs);
+  const hipError_t e = mr::launch_preference(a, st);
+  return e == hipSuccess ? MR_OK : hip_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -398,6 +574,38 @@ mr_status mr_adamw_step(const void* const* params, const void* const* grads, con
   return guarded([&] {
     return adamw_step(params, grads, counts, P, dtype, grad_dtype, format, state, params_out, state_out, hyper, clip,
                       reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+mr_status mr_token_logprob_forward(const void* logits, size_t rows, size_t cols, size_t stride, mr_dtype dtype, const int64_t* targets,
+                                   double temperature, float* logp, float* stats, mr_stream stream) {
+  return guarded([&] {
+    return token_logprob_forward(logits, rows, cols, stride, dtype, targets, temperature, logp, stats, reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+mr_status mr_token_logprob_backward(const void* logits, size_t rows, size_t cols, size_t stride, mr_dtype dtype, const int64_t* targets,
+                                    double temperature, const float* stats, const float* dlogp, void* dlogits, size_t dstride,
+                                    mr_stream stream) {
+  return guarded([&] {
+    return token_logprob_backward(logits, rows, cols, stride, dtype, targets, temperature, stats, dlogp, dlogits, dstride,
+                                  reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+mr_status mr_policy_loss(const void* logits, size_t rows, size_t cols, size_t stride, mr_dtype dtype, const int64_t* targets,
+                         const float* old_logp, const float* ref_logp, const float* advantages, const float* weights,
+                         const mr_policy_hyper* hyper, float* record, float* logp, void* dlogits, size_t dstride, mr_stream stream) {
+  return guarded([&] {
+    return policy_loss(logits, rows, cols, stride, dtype, targets, old_logp, ref_logp, advantages, weights, hyper, record, logp, dlogits,
+                       dstride, reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+mr_status mr_preference_loss(const float* logp, const float* ref_logp, size_t rows, const int64_t* offsets, size_t pairs,
+                             const mr_preference_hyper* hyper, float* record, float* margins, float* dlogp, mr_stream stream) {
+  return guarded([&] {
+    return preference_loss(logp, ref_logp, rows, offsets, pairs, hyper, record, margins, dlogp, reinterpret_cast<hipStream_t>(stream));
   });
 }
 

@@ -342,6 +342,58 @@ mr_status mr_adamw_step(const void* const* params, const void* const* grads, con
                         const mr_adamw_state* state_out, const mr_adamw_hyper* hyper, const float* clip, mr_stream stream);
 
 /*
+ * Losses on logits: log-probabilities of target tokens with their gradient, a clipped policy loss and a preference loss.
+ *
+ * Logits are `rows` rows (tokens, of any number of packed sequences) of `cols` elements (the vocabulary) of `dtype` (MR_BF16,
+ * MR_FP16, MR_FP32), `stride` >= cols elements apart, so that a padded vocabulary's last columns may be left out; rows and
+ * pointers lie anywhere on the element grid.  In fp32, with T the temperature (> 0, log2(e)/T a normal fp32 number),
+ *     m = max_j z_j,   S = sum_j exp((z_j - m) / T),   logp = (z_t - m) / T - ln S
+ * A row whose target lies outside [0, cols) (-100, say: prompts and padding), or, in the policy loss, whose weight is 0, carries
+ * no loss: it is not read, its logp and statistics are 0 and its gradient is zeros.  Logits of -inf have probability 0; other
+ * infinities and NaN give what the formulas give, in their row and in the sums over rows.
+ *
+ * mr_token_logprob_forward:   logp (rows floats, or NULL) and stats (rows pairs of floats {m, S} for the backward pass, or NULL).
+ * mr_token_logprob_backward:  dlogits[i][j] = narrow(dlogp_i / T * ([j = t_i] - exp((z_ij - m_i) / T) / S_i))
+ * mr_policy_loss:  for each row, with r = exp(logp - old_logp) and d = ref_logp - logp,
+ *         loss_i = max(-A r, -A min(max(r, 1 - clip_low), 1 + clip_high)) + kl_coef * (exp(d) - d - 1)
+ *     record[0..3] = sums over the rows of  w loss_i,  w (exp(d) - d - 1),  w [the clipped term is the larger],  w
+ *     (fp64 sums in an order set by the sizes alone), and with dlogits the gradient of grad_scale * record[0], from the same
+ *     pass over the logits where a row fits a workgroup's registers (131072 16-bit or 65536 fp32 columns).  A term that is
+ *     clipped, and only that, passes no gradient.
+ *       old_logp  of the policy that sampled the tokens; NULL: of this one (r = 1).  ref_logp: NULL without a KL term (d = 0).
+ *       advantages  rows floats;  weights: rows floats (a mask over its sum, say), or NULL: ones.
+ *       logp, dlogits  or NULL.
+ * mr_preference_loss:  rows hold 2 * pairs sequences, sequence k in [offsets[k], offsets[k+1]): pair p's chosen one is 2p, its
+ *     rejected one 2p+1.  With s_k the sum of logp - ref_logp over a sequence and h_p = beta * (s_2p - s_2p+1),
+ *         loss_p = -(1 - smoothing) ln sigmoid(h_p) - smoothing ln sigmoid(-h_p)
+ *     record[0..2] = loss_scale * sum of loss_p,  the share of h_p > 0,  the mean of h_p;  margins[p] = h_p, or NULL;
+ *     dlogp: the gradient of grad_scale * record[0] by each row's logp, zeros in rows of no sequence, or NULL; may be logp
+ *     exactly.  offsets (device) do not decrease; they are held to [0, rows], and others give undefined values.
+ *
+ *  targets  device, rows int64.  dlogits: rows `dstride` elements apart, only their `cols` elements written; it may be the logits
+ *           exactly, with their stride.  Other overlaps -> MR_ERR_ALIAS; the rest is checked as above.  rows == 0 is a no-op,
+ *           but for the records, which become zeros.
+ *  The losses and a forward pass of few rows keep partial sums in the stream's library workspace; one that the caller binds
+ *  is large enough with mr_workspace_bytes(1, 256 * rows + 65536, MR_FP32) bytes.
+ */
+typedef struct mr_policy_hyper {
+  double temperature, clip_low, clip_high, kl_coef, grad_scale; /* clip_low in [0, 1], clip_high >= 0, grad_scale > 0 */
+} mr_policy_hyper;
+typedef struct mr_preference_hyper {
+  double beta, smoothing, loss_scale, grad_scale; /* smoothing in [0, 0.5], grad_scale > 0 */
+} mr_preference_hyper;
+mr_status mr_token_logprob_forward(const void* logits, size_t rows, size_t cols, size_t stride, mr_dtype dtype, const int64_t* targets,
+                                   double temperature, float* logp, float* stats, mr_stream stream);
+mr_status mr_token_logprob_backward(const void* logits, size_t rows, size_t cols, size_t stride, mr_dtype dtype, const int64_t* targets,
+                                    double temperature, const float* stats, const float* dlogp, void* dlogits, size_t dstride,
+                                    mr_stream stream);
+mr_status mr_policy_loss(const void* logits, size_t rows, size_t cols, size_t stride, mr_dtype dtype, const int64_t* targets,
+                         const float* old_logp, const float* ref_logp, const float* advantages, const float* weights,
+                         const mr_policy_hyper* hyper, float* record, float* logp, void* dlogits, size_t dstride, mr_stream stream);
+mr_status mr_preference_loss(const float* logp, const float* ref_logp, size_t rows, const int64_t* offsets, size_t pairs,
+                             const mr_preference_hyper* hyper, float* record, float* margins, float* dlogp, mr_stream stream);
+
+/*
  * Two-shot workspace.
  *
  * By default the library allocates, on first two-shot use of a (device, stream) pair, a grow-only
@@ -456,7 +508,7 @@ mr_status mr_get_option(mr_option opt, int64_t* value);
  * mr_allgather_param_contig_sdma, mr_sdma_engines and MR_ERR_ENGINE; 1.04 added
  * mr_allreduce_sum_noalloc and the last-arriver hand-off on XCD-local units (the default up to 32 MiB
  * per rank buffer); 1.05 added MR_OPT_SDMA_CU_BELOW (small parameters of the SDMA gather on the
- * compute units).  The training-step entry points (mr_layer_norm_forward and the four after it) came later
+ * compute units).  The training-step entry points (mr_layer_norm_forward and those after it) came later
  * under the same number: they add symbols and change none. */
 int mr_version(void);
 
