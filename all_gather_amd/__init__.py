@@ -1,5 +1,5 @@
 """Python binding of libmr, the MI355X W-way sum-reduce and param-contiguous gather library, with the operators of
-a training step around them (layer norm, losses on logits, gradient norm, AdamW).
+a training step around them (layer norm, losses on logits, gradient norm, AdamW, Muon).
 
 A thin ctypes layer over the C ABI declared in include/mr.h: it turns torch tensors into device
 pointers, sizes and the current HIP stream, calls the entry point of the same name and raises on a
@@ -28,6 +28,7 @@ STATUS = {
 }
 DTYPE_CODE = {"bf16": 0, "fp16": 1, "fp32": 2, "int32": 3}
 STATE_FORMAT = {32: 0, 8: 1}
+MUON_ADJUST = {"ratio": 0, "rms": 1}
 MODE_CODE = {"oneshot": 0, "twoshot": 1}
 OPTION_CODE = {"twoshot_sync": 0, "spin_limit": 1, "tile_shape": 2, "sdma_cu_below": 3}
 TWOSHOT_SYNC = {"tile": 0, "chunk": 1, "grid": 2, "last": 3, "auto": 4}
@@ -54,6 +55,15 @@ class _PolicyHyperC(ctypes.Structure):
 
 class _PreferenceHyperC(ctypes.Structure):
     _fields_ = [(k, ctypes.c_double) for k in ("beta", "smoothing", "loss_scale", "grad_scale")]
+
+
+class _MuonStateC(ctypes.Structure):
+    _fields_ = [("momentum", ctypes.c_void_p), ("master", ctypes.c_void_p)]
+
+
+class _MuonHyperC(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("lr", "momentum", "weight_decay", "eps")] + [
+        ("coefficients", ctypes.POINTER(ctypes.c_double))] + [(k, ctypes.c_int) for k in ("steps", "nesterov", "products", "adjust")]
 
 
 # Exported symbols of include/mr.h, with ctypes signatures.
@@ -98,6 +108,10 @@ _SIGS = {
                                      ctypes.POINTER(ctypes.c_uint64)] + [ctypes.c_int] * 4 +
                       [ctypes.POINTER(_AdamWStateC), ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(_AdamWStateC),
                        ctypes.POINTER(_AdamWHyperC), ctypes.c_void_p, ctypes.c_void_p]),
+    "mr_muon_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(ctypes.c_uint64)] * 2 + [ctypes.c_int] * 2),
+    "mr_muon_step": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p)] * 2 + [ctypes.POINTER(ctypes.c_uint64)] * 2 + [ctypes.c_int] * 3 +
+                     [ctypes.POINTER(_MuonStateC), ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(_MuonStateC),
+                      ctypes.POINTER(_MuonHyperC), ctypes.c_void_p, ctypes.c_void_p]),
     "mr_token_logprob_forward": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_size_t] * 3 + [ctypes.c_int, ctypes.c_void_p,
                                                 ctypes.c_double] + [ctypes.c_void_p] * 3),
     "mr_token_logprob_backward": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_size_t] * 3 + [ctypes.c_int, ctypes.c_void_p,
@@ -695,6 +709,105 @@ def adamw_step(params: Sequence, grads: Sequence, state: AdamWState, lr: float, 
     ``params_out`` / ``state_out``.  ``clip``: grad_norm's record, whose factor multiplies the gradients and which leaves the
     step out where a gradient is not finite.  ``seed``: of the 8-bit state's stochastic rounding."""
     prepare_adamw(params, grads, state, params_out, state_out, betas, eps, weight_decay, clip, seed, stream)(lr, step)
+
+
+@dataclasses.dataclass
+class MuonState:
+    """Muon's flat state of a list of matrices, laid out as AdamWState is: ``m``, the momentum (fp32), and ``master``, fp32 copies of
+    16-bit parameters, or None."""
+
+    m: Any
+    master: Any = None
+
+
+def muon_init(params: Sequence, master: bool = False) -> MuonState:
+    """A zero state for the matrices ``params``; with ``master``, fp32 copies of them."""
+    torch = _torch()
+    at, n = adamw_offsets([p.numel() for p in params])
+    st = MuonState(torch.zeros(n, device=params[0].device))
+    if master:
+        st.master = torch.zeros(n, device=params[0].device)
+        for p, a in zip(params, at):
+            st.master[a:a + p.numel()].copy_(p.detach().reshape(-1))
+    return st
+
+
+def _matrices(params):
+    for p in params:
+        if p.dim() != 2:
+            raise ValueError("Muon takes matrices")
+    n = max(len(params), 1)
+    return (ctypes.c_uint64 * n)(*[p.shape[0] for p in params]), (ctypes.c_uint64 * n)(*[p.shape[1] for p in params])
+
+
+def muon_workspace_bytes(shapes: Sequence, products: int = 16) -> int:
+    """Bytes that a workspace bound with set_workspace needs for a muon_step over matrices of the given (rows, columns)."""
+    n = max(len(shapes), 1)
+    return int(lib().mr_muon_workspace_bytes((ctypes.c_uint64 * n)(*[r for r, _ in shapes]), (ctypes.c_uint64 * n)(*[c for _, c in shapes]),
+                                             len(shapes), products))
+
+
+def prepare_muon(params: Sequence, grads: Sequence, state: MuonState, params_out=None, state_out: MuonState | None = None,
+                 momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.1, eps: float = 1e-7, coefficients=None,
+                 steps: int = 5, adjust: str = "ratio", products: int = 16, clip=None, stream=None):
+    """Pre-marshalled mr_muon_step for matrices that stay where they are: the returned ``call(lr)`` takes a step, on ``stream`` or
+    the one that is current at preparation.  Results go in place, or to ``params_out`` / ``state_out``."""
+    params, grads = list(params), list(grads)
+    rows, cols = _matrices(params)
+    counts = [p.numel() for p in params]
+    n = sum(-(-k // ADAMW_BLOCK) * ADAMW_BLOCK for k in counts)
+    pp, gp = _tensor_list(params, "params"), _tensor_list(grads, "grads", counts)
+    if any(g.shape != p.shape for g, p in zip(grads, params)):
+        raise ValueError("grads must be shaped like the params")
+    if params_out is not None:
+        params_out = list(params_out)
+        if params and params_out and params_out[0].dtype != params[0].dtype:
+            raise ValueError("params_out must be of the params' dtype")
+    po = None if params_out is None else _tensor_list(params_out, "params_out", counts)
+    if params and dtype_name(grads[0]) not in (dtype_name(params[0]), "fp32"):
+        raise ValueError("grads must be of the params' dtype or torch.float32")
+    f32 = _torch().float32
+
+    def state_c(st):
+        return _MuonStateC(_need(st.m, "m", f32, n), _opt(st.master, "master", (f32,), n))
+
+    sin = state_c(state)
+    sout = None if state_out is None else state_c(state_out)
+    _opt(clip, "clip", (f32,), 3)
+    coef = None
+    if coefficients is not None:
+        flat = [float(x) for c in coefficients for x in (c if isinstance(c, (tuple, list)) else (c,))]
+        if len(flat) == 3:
+            flat = flat * steps
+        if len(flat) != 3 * steps:
+            raise ValueError("coefficients must be one (a, b, c), or one for every step")
+        coef = (ctypes.c_double * len(flat))(*flat)
+    hyper = _MuonHyperC(0.0, momentum, weight_decay, eps, coef, steps, int(nesterov), products, MUON_ADJUST[adjust])
+    args = (pp, gp, rows, cols, len(params), DTYPE_CODE[dtype_name(params[0])] if params else 2,
+            DTYPE_CODE[dtype_name(grads[0])] if grads else 2, ctypes.byref(sin), po, None if sout is None else ctypes.byref(sout),
+            ctypes.byref(hyper), None if clip is None else clip.data_ptr(), _stream_handle(stream))
+    f = lib().mr_muon_step
+
+    def call(lr: float) -> None:
+        hyper.lr = lr
+        st = f(*args)
+        if st != MR_OK:
+            raise MRError(st, "mr_muon_step")
+
+    call.keepalive = (params, grads, state, params_out, state_out, clip, sin, sout, hyper, coef)
+    return call
+
+
+def muon_step(params: Sequence, grads: Sequence, state: MuonState, lr: float, params_out=None, state_out: MuonState | None = None,
+              momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.1, eps: float = 1e-7, coefficients=None,
+              steps: int = 5, adjust: str = "ratio", products: int = 16, clip=None, stream=None) -> None:
+    """One Muon step over the matrices ``params``, in place or into ``params_out`` / ``state_out``: momentum, ``steps`` Newton-Schulz
+    iterations on the update, and p' = (1 - lr * weight_decay) * p - lr * s * X, where s is sqrt(max(1, rows / cols)) (``adjust``
+    "ratio") or 0.2 * sqrt(max(rows, cols)) ("rms").  ``products``: 16 (operands rounded to fp16) or 32 (as exact as fp32, at three
+    times the work).  ``coefficients``: one (a, b, c) or one for every step.  ``clip``: grad_norm's record, whose factor multiplies the
+    gradients and which leaves the step out where a gradient is not finite."""
+    prepare_muon(params, grads, state, params_out, state_out, momentum, nesterov, weight_decay, eps, coefficients, steps, adjust, products,
+                 clip, stream)(lr)
 
 
 def workspace_bytes(W: int, n: int, dtype: str) -> int:

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmr.so")
 SOURCES = ["api.hip", "reduce_kernels.hip", "gather_kernels.hip", "probe_kernels.hip", "sdma.hip", "noalloc.hip",
-           "train_api.hip", "norm_fwd.hip", "norm_bwd.hip", "optim_kernels.hip", "loss_kernels.hip"]
+           "train_api.hip", "norm_fwd.hip", "norm_bwd.hip", "optim_kernels.hip", "loss_kernels.hip",
+           "muon_kernels.hip"]
 ARCH = "gfx950"
 
 # Device flags: no fast-math and no contraction (the sums must be plain fp32 RNE adds in order),

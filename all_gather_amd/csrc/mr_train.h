@@ -143,6 +143,86 @@ struct PreferenceArgs {
 uint32_t preference_groups(size_t pairs);
 hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st);
 
+// ------------------------------------------------------------------------------------------------ Muon
+//
+// A matrix of rows x cols is orthogonalised as X, m x n with m <= n: itself, or its transpose where rows > cols.  The
+// stream's workspace holds, in fp16 and each as `pieces` matrices after one another, X [m][ldn], its transpose [n][ldm] twice (a
+// product reads one and writes the other), A = X X^T and P = a I + b A + c A^2 [m][ldm]; ldm and ldn are m and n rounded up to
+// two of a product's stages (ns_padded), and columns past m and n are zero.
+constexpr int kMuonMats = 32;       // matrices of one launch
+constexpr uint32_t kNsK = 64;       // columns that a product takes at a time: a stage
+__host__ __device__ inline uint32_t ns_padded(uint32_t n) { return (n + 2 * kNsK - 1) / (2 * kNsK) * (2 * kNsK); }
+constexpr int kNsShift = 12;        // matrices are held times 2^12
+constexpr uint32_t kMomentumTile = 4096;  // elements
+struct MomentumArgs {
+  const char* g[kMuonMats];
+  uint64_t n[kMuonMats];
+  uint64_t at[kMuonMats];  // first element in the flat state
+  uint32_t tile_prefix[kMuonMats + 1];
+  uint32_t P;
+  const float* m;
+  float* m_out;
+  float* master_out;      // null: none (its elements between matrices become zeros)
+  const float* clip;      // {norm, factor, all finite} or null
+  double* sums;           // [tiles] sums of squares
+  double* norms;          // [P] their sums
+  uint32_t* arrived;      // [P] zero between launches
+  float mu, c;            // c = 1 - mu
+  int nesterov;
+};
+struct OrientArgs {
+  const char* g[kMuonMats];
+  _Float16* direct[kMuonMats];  // rows x ld_direct: the matrix itself
+  _Float16* turned[kMuonMats];  // cols x ld_turned: its transpose
+  uint64_t at[kMuonMats];
+  uint32_t rows[kMuonMats], cols[kMuonMats];
+  uint32_t tile_prefix[kMuonMats + 1];
+  uint32_t P;
+  const float* m;  // the new momentum
+  const float* clip;
+  const double* norms;
+  double eps;
+  float mu, c;
+  int nesterov, pieces;
+};
+// C = A B^T with A [M][lda], B [N][ldb] over K columns, and what becomes of it:
+enum NsKind { kNsGram, kNsPoly, kNsStep, kNsLast };
+struct NsProduct {
+  const _Float16* a;
+  const _Float16* b;
+  _Float16* c;       // [M][ldc]; kNsLast: unused
+  _Float16* ct;      // [N][ldct], the transpose (kNsStep)
+  uint32_t M, N, K;    // K: padded; lda = ldb = K
+  uint32_t ldc, ldct;  // N and M padded: the tiles cover them
+};
+struct NsArgs {
+  NsProduct p[kMuonMats];
+  uint32_t tile_prefix[kMuonMats + 1];
+  uint32_t P;
+  int pieces;
+  float ca, cb, cc;  // kNsPoly
+};
+struct NsUpdate {
+  const char* p;   // parameters: null where a master copy is read
+  char* po;
+  uint64_t at;     // first element in the flat state
+  float scale;     // lr times the matrix's factor
+  uint32_t turned; // the product is the matrix's transpose
+};
+struct NsLastArgs {
+  NsArgs s;
+  NsUpdate u[kMuonMats];
+  const float* master;
+  float* master_out;
+  const float* clip;
+  float keep;
+};
+uint32_t ns_tile(uint32_t m, uint32_t n);  // rows and columns of a product's tiles for a matrix of this shape
+hipError_t launch_momentum(const MomentumArgs& a, mr_dtype gdt, hipStream_t st);
+hipError_t launch_orient(const OrientArgs& a, mr_dtype gdt, hipStream_t st);
+hipError_t launch_ns(const NsArgs& a, NsKind kind, uint32_t tile, hipStream_t st);
+hipError_t launch_ns_last(const NsLastArgs& a, mr_dtype dt, uint32_t tile, hipStream_t st);
+
 // Helpers of api.hip.  stream_workspace: the stream's library workspace (or the one of the capture under way), with room
 // for `bytes`: its Ctrl words and its data area.  Earlier work on the stream has finished with both when a later launch
 // runs, and no other thread's call uses them between this call's launches while `use` is held.

@@ -1,0 +1,418 @@
+// Muon's step over a list of matrices, for gfx950: momentum, Newton-Schulz orthogonalisation, update.
+//
+//   m' = mu m + (1 - mu) f g,   u = mu m' + (1 - mu) f g (Nesterov) or m',   X = u / max(|u|, eps)
+//   steps times:  A = X X^T,  P = a I + b A + c A^2,  X = P X
+//   p' = (1 - lr wd) p - lr s X
+//
+// The products are the work: per step 2 m^2 n (A, half of it by symmetry), 2 m^3 (A^2, likewise) and 2 m^2 n operations.
+// They run on the matrix cores with fp16 operands and fp32 sums.  fp16, not bf16: X, A and P are bounded by their spectral norms (the
+// host checks that the polynomials keep them below 16), so held times 2^12 they use fp16's range and have 8 times bf16's
+// precision at the same rate.  The polynomial raises what is left of a small singular value 485-fold in five steps, and the
+// rounding of X with it: after them X is off by 1e-3 to 2e-2 of its norm (bf16: 1e-2 to 2e-1), which an update of 16-bit parameters does
+// not resolve.  For fp32 results every matrix is held in two fp16 pieces, hi + lo, and a product is three: off by 1e-5, as in fp32.
+//
+// Every product is C = A B^T with both operands' rows along the sum, so one kernel serves all three: X's transpose is kept
+// beside it, and A and P are symmetric.
+
+#include <hip/hip_runtime.h>
+
+#include "mr_train.h"
+#include "packs.h"
+
+namespace mr {
+namespace {
+
+typedef _Float16 f16;
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kUp = 1 << kNsShift, kDown = 1.0f / (1 << kNsShift);
+
+// The matrix whose tiles hold tile t.
+__device__ __forceinline__ uint32_t entry_of(const uint32_t* prefix, uint32_t P, uint32_t t) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t first = lane < P ? prefix[lane] : 0xffffffffu;
+  return static_cast<uint32_t>(__builtin_popcountll(__builtin_amdgcn_ballot_w64(first <= t))) - 1;
+}
+static_assert(kMuonMats <= 64, "one prefix entry a lane");
+
+struct Clip {
+  float f;
+  bool take;
+};
+__device__ __forceinline__ Clip clip_of(const float* clip) { return clip ? Clip{clip[1], clip[2] != 0.0f} : Clip{1.0f, true}; }
+
+// The new momentum and the update before it is normalised, from the old momentum and from the new: the same bits.
+__device__ __forceinline__ float new_momentum(float m, float g, float mu, float c) { return mu * m + c * g; }
+__device__ __forceinline__ float update_of(float m_new, float g, float mu, float c, int nesterov) { return nesterov ? mu * m_new + c * g : m_new; }
+
+__device__ __forceinline__ double group_sum(double x) {
+  __shared__ double lds[4];
+  x = wave_sum(x);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+// m' of a tile of one matrix, and its part of |u|^2 in fp64; the workgroup that finishes its matrix last adds the parts up in order.
+template <class G>
+__global__ __launch_bounds__(256) void momentum(MomentumArgs a) {
+  const Clip clip = clip_of(a.clip);
+  const uint32_t i = entry_of(a.tile_prefix, a.P, blockIdx.x), tile = blockIdx.x - a.tile_prefix[i];
+  const uint64_t e0 = uint64_t{tile} * kMomentumTile, n = a.n[i], padded = (n + kMxBlock - 1) / kMxBlock * kMxBlock;
+  const char* g = a.g[i];
+  const float* m = a.m + a.at[i];
+  float* mo = a.m_out + a.at[i];
+  double s = 0.0;
+#pragma unroll
+  for (uint32_t k = 0; k < kMomentumTile / 1024; ++k) {
+    const uint64_t e = e0 + k * 1024 + threadIdx.x * 4;
+    if (e >= padded) continue;  // whole packs of the state
+    const int live = e >= n ? 0 : n - e < 4 ? static_cast<int>(n - e) : 4;
+    float gf[4], mf[4], out[4];
+    widen(load_part<G, 4, true>(g + e * G::kSize, live), gf);
+    widen(load_raw<EFp32, 4, true>(reinterpret_cast<const char*>(m + e)), mf);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float gj = clip.f * gf[j];
+      out[j] = j < live ? clip.take ? new_momentum(mf[j], gj, a.mu, a.c) : mf[j] : 0.0f;
+      const double u = j < live ? static_cast<double>(update_of(out[j], gj, a.mu, a.c, a.nesterov)) : 0.0;
+      s = __builtin_fma(u, u, s);
+    }
+    store_raw<EFp32, 4, false>(reinterpret_cast<char*>(mo + e), narrow<EFp32, 4>(out));
+    if (a.master_out)
+      for (int j = live; j < 4; ++j) a.master_out[a.at[i] + e + j] = 0.0f;
+  }
+  s = group_sum(s);
+  __shared__ bool last;
+  const uint32_t tiles = a.tile_prefix[i + 1] - a.tile_prefix[i];
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(a.sums + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    last = __hip_atomic_fetch_add(a.arrived + i, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == tiles - 1;
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  }
+  __syncthreads();
+  if (!last) return;
+  s = 0.0;
+  for (uint32_t t = threadIdx.x; t < tiles; t += 256)
+    s += __hip_atomic_load(a.sums + a.tile_prefix[i] + t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  s = group_sum(s);
+  if (threadIdx.x == 0) {
+    a.norms[i] = __builtin_sqrt(s);
+    __hip_atomic_store(a.arrived + i, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+
+__device__ __forceinline__ void store_pieces(f16* at, size_t piece, int pieces, float x) {
+  const f16 hi = static_cast<f16>(x);
+  *at = hi;
+  if (pieces == 2) at[piece] = static_cast<f16>(x - static_cast<float>(hi));
+}
+
+// u / |u| of a 64 x 64 tile, times 2^12, in fp16: as it lies, and transposed.  Columns past the matrix become zeros.
+template <class G>
+__global__ __launch_bounds__(256) void orient(OrientArgs a) {
+  __shared__ float tile[64][65];
+  const Clip clip = clip_of(a.clip);
+  const uint32_t i = entry_of(a.tile_prefix, a.P, blockIdx.x), t = blockIdx.x - a.tile_prefix[i];
+  const uint32_t rows = a.rows[i], cols = a.cols[i], ld_direct = ns_padded(cols), ld_turned = ns_padded(rows), across = ld_direct / 64;
+  const uint32_t r0 = t / across * 64, c0 = t % across * 64, x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  const double norm = a.norms[i];
+  const double by = norm > a.eps ? norm : norm == norm ? a.eps : norm;  // NaN stays
+  const float inv = static_cast<float>(static_cast<double>(kUp) / by);
+#pragma unroll 4
+  for (uint32_t k = 0; k < 16; ++k) {
+    const uint32_t r = r0 + k * 4 + y, c = c0 + x;
+    float u = 0.0f;
+    if (r < rows && c < cols) {
+      const size_t e = static_cast<size_t>(r) * cols + c;
+      u = update_of(a.m[a.at[i] + e], clip.f * load1<G>(a.g[i] + e * G::kSize), a.mu, a.c, a.nesterov) * inv;
+    }
+    tile[k * 4 + y][x] = u;
+    if (r < rows) store_pieces(a.direct[i] + static_cast<size_t>(r) * ld_direct + c, static_cast<size_t>(rows) * ld_direct, a.pieces, u);
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (uint32_t k = 0; k < 16; ++k) {
+    const uint32_t c = c0 + k * 4 + y, r = r0 + x;
+    if (c < cols) store_pieces(a.turned[i] + static_cast<size_t>(c) * ld_turned + r, static_cast<size_t>(cols) * ld_turned, a.pieces, tile[x][k * 4 + y]);
+  }
+}
+
+// ------------------------------------------------------------------------------------------- products
+//
+// A workgroup of WR x WC waves makes a BM x BN tile; a wave holds its part of it as 32 x 32 blocks in accumulators.  The operands'
+// next 64 columns go from memory straight to LDS while the current ones are multiplied.  In LDS a row of 64 is 8 chunks of
+// 16 bytes; chunk c of row r lies at place c ^ swizzle(r), so that the rows a wave reads at once fall on different banks.  (The
+// hardware writes a wave's 64 chunks one after another: the lane that fills a place fetches the chunk that belongs there.)
+constexpr int kRow = kNsK;  // halves of an LDS row
+__device__ __forceinline__ uint32_t swizzle(uint32_t r) { return r & 7; }
+
+// Rows [0, R) of an operand's tile, 64 columns, by all waves of the workgroup.
+template <int R, int Waves>
+struct Fetch {
+  static constexpr int kLoads = R / 8 / Waves;
+  static_assert(R % (8 * Waves) == 0, "whole loads");
+  uint32_t off[kLoads];  // bytes
+  __device__ Fetch(uint32_t rows_left, uint32_t ld) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t r = (i * Waves + wave) * 8 + lane / 8;
+      const uint32_t row = r < rows_left ? r : rows_left - 1;  // rows past the matrix: its last one; their results are not used
+      off[i] = (row * ld + ((lane % 8) ^ swizzle(r)) * 8) * 2;
+    }
+  }
+  __device__ __forceinline__ void issue(const char* base, f16* lds) const {
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + off[i]),
+                                       (__attribute__((address_space(3))) void*)(lds + (i * Waves + wave) * 8 * kRow), 16, 0, 0);
+  }
+};
+
+struct Where {  // a workgroup's tile
+  uint32_t i, ti, tj;
+};
+template <int BM, int BN>
+__device__ __forceinline__ Where tile_of(const NsArgs& a, bool symmetric) {
+  // neighbouring tiles on one XCD, whose L2 then holds their operands
+  const uint32_t total = gridDim.x, per = total / kXcds, rest = total % kXcds, x = blockIdx.x % kXcds, k = blockIdx.x / kXcds;
+  const uint32_t t = x * per + (x < rest ? x : rest) + k;
+  Where w;
+  w.i = __builtin_amdgcn_readfirstlane(entry_of(a.tile_prefix, a.P, t));
+  const uint32_t q = t - a.tile_prefix[w.i];
+  const uint32_t tm = (a.p[w.i].ldct + BM - 1) / BM, tn = (a.p[w.i].ldc + BN - 1) / BN;
+  if (symmetric) {  // the lower triangle, row by row
+    uint32_t r = static_cast<uint32_t>((__builtin_sqrtf(8.0f * q + 1.0f) - 1.0f) * 0.5f);
+    while (r * (r + 1) / 2 > q) --r;
+    while ((r + 1) * (r + 2) / 2 <= q) ++r;
+    w.ti = r;
+    w.tj = q - r * (r + 1) / 2;
+  } else {  // panels of 8 tile rows, column by column
+    const uint32_t panel = q / (8 * tn), rows = tm - panel * 8 < 8 ? tm - panel * 8 : 8, in = q - panel * 8 * tn;
+    w.ti = panel * 8 + in % rows;
+    w.tj = in / rows;
+  }
+  w.ti = __builtin_amdgcn_readfirstlane(w.ti);
+  w.tj = __builtin_amdgcn_readfirstlane(w.tj);
+  return w;
+}
+
+template <int BM, int BN, int WR, int WC>
+struct Tile {
+  static constexpr int kWaves = WR * WC, kMi = BM / WR / 32, kNj = BN / WC / 32;
+  static constexpr int kHalves = (BM + BN) * kRow;  // of a stage
+  f32x16 acc[kMi][kNj];  // block (i, j), transposed: lane l has row l % 32, columns 8 (e / 4) + 4 (l / 32) + e % 4
+
+  __device__ __forceinline__ void multiply(const f16* lds) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t ra = wave / WC * (BM / WR) + lane % 32, rb = wave % WC * (BN / WC) + lane % 32;
+#pragma unroll
+    for (int k = 0; k < static_cast<int>(kNsK) / 16; ++k) {
+      f16x8 x[kMi], y[kNj];
+#pragma unroll
+      for (int i = 0; i < kMi; ++i)
+        x[i] = *reinterpret_cast<const f16x8*>(lds + (ra + i * 32) * kRow + ((2 * k + lane / 32) ^ swizzle(ra)) * 8);
+#pragma unroll
+      for (int j = 0; j < kNj; ++j)
+        y[j] = *reinterpret_cast<const f16x8*>(lds + (BM + rb + j * 32) * kRow + ((2 * k + lane / 32) ^ swizzle(rb)) * 8);
+#pragma unroll
+      for (int i = 0; i < kMi; ++i)
+#pragma unroll
+        for (int j = 0; j < kNj; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[j], x[i], acc[i][j], 0, 0, 0);
+    }
+  }
+
+  // The sum over K columns (an even number of stages), of 1 product or (two pieces) 3, the smaller ones first.
+  __device__ __forceinline__ void run(const NsProduct& p, uint32_t ti, uint32_t tj, int pieces) {
+    __shared__ __attribute__((aligned(16))) f16 s0[kHalves];
+    __shared__ __attribute__((aligned(16))) f16 s1[kHalves];
+#pragma unroll
+    for (int i = 0; i < kMi; ++i)
+#pragma unroll
+      for (int j = 0; j < kNj; ++j) acc[i][j] = f32x16{};
+    const Fetch<BM, kWaves> fa(ti * BM < p.M ? p.M - ti * BM : 1, p.K);
+    const Fetch<BN, kWaves> fb(tj * BN < p.N ? p.N - tj * BN : 1, p.K);
+    const char* a0 = reinterpret_cast<const char*>(p.a + static_cast<size_t>(ti) * BM * p.K);
+    const char* b0 = reinterpret_cast<const char*>(p.b + static_cast<size_t>(tj) * BN * p.K);
+    const size_t a_piece = static_cast<size_t>(p.M) * p.K * 2, b_piece = static_cast<size_t>(p.N) * p.K * 2;
+    const uint32_t per = p.K / kNsK, steps = pieces == 2 ? 3 * per : per;
+    uint32_t at = 0, seg = 0;  // of the next fetch
+    auto fetch = [&](f16* s) {
+      const char* a = a0 + (pieces == 2 && seg == 1 ? a_piece : 0) + static_cast<size_t>(at) * kNsK * 2;
+      const char* b = b0 + (pieces == 2 && seg == 0 ? b_piece : 0) + static_cast<size_t>(at) * kNsK * 2;
+      fa.issue(a, s);
+      fb.issue(b, s + BM * kRow);
+      if (++at == per) at = 0, ++seg;
+    };
+    if (ti * BM >= p.M || tj * BN >= p.N) return;  // columns past the matrix alone
+    fetch(s0);
+    for (uint32_t k = 0; k < steps; k += 2) {
+      __syncthreads();  // this stage has arrived, and the other one has been read
+      fetch(s1);
+      __builtin_amdgcn_sched_barrier(0);  // on their way before the products, not between them
+      multiply(s0);
+      __syncthreads();
+      if (k + 2 < steps) fetch(s0);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(s1);
+    }
+  }
+
+  // f(row, column, the four values in that row from that column on): everywhere in the tile, past the matrix too.
+  template <class F>
+  __device__ __forceinline__ void each(uint32_t ti, uint32_t tj, F f) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t r0 = ti * BM + wave / WC * (BM / WR) + lane % 32, c0 = tj * BN + wave % WC * (BN / WC) + 4 * (lane / 32);
+#pragma unroll
+    for (int i = 0; i < kMi; ++i)
+#pragma unroll
+      for (int j = 0; j < kNj; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = acc[i][j][4 * e + q];
+          f(r0 + i * 32, c0 + j * 32 + 8 * e, v);
+        }
+  }
+};
+
+template <NsKind Kind, int BM, int BN, int WR, int WC>
+__global__ __launch_bounds__(WR* WC * 64) void ns_product(NsArgs a) {
+  constexpr bool kSym = Kind != kNsStep;
+  const Where w = tile_of<BM, BN>(a, kSym);
+  const NsProduct p = a.p[w.i];
+  Tile<BM, BN, WR, WC> t;
+  t.run(p, w.ti, w.tj, a.pieces);
+  const size_t c_piece = static_cast<size_t>(p.M) * p.ldc, ct_piece = static_cast<size_t>(p.N) * p.ldct;
+  const size_t a_piece = static_cast<size_t>(p.M) * p.K;
+  t.each(w.ti, w.tj, [&](uint32_t r, uint32_t c, float (&v)[4]) {
+    if constexpr (Kind == kNsPoly) {
+      float add[4] = {};
+      if (r < p.M && c < p.K) {  // P's columns are A's
+        for (int s = 0; s < a.pieces; ++s) {
+          const f16x4 x = *reinterpret_cast<const f16x4*>(p.a + s * a_piece + static_cast<size_t>(r) * p.K + c);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) add[q] += static_cast<float>(x[q]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = a.cb * add[q] + a.cc * (v[q] * kDown) + (r == c + q ? a.ca * kUp : 0.0f);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] *= kDown;
+    }
+    f16x4 hi, lo;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (c + q >= p.N || r >= p.M) v[q] = 0.0f;  // the columns past the matrix, of C and of its transpose
+      hi[q] = static_cast<f16>(v[q]);
+      lo[q] = static_cast<f16>(v[q] - static_cast<float>(hi[q]));
+    }
+    if (r < p.M && c < p.ldc) {
+      f16* at = p.c + static_cast<size_t>(r) * p.ldc + c;
+      *reinterpret_cast<f16x4*>(at) = hi;
+      if (a.pieces == 2) *reinterpret_cast<f16x4*>(at + c_piece) = lo;
+    }
+    if ((!kSym || w.ti != w.tj) && r < p.ldct) {
+      f16* base = kSym ? p.c : p.ct;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c + q < p.N) {
+          f16* at = base + static_cast<size_t>(c + q) * p.ldct + r;
+          *at = hi[q];
+          if (a.pieces == 2) at[ct_piece] = lo[q];
+        }
+    }
+  });
+}
+
+// The last product of the last step, which updates the parameters instead of being stored.
+template <class T, int BM, int BN, int WR, int WC>
+__global__ __launch_bounds__(WR* WC * 64) void ns_last(NsLastArgs a) {
+  const Where w = tile_of<BM, BN>(a.s, false);
+  const NsProduct p = a.s.p[w.i];
+  const NsUpdate u = a.u[w.i];
+  const Clip clip = clip_of(a.clip);
+  Tile<BM, BN, WR, WC> t;
+  t.run(p, w.ti, w.tj, a.s.pieces);
+  const float by = u.scale * kDown * kDown;
+  t.each(w.ti, w.tj, [&](uint32_t r, uint32_t c, float (&v)[4]) {
+    if (r >= p.M) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (c + q >= p.N) continue;
+      const size_t e = u.turned ? static_cast<size_t>(c + q) * p.M + r : static_cast<size_t>(r) * p.N + c + q;
+      const float old = a.master ? a.master[u.at + e] : load1<T>(u.p + e * T::kSize);
+      const float now = clip.take ? a.keep * old - by * v[q] : old;
+      if (a.master) a.master_out[u.at + e] = now;
+      store1<T>(u.po + e * T::kSize, now);
+    }
+  });
+}
+
+template <NsKind Kind>
+void product(const NsArgs& a, uint32_t tile, hipStream_t st) {
+  const dim3 grid(a.tile_prefix[a.P]);
+  if (tile == 256)
+    hipLaunchKernelGGL((ns_product<Kind, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
+  else if (tile == 128)
+    hipLaunchKernelGGL((ns_product<Kind, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((ns_product<Kind, 64, 64, 2, 2>), grid, dim3(256), 0, st, a);
+}
+template <class T>
+void last(const NsLastArgs& a, uint32_t tile, hipStream_t st) {
+  const dim3 grid(a.s.tile_prefix[a.s.P]);
+  if (tile == 256)
+    hipLaunchKernelGGL((ns_last<T, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
+  else if (tile == 128)
+    hipLaunchKernelGGL((ns_last<T, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((ns_last<T, 64, 64, 2, 2>), grid, dim3(256), 0, st, a);
+}
+
+template <class F>
+void by_type(mr_dtype dt, F f) {
+  if (dt == MR_BF16)
+    f(EBf16{});
+  else if (dt == MR_FP16)
+    f(EFp16{});
+  else
+    f(EFp32{});
+}
+
+}  // namespace
+
+uint32_t ns_tile(uint32_t m, uint32_t) { return m >= 2048 ? 256 : m >= 512 ? 128 : 64; }
+
+hipError_t launch_momentum(const MomentumArgs& a, mr_dtype gdt, hipStream_t st) {
+  by_type(gdt, [&](auto g) { hipLaunchKernelGGL((momentum<decltype(g)>), dim3(a.tile_prefix[a.P]), dim3(256), 0, st, a); });
+  return hipGetLastError();
+}
+hipError_t launch_orient(const OrientArgs& a, mr_dtype gdt, hipStream_t st) {
+  by_type(gdt, [&](auto g) { hipLaunchKernelGGL((orient<decltype(g)>), dim3(a.tile_prefix[a.P]), dim3(256), 0, st, a); });
+  return hipGetLastError();
+}
+hipError_t launch_ns(const NsArgs& a, NsKind kind, uint32_t tile, hipStream_t st) {
+  if (kind == kNsGram)
+    product<kNsGram>(a, tile, st);
+  else if (kind == kNsPoly)
+    product<kNsPoly>(a, tile, st);
+  else
+    product<kNsStep>(a, tile, st);
+  return hipGetLastError();
+}
+hipError_t launch_ns_last(const NsLastArgs& a, mr_dtype dt, uint32_t tile, hipStream_t st) {
+  by_type(dt, [&](auto t) { last<decltype(t)>(a, tile, st); });
+  return hipGetLastError();
+}
+
+}  // namespace mr

@@ -539,6 +539,284 @@ mr_status preference_loss(const float* logp, const float* ref_logp, size_t rows,
   return e == hipSuccess ? MR_OK : hip_fail(e);
 }
 
+// Do the polynomials keep X, A = X X^T and P = a I + b A + c A^2 where fp16 times 2^12 holds them?  R bounds X's singular values:
+// 1 at the start, where the Frobenius norm is; with some room for the roundings.
+bool polynomials_fit(const double* coef, int steps) {
+  double R = 1.0;
+  const auto at = [](const double* k, double l) { return k[0] + l * (k[1] + l * k[2]); };
+  for (int i = 0; i < steps; ++i, coef += 3) {
+    for (int j = 0; j < 3; ++j)
+      if (!std::isfinite(coef[j])) return false;
+    R *= 1.01;
+    const double L = R * R;
+    // P's eigenvalues are largest at an end of [0, L] or where the derivative in l = s^2 is zero, X's singular values s P(s^2) likewise
+    double p = std::max(std::fabs(at(coef, 0.0)), std::fabs(at(coef, L)));
+    if (coef[2] != 0.0) {
+      const double l = -coef[1] / (2.0 * coef[2]);
+      if (l > 0.0 && l < L) p = std::max(p, std::fabs(at(coef, l)));
+    }
+    double x = R * std::fabs(at(coef, L));
+    const double qa = 5.0 * coef[2], qb = 3.0 * coef[1], qc = coef[0], d = qb * qb - 4.0 * qa * qc;
+    const double roots[3] = {qa != 0.0 && d >= 0.0 ? (-qb + std::sqrt(d)) / (2.0 * qa) : -1.0,
+                             qa != 0.0 && d >= 0.0 ? (-qb - std::sqrt(d)) / (2.0 * qa) : -1.0, qa == 0.0 && qb != 0.0 ? -qc / qb : -1.0};
+    for (double l : roots)
+      if (l > 0.0 && l < L) x = std::max(x, std::sqrt(l) * std::fabs(at(coef, l)));
+    if (L > 15.0 || p > 15.0 || x > 3.8) return false;
+    R = x;
+  }
+  return true;
+}
+
+constexpr double kLeastNorm = 0x1p-114;           // 2^12 over it is an fp32 number
+constexpr double kNsCoef[3] = {3.4445, -4.775, 2.0315};
+constexpr int kNsMostSteps = 16;
+constexpr uint64_t kMostSide = 1 << 16;           // rows or columns of a matrix
+constexpr uint64_t kMuonGroupBytes = uint64_t{2} << 30;  // workspace from which a list is worked off in parts
+
+// A matrix's part of the workspace: elements of fp16.
+struct MuonShape {
+  uint32_t m, n, ldm, ldn;
+  bool turned;
+  uint64_t halves;  // of X, X^T twice, A and P
+};
+MuonShape muon_shape(uint64_t rows, uint64_t cols, int pieces) {
+  MuonShape s;
+  s.turned = rows > cols;
+  s.m = static_cast<uint32_t>(s.turned ? cols : rows);
+  s.n = static_cast<uint32_t>(s.turned ? rows : cols);
+  s.ldm = mr::ns_padded(s.m);
+  s.ldn = mr::ns_padded(s.n);
+  s.halves = pieces * (uint64_t{s.m} * s.ldn + 2 * (uint64_t{s.n} * s.ldm) + 2 * (uint64_t{s.m} * s.ldm));
+  return s;
+}
+uint32_t momentum_tiles(uint64_t n) { return static_cast<uint32_t>((n + mr::kMomentumTile - 1) / mr::kMomentumTile); }
+
+// Matrices of one workspace: those from `first` on that fit together, and the bytes they take.
+struct MuonGroup {
+  int first, end, count;  // count: those that are not empty
+  uint64_t bytes;         // of halves, then sums, then norms
+  uint64_t sums;
+};
+MuonGroup muon_group(const uint64_t* rows, const uint64_t* cols, int P, int first, int pieces) {
+  MuonGroup g{first, first, 0, 0, 0};
+  uint64_t halves = 0;
+  for (; g.end < P && g.count < mr::kMuonMats; ++g.end) {
+    if (rows[g.end] * cols[g.end] == 0) continue;
+    const uint64_t more = muon_shape(rows[g.end], cols[g.end], pieces).halves;
+    if (g.count && (halves + more) * 2 > kMuonGroupBytes) break;
+    halves += more;
+    g.sums += momentum_tiles(rows[g.end] * cols[g.end]);
+    ++g.count;
+  }
+  g.bytes = halves * 2 + g.sums * 8 + mr::kMuonMats * 8;
+  return g;
+}
+
+mr_status check_matrices(const uint64_t* rows, const uint64_t* cols, int P) {
+  if (P < 0 || (P && (!rows || !cols))) return MR_ERR_INVALID_ARG;
+  for (int i = 0; i < P; ++i)
+    if (rows[i] > kMostSide || cols[i] > kMostSide || rows[i] * cols[i] > kMaxCount) return MR_ERR_INVALID_ARG;
+  return MR_OK;
+}
+
+size_t muon_workspace(const uint64_t* rows, const uint64_t* cols, int P, int products) {
+  if ((products != 16 && products != 32) || check_matrices(rows, cols, P) != MR_OK) return 0;
+  uint64_t most = 0;
+  for (int i = 0; i < P;) {
+    const MuonGroup g = muon_group(rows, cols, P, i, products / 16);
+    most = std::max(most, g.bytes);
+    i = g.end;
+  }
+  return mr::workspace_bytes_for(std::max<uint64_t>(most, row_words_bytes(mr::kMuonMats)), 1);
+}
+
+mr_status muon_step(const void* const* params, const void* const* grads, const uint64_t* rows, const uint64_t* cols, int P, mr_dtype dtype,
+                    mr_dtype gdtype, const mr_muon_state* in, void* const* params_out, const mr_muon_state* out, const mr_muon_hyper* h,
+                    const float* clip, hipStream_t st) {
+  mr_status s = check_types(dtype, gdtype);
+  if (s != MR_OK) return s;
+  if (!h || (h->products != 16 && h->products != 32) || (h->adjust != MR_MUON_RATIO && h->adjust != MR_MUON_RMS) || h->steps < 1 ||
+      h->steps > kNsMostSteps)
+    return MR_ERR_INVALID_ARG;
+  const float eps32 = static_cast<float>(h->eps);
+  if (!std::isfinite(h->lr) || !std::isfinite(h->weight_decay) || !(h->momentum >= 0.0 && h->momentum < 1.0) || !(h->eps >= kLeastNorm) ||
+      !std::isfinite(eps32))
+    return MR_ERR_INVALID_ARG;
+  double coef[3 * kNsMostSteps];
+  for (int i = 0; i < 3 * h->steps; ++i) coef[i] = h->coefficients ? h->coefficients[i] : kNsCoef[i % 3];
+  if (!polynomials_fit(coef, h->steps)) return MR_ERR_INVALID_ARG;
+  s = check_matrices(rows, cols, P);
+  if (s != MR_OK) return s;
+  uint64_t total = 0;
+  for (int i = 0; i < P; ++i) {
+    total += (rows[i] * cols[i] + mr::kMxBlock - 1) / mr::kMxBlock * mr::kMxBlock;
+    if (total >= uint64_t{mr::kMxBlock} << 32) return MR_ERR_INVALID_ARG;
+  }
+  if (total == 0) return MR_OK;
+  if (!in || !grads) return MR_ERR_INVALID_ARG;
+  const bool master = in->master != nullptr;
+  if (master && dtype == MR_FP32) return MR_ERR_DTYPE;
+  if (!out) out = in;
+  if ((!params && !(master && params_out)) || master != (out->master != nullptr)) return MR_ERR_INVALID_ARG;
+  for (const mr_muon_state* q : {in, out})
+    if (!q->momentum || !on_grid(q->momentum, 256) || !on_grid(q->master, 256)) return MR_ERR_INVALID_ARG;
+  if (!on_grid(clip, 4)) return MR_ERR_INVALID_ARG;
+  const size_t es = mr::elem_size(dtype), gs = mr::elem_size(gdtype);
+  auto count = [&](int i) { return rows[i] * cols[i]; };
+  auto param_in = [&](int i) { return params ? params[i] : nullptr; };
+  auto param_out = [&](int i) { return params_out ? params_out[i] : const_cast<void*>(params[i]); };
+  for (int i = 0; i < P; ++i) {
+    if (count(i) == 0) continue;
+    if (!grads[i] || !on_grid(grads[i], gs) || !param_out(i) || !on_grid(param_out(i), es)) return MR_ERR_INVALID_ARG;
+    if (!master && (!param_in(i) || !on_grid(param_in(i), es))) return MR_ERR_INVALID_ARG;
+  }
+  Outputs outs(&t_spans);
+  for (int i = 0; i < P; ++i) outs.add(param_out(i), count(i) * es, i);
+  outs.add(out->momentum, total * 4, -1);
+  outs.add(out->master, total * 4, -2);
+  if (!outs.ok()) return MR_ERR_ALIAS;
+  auto only = [](int id) { return [id](int o) { return o == id; }; };
+  bool fine = outs.admits(in->momentum, total * 4, only(-1)) && outs.admits(in->master, total * 4, only(-2)) && outs.admits(clip, 12);
+  for (int i = 0; fine && i < P; ++i)
+    fine = outs.admits(grads[i], count(i) * gs) && (master || outs.admits(param_in(i), count(i) * es, only(i)));
+  if (!fine) return MR_ERR_ALIAS;
+
+  const int pieces = h->products / 16;
+  const float mu = static_cast<float>(h->momentum), c = static_cast<float>(1.0 - h->momentum);
+  mr::Ctrl* ctrl = nullptr;
+  char* data = nullptr;
+  std::unique_lock<std::mutex> use;  // to the last launch
+  uint64_t most = row_words_bytes(mr::kMuonMats);
+  for (int i = 0; i < P;) {
+    const MuonGroup g = muon_group(rows, cols, P, i, pieces);
+    most = std::max(most, g.bytes);
+    i = g.end;
+  }
+  s = mr::stream_workspace(st, most, &ctrl, &data, &use);
+  if (s != MR_OK) return s;
+  uint64_t at = 0;
+  for (int first = 0; first < P;) {
+    const MuonGroup g = muon_group(rows, cols, P, first, pieces);
+    struct Mat {
+      MuonShape s;
+      int i;
+      uint64_t at;
+      _Float16 *x, *xt[2], *a, *p;
+    } mats[mr::kMuonMats];
+    mr::MomentumArgs mo{};
+    mr::OrientArgs od{};
+    _Float16* next = reinterpret_cast<_Float16*>(data);
+    for (int i = first; i < g.end; ++i) {
+      if (count(i) == 0) continue;
+      const uint32_t k = mo.P++;
+      Mat& q = mats[k];
+      q.s = muon_shape(rows[i], cols[i], pieces);
+      q.i = i;
+      q.at = at;
+      auto take = [&](uint64_t halves) {
+        _Float16* r = next;
+        next += halves * pieces;
+        return r;
+      };
+      const MuonShape& z = q.s;
+      q.x = take(uint64_t{z.m} * z.ldn);
+      q.xt[0] = take(uint64_t{z.n} * z.ldm);
+      q.xt[1] = take(uint64_t{z.n} * z.ldm);
+      q.a = take(uint64_t{z.m} * z.ldm);
+      q.p = take(uint64_t{z.m} * z.ldm);
+      mo.g[k] = static_cast<const char*>(grads[i]);
+      mo.n[k] = count(i);
+      mo.at[k] = at;
+      mo.tile_prefix[k + 1] = mo.tile_prefix[k] + momentum_tiles(count(i));
+      od.g[k] = mo.g[k];
+      od.direct[k] = z.turned ? q.xt[0] : q.x;
+      od.turned[k] = z.turned ? q.x : q.xt[0];
+      od.at[k] = at;
+      od.rows[k] = static_cast<uint32_t>(rows[i]);
+      od.cols[k] = static_cast<uint32_t>(cols[i]);
+      od.tile_prefix[k + 1] = od.tile_prefix[k] + (z.ldm / 64) * (z.ldn / 64);
+      at += (count(i) + mr::kMxBlock - 1) / mr::kMxBlock * mr::kMxBlock;
+    }
+    first = g.end;
+    if (mo.P == 0) continue;
+    mo.m = in->momentum;
+    mo.m_out = out->momentum;
+    mo.master_out = out->master;
+    mo.clip = od.clip = clip;
+    mo.sums = reinterpret_cast<double*>(next);
+    mo.norms = mo.sums + g.sums;
+    mo.arrived = row_words(ctrl);
+    mo.mu = od.mu = mu;
+    mo.c = od.c = c;
+    mo.nesterov = od.nesterov = h->nesterov != 0;
+    od.P = mo.P;
+    od.m = out->momentum;
+    od.norms = mo.norms;
+    od.eps = h->eps;
+    od.pieces = pieces;
+    if (mr::trace_on())
+      std::fprintf(stderr, "[mr] muon matrices=%u dtype=%d grad=%d products=%d master=%d workspace=%llu\n", mo.P, static_cast<int>(dtype),
+                   static_cast<int>(gdtype), h->products, master ? 1 : 0, static_cast<unsigned long long>(g.bytes));
+    hipError_t e = mr::launch_momentum(mo, gdtype, st);
+    if (e == hipSuccess) e = mr::launch_orient(od, gdtype, st);
+    // one launch for the matrices of each tile size
+    for (int step = 0; step < h->steps && e == hipSuccess; ++step) {
+      const double* k3 = coef + 3 * step;
+      for (int kind = mr::kNsGram; kind <= mr::kNsStep && e == hipSuccess; ++kind)
+        for (uint32_t tile : {256u, 128u, 64u}) {
+          mr::NsLastArgs la{};
+          mr::NsArgs& a = la.s;
+          const bool final = kind == mr::kNsStep && step + 1 == h->steps;
+          for (uint32_t k = 0; k < mo.P; ++k) {
+            const Mat& q = mats[k];
+            const MuonShape& z = q.s;
+            if (mr::ns_tile(z.m, z.n) != tile) continue;
+            mr::NsProduct& p = a.p[a.P];
+            const uint32_t tm = (z.ldm + tile - 1) / tile, tn = (z.ldn + tile - 1) / tile;
+            p.M = z.m;
+            p.ldct = z.ldm;
+            if (kind == mr::kNsStep) {
+              p.a = q.p, p.b = q.xt[step & 1], p.c = q.x, p.ct = q.xt[(step + 1) & 1];
+              p.N = z.n, p.K = z.ldm, p.ldc = z.ldn;
+            } else {
+              p.a = p.b = kind == mr::kNsGram ? q.x : q.a;
+              p.c = kind == mr::kNsGram ? q.a : q.p;
+              p.N = z.m, p.K = kind == mr::kNsGram ? z.ldn : z.ldm, p.ldc = z.ldm;
+            }
+            a.tile_prefix[a.P + 1] = a.tile_prefix[a.P] + (kind == mr::kNsStep ? tm * tn : tm * (tm + 1) / 2);
+            if (final) {
+              mr::NsUpdate& u = la.u[a.P];
+              u.p = static_cast<const char*>(param_in(q.i));
+              u.po = static_cast<char*>(param_out(q.i));
+              u.at = q.at;
+              const double r = static_cast<double>(rows[q.i]), cc = static_cast<double>(cols[q.i]);
+              u.scale = static_cast<float>(h->lr * (h->adjust == MR_MUON_RATIO ? std::sqrt(std::max(1.0, r / cc)) : 0.2 * std::sqrt(std::max(r, cc))));
+              u.turned = z.turned;
+            }
+            ++a.P;
+          }
+          if (a.P == 0) continue;
+          a.pieces = pieces;
+          a.ca = static_cast<float>(k3[0]);
+          a.cb = static_cast<float>(k3[1]);
+          a.cc = static_cast<float>(k3[2]);
+          if (final) {
+            la.master = in->master;
+            la.master_out = out->master;
+            la.clip = clip;
+            la.keep = static_cast<float>(1.0 - h->lr * h->weight_decay);
+            e = mr::launch_ns_last(la, dtype, tile, st);
+          } else {
+            e = mr::launch_ns(a, static_cast<mr::NsKind>(kind), tile, st);
+          }
+          if (e != hipSuccess) break;
+        }
+    }
+    if (e != hipSuccess) return hip_fail(e);
+  }
+  return MR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -606,6 +884,17 @@ mr_status mr_preference_loss(const float* logp, const float* ref_logp, size_t ro
                              const mr_preference_hyper* hyper, float* record, float* margins, float* dlogp, mr_stream stream) {
   return guarded([&] {
     return preference_loss(logp, ref_logp, rows, offsets, pairs, hyper, record, margins, dlogp, reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+size_t mr_muon_workspace_bytes(const uint64_t* rows, const uint64_t* cols, int P, int products) { return muon_workspace(rows, cols, P, products); }
+
+mr_status mr_muon_step(const void* const* params, const void* const* grads, const uint64_t* rows, const uint64_t* cols, int P,
+                       mr_dtype dtype, mr_dtype grad_dtype, const mr_muon_state* state, void* const* params_out,
+                       const mr_muon_state* state_out, const mr_muon_hyper* hyper, const float* clip, mr_stream stream) {
+  return guarded([&] {
+    return muon_step(params, grads, rows, cols, P, dtype, grad_dtype, state, params_out, state_out, hyper, clip,
+                     reinterpret_cast<hipStream_t>(stream));
   });
 }
 

@@ -342,6 +342,47 @@ mr_status mr_adamw_step(const void* const* params, const void* const* grads, con
                         const mr_adamw_state* state_out, const mr_adamw_hyper* hyper, const float* clip, mr_stream stream);
 
 /*
+ * mr_muon_step -- one Muon step over a list of matrices: momentum, orthogonalisation by Newton-Schulz products, update.
+ *
+ * For every matrix of rows[i] x cols[i], with f = clip[1] (1 without clip),
+ *     g = f * grad,   m' = momentum*m + (1-momentum)*g,   u = momentum*m' + (1-momentum)*g (nesterov) or m'
+ *     X = u / max(|u|, eps)  (Frobenius norm),  steps times:  X = (a I + b X X^T + c (X X^T)^2) X
+ *     p' = (1 - lr*weight_decay)*p - lr*s*X,   s = sqrt(max(1, rows/cols)) (MR_MUON_RATIO) or 0.2 sqrt(max(rows, cols)) (MR_MUON_RMS)
+ *
+ *  params, grads  host arrays of P device pointers to row-major matrices, as for mr_adamw_step (types, alignment, NULL params
+ *           with a master copy and params_out).  rows[i], cols[i] <= 65536, rows[i]*cols[i] <= 2^33, either may be 0.
+ *  state    momentum and master: floats, laid out as mr_adamw_state_elems says (counts rows[i]*cols[i]), 256-byte aligned;
+ *           elements between matrices become 0.  master NULL: none; with it, p is read from master and written to both.
+ *  params_out, state_out  where results go; NULL: in place.  Each output may be its own input exactly; any other overlap
+ *           -> MR_ERR_ALIAS.
+ *  hyper    momentum in [0, 1), eps from 2^-114, lr, weight_decay and eps finite.  steps 1 to 16.  coefficients: host array of
+ *           {a, b, c} for every step; NULL: 3.4445, -4.775, 2.0315.  Polynomials that take a singular value of X past 3.8, or P = a I
+ *           + b A + c A^2 past 15, -> MR_ERR_INVALID_ARG.
+ *           products = 16: operands of the products rounded to fp16 (held times 2^12, sums fp32); X is then off by 1e-3 to 2e-2
+ *           of its norm, the more the lower its rank; 32: operands in two fp16 pieces, three products for one; off as fp32 is.
+ *  clip     device, mr_grad_norm's 3 floats, or NULL.  Where clip[2] is 0 the step is not taken: outputs are the inputs.
+ *  A gradient or momentum that is not finite gives NaN in its own matrix only.
+ *  Matrices are worked off up to 32 at a time, in the stream's library workspace (see mr_set_workspace), about five to ten bytes
+ *  an element for products = 16 and twice that for 32, up to 2 GiB or what the largest matrix takes.  mr_muon_workspace_bytes: bytes that one
+ *  bound by the caller needs for a list (0: invalid arguments).  hyper is read on the host: a graph repeats its lr.
+ */
+typedef enum mr_muon_adjust { MR_MUON_RATIO = 0, MR_MUON_RMS = 1 } mr_muon_adjust;
+typedef struct mr_muon_state {
+  float* momentum;
+  float* master;
+} mr_muon_state;
+typedef struct mr_muon_hyper {
+  double lr, momentum, weight_decay, eps;
+  const double* coefficients; /* host, 3 * steps, or NULL */
+  int steps, nesterov, products;
+  mr_muon_adjust adjust;
+} mr_muon_hyper;
+size_t mr_muon_workspace_bytes(const uint64_t* rows, const uint64_t* cols, int P, int products);
+mr_status mr_muon_step(const void* const* params, const void* const* grads, const uint64_t* rows, const uint64_t* cols, int P,
+                       mr_dtype dtype, mr_dtype grad_dtype, const mr_muon_state* state, void* const* params_out,
+                       const mr_muon_state* state_out, const mr_muon_hyper* hyper, const float* clip, mr_stream stream);
+
+/*
  * Losses on logits: log-probabilities of target tokens with their gradient, a clipped policy loss and a preference loss.
  *
  * Logits are `rows` rows (tokens, of any number of packed sequences) of `cols` elements (the vocabulary) of `dtype` (MR_BF16,
