@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256) void orient(OrientArgs a) {
 // 16 bytes; chunk c of row r lies at place c ^ swizzle(r), so that the rows a wave reads at once fall on different banks.  (The
 // hardware writes a wave's 64 chunks one after another: the lane that fills a place fetches the chunk that belongs there.)
 constexpr int kRow = kNsK;  // halves of an LDS row
-__device__ __forceinline__ uint32_t swizzle(uint32_t r) { return r & 7; }
+__device__ __forceinline__ uint32_t swizzle(uint32_t r) { return r >> 1 & 7; }
 
 // Rows [0, R) of an operand's tile, 64 columns, by all waves of the workgroup.
 template <int R, int Waves>
@@ -181,12 +181,12 @@ struct Where {  // a workgroup's tile
 };
 template <int BM, int BN>
 __device__ __forceinline__ Where tile_of(const NsArgs& a, bool symmetric) {
-  // neighbouring tiles on one XCD, whose L2 then holds their operands
-  const uint32_t total = gridDim.x, per = total / kXcds, rest = total % kXcds, x = blockIdx.x % kXcds, k = blockIdx.x / kXcds;
-  const uint32_t t = x * per + (x < rest ? x : rest) + k;
   Where w;
-  w.i = __builtin_amdgcn_readfirstlane(entry_of(a.tile_prefix, a.P, t));
-  const uint32_t q = t - a.tile_prefix[w.i];
+  w.i = __builtin_amdgcn_readfirstlane(entry_of(a.tile_prefix, a.P, blockIdx.x));
+  // neighbouring tiles of a matrix on one XCD, whose L2 then holds their operands; every matrix over all XCDs
+  const uint32_t first = a.tile_prefix[w.i], total = a.tile_prefix[w.i + 1] - first, b = blockIdx.x - first;
+  const uint32_t per = total / kXcds, rest = total % kXcds, x = b % kXcds;
+  const uint32_t q = x * per + (x < rest ? x : rest) + b / kXcds;
   const uint32_t tm = (a.p[w.i].ldct + BM - 1) / BM, tn = (a.p[w.i].ldc + BN - 1) / BN;
   if (symmetric) {  // the lower triangle, row by row
     uint32_t r = static_cast<uint32_t>((__builtin_sqrtf(8.0f * q + 1.0f) - 1.0f) * 0.5f);
@@ -210,6 +210,16 @@ struct Tile {
   static constexpr int kHalves = (BM + BN) * kRow;  // of a stage
   f32x16 acc[kMi][kNj];  // block (i, j), transposed: lane l has row l % 32, columns 8 (e / 4) + 4 (l / 32) + e % 4
 
+  // Two arrays, not one: so the compiler knows that a stage's reads need not wait for what is on its way to the other.
+  static __device__ __forceinline__ f16* stage0() {
+    __shared__ __attribute__((aligned(16))) f16 s[kHalves];
+    return s;
+  }
+  static __device__ __forceinline__ f16* stage1() {
+    __shared__ __attribute__((aligned(16))) f16 s[kHalves];
+    return s;
+  }
+
   __device__ __forceinline__ void multiply(const f16* lds) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t ra = wave / WC * (BM / WR) + lane % 32, rb = wave % WC * (BN / WC) + lane % 32;
@@ -231,8 +241,8 @@ struct Tile {
 
   // The sum over K columns (an even number of stages), of 1 product or (two pieces) 3, the smaller ones first.
   __device__ __forceinline__ void run(const NsProduct& p, uint32_t ti, uint32_t tj, int pieces) {
-    __shared__ __attribute__((aligned(16))) f16 s0[kHalves];
-    __shared__ __attribute__((aligned(16))) f16 s1[kHalves];
+    f16* const s0 = stage0();
+    f16* const s1 = stage1();
 #pragma unroll
     for (int i = 0; i < kMi; ++i)
 #pragma unroll
@@ -265,24 +275,74 @@ struct Tile {
     }
   }
 
-  // f(row, column, the four values in that row from that column on): everywhere in the tile, past the matrix too.
-  template <class F>
-  __device__ __forceinline__ void each(uint32_t ti, uint32_t tj, F f) {
+  // Results leave through LDS, where each wave turns chunks of kCr x kCc of its part in a place of its own, so that a lane has 8
+  // values that lie together in memory, and 8 lanes 128 bytes (kCr = 64).  A row is kCc / 4 places of 16 bytes; place c of row r
+  // lies at c ^ spread(r): both a wave's writes (32 rows, one place each) and its reads down the columns meet all banks.
+  static constexpr int kCr = BM / WR < 64 ? BM / WR : 64, kCc = BN / WC;
+  static_assert((kCr == 64 && kCc == 64) || (kCr == 32 && kCc == 32), "chunks");
+  static_assert(kCr * kCc * 4 * kWaves <= 4 * kHalves, "room in the stages");
+  static __device__ __forceinline__ uint32_t place(uint32_t r, uint32_t c) {
+    return r * kCc + (((c / 4) ^ ((r ^ r >> 3) & (kCc / 4 - 1))) * 4) + c % 4;
+  }
+
+  // row(r, c, v): 8 values of row r from column c on, which it may change; column(r, c, v): 8 values of column c from row r on.
+  template <bool Rows, bool Columns, class R, class C>
+  __device__ __forceinline__ void leave(uint32_t ti, uint32_t tj, R row, C column) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t r0 = ti * BM + wave / WC * (BM / WR) + lane % 32, c0 = tj * BN + wave % WC * (BN / WC) + 4 * (lane / 32);
+    float* lds = reinterpret_cast<float*>(wave < kWaves / 2 ? stage0() : stage1()) + wave % (kWaves / 2) * (kHalves / kWaves);
+    const uint32_t r0 = ti * BM + wave / WC * (BM / WR), c0 = tj * BN + wave % WC * (BN / WC);
+    __syncthreads();  // the stages have been read
 #pragma unroll
-    for (int i = 0; i < kMi; ++i)
+    for (int h = 0; h < kMi * 32 / kCr; ++h) {
 #pragma unroll
-      for (int j = 0; j < kNj; ++j)
+      for (int i = 0; i < kCr / 32; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v[4];
+        for (int j = 0; j < kNj; ++j)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = acc[i][j][4 * e + q];
-          f(r0 + i * 32, c0 + j * 32 + 8 * e, v);
+          for (int e = 0; e < 4; ++e) {
+            typedef float f32x4 __attribute__((ext_vector_type(4)));
+            const f32x16& x = acc[h * (kCr / 32) + i][j];
+            *reinterpret_cast<f32x4*>(lds + place(i * 32 + lane % 32, j * 32 + 8 * e + 4 * (lane / 32))) =
+                f32x4{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]};
+          }
+      if constexpr (Rows) {
+#pragma unroll 2
+        for (int k = 0; k < kCr * kCc / 512; ++k) {
+          const uint32_t r = k * (512 / kCc) + lane / (kCc / 8), c = lane % (kCc / 8) * 8;
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = lds[place(r, c + q / 4 * 4) + q % 4];
+          row(r0 + h * kCr + r, c0 + c, v);
+          if constexpr (Columns)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) lds[place(r, c + q / 4 * 4) + q % 4] = v[q];
         }
+      }
+      if constexpr (Columns) {
+#pragma unroll 2
+        for (int k = 0; k < kCr * kCc / 512; ++k) {
+          const uint32_t c = k * (512 / kCr) + lane / (kCr / 8), r = lane % (kCr / 8) * 8;
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = lds[place(r + q, c)];
+          column(r0 + h * kCr + r, c0 + c, v);
+        }
+      }
+    }
   }
 };
+
+// 8 values in fp16 (the rest of them in a second piece) to `at`.
+__device__ __forceinline__ void store8_pieces(f16* at, size_t piece, int pieces, float (&v)[8]) {
+  f16x8 hi, lo;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    hi[q] = static_cast<f16>(v[q]);
+    lo[q] = static_cast<f16>(v[q] - static_cast<float>(hi[q]));
+  }
+  *reinterpret_cast<f16x8*>(at) = hi;
+  if (pieces == 2) *reinterpret_cast<f16x8*>(at + piece) = lo;
+}
 
 template <NsKind Kind, int BM, int BN, int WR, int WC>
 __global__ __launch_bounds__(WR* WC * 64) void ns_product(NsArgs a) {
@@ -293,45 +353,34 @@ __global__ __launch_bounds__(WR* WC * 64) void ns_product(NsArgs a) {
   t.run(p, w.ti, w.tj, a.pieces);
   const size_t c_piece = static_cast<size_t>(p.M) * p.ldc, ct_piece = static_cast<size_t>(p.N) * p.ldct;
   const size_t a_piece = static_cast<size_t>(p.M) * p.K;
-  t.each(w.ti, w.tj, [&](uint32_t r, uint32_t c, float (&v)[4]) {
-    if constexpr (Kind == kNsPoly) {
-      float add[4] = {};
-      if (r < p.M && c < p.K) {  // P's columns are A's
-        for (int s = 0; s < a.pieces; ++s) {
-          const f16x4 x = *reinterpret_cast<const f16x4*>(p.a + s * a_piece + static_cast<size_t>(r) * p.K + c);
+  const bool both = !kSym || w.ti != w.tj;
+  t.template leave<true, true>(
+      w.ti, w.tj,
+      [&](uint32_t r, uint32_t c, float (&v)[8]) {
+        const bool in = r < p.M && c < p.ldc;
+        if constexpr (Kind == kNsPoly) {
+          float add[8] = {};
+          if (in) {  // P's columns are A's
+            for (int s = 0; s < a.pieces; ++s) {
+              const f16x8 x = *reinterpret_cast<const f16x8*>(p.a + s * a_piece + static_cast<size_t>(r) * p.K + c);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) add[q] += static_cast<float>(x[q]);
+              for (int q = 0; q < 8; ++q) add[q] += static_cast<float>(x[q]);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = a.cb * add[q] + a.cc * (v[q] * kDown) + (r == c + q ? a.ca * kUp : 0.0f);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] *= kDown;
         }
-      }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = a.cb * add[q] + a.cc * (v[q] * kDown) + (r == c + q ? a.ca * kUp : 0.0f);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] *= kDown;
-    }
-    f16x4 hi, lo;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (c + q >= p.N || r >= p.M) v[q] = 0.0f;  // the columns past the matrix, of C and of its transpose
-      hi[q] = static_cast<f16>(v[q]);
-      lo[q] = static_cast<f16>(v[q] - static_cast<float>(hi[q]));
-    }
-    if (r < p.M && c < p.ldc) {
-      f16* at = p.c + static_cast<size_t>(r) * p.ldc + c;
-      *reinterpret_cast<f16x4*>(at) = hi;
-      if (a.pieces == 2) *reinterpret_cast<f16x4*>(at + c_piece) = lo;
-    }
-    if ((!kSym || w.ti != w.tj) && r < p.ldct) {
-      f16* base = kSym ? p.c : p.ct;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (c + q < p.N) {
-          f16* at = base + static_cast<size_t>(c + q) * p.ldct + r;
-          *at = hi[q];
-          if (a.pieces == 2) at[ct_piece] = lo[q];
-        }
-    }
-  });
+        for (int q = 0; q < 8; ++q)
+          if (c + q >= p.N || r >= p.M) v[q] = 0.0f;  // what lies past the matrix, in C and in its transpose
+        if (in) store8_pieces(p.c + static_cast<size_t>(r) * p.ldc + c, c_piece, a.pieces, v);
+      },
+      [&](uint32_t r, uint32_t c, float (&v)[8]) {
+        if (both && r < p.ldct && c < p.N) store8_pieces((kSym ? p.c : p.ct) + static_cast<size_t>(c) * p.ldct + r, ct_piece, a.pieces, v);
+      });
 }
 
 // The last product of the last step, which updates the parameters instead of being stored.
@@ -344,18 +393,27 @@ __global__ __launch_bounds__(WR* WC * 64) void ns_last(NsLastArgs a) {
   Tile<BM, BN, WR, WC> t;
   t.run(p, w.ti, w.tj, a.s.pieces);
   const float by = u.scale * kDown * kDown;
-  t.each(w.ti, w.tj, [&](uint32_t r, uint32_t c, float (&v)[4]) {
-    if (r >= p.M) return;
+  // n (1 to 8) of the values v belong to the matrix, from its element e on
+  auto update = [&](size_t e, int n, const float (&v)[8]) {
+    float x[8];
+    if (a.master)
+      widen(load_part<EFp32, 8, true>(reinterpret_cast<const char*>(a.master + u.at + e), n), x);
+    else
+      widen(load_part<T, 8, true>(u.p + e * T::kSize, n), x);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (c + q >= p.N) continue;
-      const size_t e = u.turned ? static_cast<size_t>(c + q) * p.M + r : static_cast<size_t>(r) * p.N + c + q;
-      const float old = a.master ? a.master[u.at + e] : load1<T>(u.p + e * T::kSize);
-      const float now = clip.take ? a.keep * old - by * v[q] : old;
-      if (a.master) a.master_out[u.at + e] = now;
-      store1<T>(u.po + e * T::kSize, now);
-    }
-  });
+    for (int q = 0; q < 8; ++q) x[q] = clip.take ? a.keep * x[q] - by * v[q] : x[q];
+    if (a.master) store_part<EFp32, 8, true>(reinterpret_cast<char*>(a.master_out + u.at + e), x, n);
+    store_part<T, 8, true>(u.po + e * T::kSize, x, n);
+  };
+  auto left = [](uint32_t at, uint32_t end) { return end - at < 8 ? static_cast<int>(end - at) : 8; };
+  if (u.turned)
+    t.template leave<false, true>(w.ti, w.tj, [](uint32_t, uint32_t, float (&)[8]) {}, [&](uint32_t r, uint32_t c, float (&v)[8]) {
+      if (r < p.M && c < p.N) update(static_cast<size_t>(c) * p.M + r, left(r, p.M), v);
+    });
+  else
+    t.template leave<true, false>(w.ti, w.tj, [&](uint32_t r, uint32_t c, float (&v)[8]) {
+      if (r < p.M && c < p.N) update(static_cast<size_t>(r) * p.N + c, left(c, p.N), v);
+    }, [](uint32_t, uint32_t, float (&)[8]) {});
 }
 
 template <NsKind Kind>

@@ -759,7 +759,10 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
                    static_cast<int>(gdtype), h->products, master ? 1 : 0, static_cast<unsigned long long>(g.bytes));
     hipError_t e = mr::launch_momentum(mo, gdtype, st);
     if (e == hipSuccess) e = mr::launch_orient(od, gdtype, st);
-    // one launch for the matrices of each tile size
+    // one launch for the matrices of each tile size; those of the longest sums first, so that the short tiles fill the end
+    uint32_t order[mr::kMuonMats];
+    for (uint32_t k = 0; k < mo.P; ++k) order[k] = k;
+    std::stable_sort(order, order + mo.P, [&](uint32_t x, uint32_t y) { return mats[x].s.n > mats[y].s.n; });
     for (int step = 0; step < h->steps && e == hipSuccess; ++step) {
       const double* k3 = coef + 3 * step;
       for (int kind = mr::kNsGram; kind <= mr::kNsStep && e == hipSuccess; ++kind)
@@ -767,8 +770,8 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
           mr::NsLastArgs la{};
           mr::NsArgs& a = la.s;
           const bool final = kind == mr::kNsStep && step + 1 == h->steps;
-          for (uint32_t k = 0; k < mo.P; ++k) {
-            const Mat& q = mats[k];
+          for (uint32_t o = 0; o < mo.P; ++o) {
+            const Mat& q = mats[order[o]];
             const MuonShape& z = q.s;
             if (mr::ns_tile(z.m, z.n) != tile) continue;
             mr::NsProduct& p = a.p[a.P];
