@@ -146,12 +146,13 @@ hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st);
 // ------------------------------------------------------------------------------------------------ Muon
 //
 // A matrix of rows x cols is orthogonalised as X, m x n with m <= n: itself, or its transpose where rows > cols.  The
-// stream's workspace holds, in fp16 and each as `pieces` matrices after one another, X [m][ldn], its transpose [n][ldm] twice (a
+// stream's workspace holds, in fp16, in panels of kNsK columns and each as `pieces` matrices after one another, X [m][ldn], its transpose [n][ldm] twice (a
 // product reads one and writes the other), A = X X^T and P = a I + b A + c A^2 [m][ldm]; ldm and ldn are m and n rounded up to
-// two of a product's stages (ns_padded), and columns past m and n are zero.
+// four of a product's stages (ns_padded), and columns past m and n are zero.
 constexpr int kMuonMats = 32;       // matrices of one launch
-constexpr uint32_t kNsK = 64;       // columns that a product takes at a time: a stage
-__host__ __device__ inline uint32_t ns_padded(uint32_t n) { return (n + 2 * kNsK - 1) / (2 * kNsK) * (2 * kNsK); }
+constexpr uint32_t kNsK = 32;       // columns that a product takes at a time: a stage
+constexpr uint32_t kNsPad = 4 * kNsK;
+__host__ __device__ inline uint32_t ns_padded(uint32_t n) { return (n + kNsPad - 1) / kNsPad * kNsPad; }
 constexpr int kNsShift = 12;        // matrices are held times 2^12
 constexpr uint32_t kMomentumTile = 4096;  // elements
 struct MomentumArgs {
@@ -185,14 +186,14 @@ struct OrientArgs {
   float mu, c;
   int nesterov, pieces;
 };
-// C = A B^T with A [M][lda], B [N][ldb] over K columns, and what becomes of it:
+// C = A B^T with A [M][K], B [N][K], and what becomes of it:
 enum NsKind { kNsGram, kNsPoly, kNsStep, kNsLast };
 struct NsProduct {
   const _Float16* a;
   const _Float16* b;
   _Float16* c;       // [M][ldc]; kNsLast: unused
   _Float16* ct;      // [N][ldct], the transpose (kNsStep)
-  uint32_t M, N, K;    // K: padded; lda = ldb = K
+  uint32_t M, N, K;    // K: padded
   uint32_t ldc, ldct;  // N and M padded: the tiles cover them
 };
 struct NsArgs {

@@ -29,6 +29,10 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kUp = 1 << kNsShift, kDown = 1.0f / (1 << kNsShift);
 
+// A matrix of `rows` rows lies in panels of 32 columns, each panel's rows after one another (64 bytes a row): what a product
+// fetches at a time is one run of memory, and no stride of a power of two.
+__device__ __forceinline__ size_t in_panels(size_t rows, uint32_t r, uint32_t c) { return (c / kNsK * rows + r) * kNsK + c % kNsK; }
+
 // The matrix whose tiles hold tile t.
 __device__ __forceinline__ uint32_t entry_of(const uint32_t* prefix, uint32_t P, uint32_t t) {
   const uint32_t lane = threadIdx.x & 63;
@@ -133,46 +137,46 @@ __global__ __launch_bounds__(256) void orient(OrientArgs a) {
       u = update_of(a.m[a.at[i] + e], clip.f * load1<G>(a.g[i] + e * G::kSize), a.mu, a.c, a.nesterov) * inv;
     }
     tile[k * 4 + y][x] = u;
-    if (r < rows) store_pieces(a.direct[i] + static_cast<size_t>(r) * ld_direct + c, static_cast<size_t>(rows) * ld_direct, a.pieces, u);
+    if (r < rows) store_pieces(a.direct[i] + in_panels(rows, r, c), static_cast<size_t>(rows) * ld_direct, a.pieces, u);
   }
   __syncthreads();
 #pragma unroll 4
   for (uint32_t k = 0; k < 16; ++k) {
     const uint32_t c = c0 + k * 4 + y, r = r0 + x;
-    if (c < cols) store_pieces(a.turned[i] + static_cast<size_t>(c) * ld_turned + r, static_cast<size_t>(cols) * ld_turned, a.pieces, tile[x][k * 4 + y]);
+    if (c < cols) store_pieces(a.turned[i] + in_panels(cols, c, r), static_cast<size_t>(cols) * ld_turned, a.pieces, tile[x][k * 4 + y]);
   }
 }
 
 // ------------------------------------------------------------------------------------------- products
 //
-// A workgroup of WR x WC waves makes a BM x BN tile; a wave holds its part of it as 32 x 32 blocks in accumulators.  The operands'
-// next 64 columns go from memory straight to LDS while the current ones are multiplied.  In LDS a row of 64 is 8 chunks of
-// 16 bytes; chunk c of row r lies at place c ^ swizzle(r), so that the rows a wave reads at once fall on different banks.  (The
-// hardware writes a wave's 64 chunks one after another: the lane that fills a place fetches the chunk that belongs there.)
-constexpr int kRow = kNsK;  // halves of an LDS row
-__device__ __forceinline__ uint32_t swizzle(uint32_t r) { return r >> 1 & 7; }
+// A workgroup of WR x WC waves makes a BM x BN tile; a wave holds its part of it as 32 x 32 blocks in accumulators.  The operands
+// go from memory straight to LDS, in stages of 32 columns on a ring of 4: three stages are on their way while one is
+// multiplied, so that a wait finds a load that was issued two stages' products ago.  In LDS a row of a stage is 4 chunks of 16 bytes;
+// chunk c of row r lies at place c ^ swizzle(r), so that the 16 rows that are read at once fall on all 64 banks.  (The hardware
+// writes a wave's 64 chunks one after another: the lane that fills a place fetches the chunk that belongs there.)
+constexpr int kStages = 4, kRow = kNsK;  // halves of an LDS row
+__device__ __forceinline__ uint32_t swizzle(uint32_t r) { return r >> 2 & 3; }
 
-// Rows [0, R) of an operand's tile, 64 columns, by all waves of the workgroup.
+// Rows [0, R) of an operand's tile, one stage, by all waves of the workgroup.  The buffer ends with the matrix's rows: past them
+// the hardware fills in zeros.
 template <int R, int Waves>
 struct Fetch {
-  static constexpr int kLoads = R / 8 / Waves;
-  static_assert(R % (8 * Waves) == 0, "whole loads");
-  uint32_t off[kLoads];  // bytes
-  __device__ Fetch(uint32_t rows_left, uint32_t ld) {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t r = (i * Waves + wave) * 8 + lane / 8;
-      const uint32_t row = r < rows_left ? r : rows_left - 1;  // rows past the matrix: its last one; their results are not used
-      off[i] = (row * ld + ((lane % 8) ^ swizzle(r)) * 8) * 2;
-    }
+  static constexpr int kLoads = R / 16 / Waves;
+  static_assert(R % (16 * Waves) == 0, "whole loads");
+  int off;    // bytes, of the first load; a further one lies 16 * Waves rows on
+  int bytes;  // of the tile's rows in a panel
+  __device__ explicit Fetch(uint32_t rows_left) {
+    const uint32_t lane = threadIdx.x & 63, r = (threadIdx.x >> 6) * 16 + lane / 4;
+    off = static_cast<int>((r * kNsK + ((lane % 4) ^ swizzle(r)) * 8) * 2);
+    bytes = static_cast<int>((rows_left < R ? rows_left : R) * kNsK * 2);
   }
-  __device__ __forceinline__ void issue(const char* base, f16* lds) const {
+  __device__ __forceinline__ void issue(const f16* base, f16* lds) const {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<f16*>(base), 0, bytes, 0x00020000);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + off[i]),
-                                       (__attribute__((address_space(3))) void*)(lds + (i * Waves + wave) * 8 * kRow), 16, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + (i * Waves + wave) * 16 * kRow), 16,
+                                               off + i * Waves * 16 * kRow * 2, 0, 0, 0);
   }
 };
 
@@ -210,69 +214,95 @@ struct Tile {
   static constexpr int kHalves = (BM + BN) * kRow;  // of a stage
   f32x16 acc[kMi][kNj];  // block (i, j), transposed: lane l has row l % 32, columns 8 (e / 4) + 4 (l / 32) + e % 4
 
-  // Two arrays, not one: so the compiler knows that a stage's reads need not wait for what is on its way to the other.
-  static __device__ __forceinline__ f16* stage0() {
-    __shared__ __attribute__((aligned(16))) f16 s[kHalves];
-    return s;
-  }
-  static __device__ __forceinline__ f16* stage1() {
+  // Arrays of their own: so the compiler knows that a stage's reads need not wait for what is on its way to another.
+  template <int S>
+  static __device__ __forceinline__ f16* stage() {
     __shared__ __attribute__((aligned(16))) f16 s[kHalves];
     return s;
   }
 
-  __device__ __forceinline__ void multiply(const f16* lds) {
+  // A wave's operands of 16 columns.
+  struct Part {
+    f16x8 x[kMi], y[kNj];
+  };
+  __device__ __forceinline__ void read(Part& p, const f16* lds, int k) const {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t ra = wave / WC * (BM / WR) + lane % 32, rb = wave % WC * (BN / WC) + lane % 32;
 #pragma unroll
-    for (int k = 0; k < static_cast<int>(kNsK) / 16; ++k) {
-      f16x8 x[kMi], y[kNj];
+    for (int i = 0; i < kMi; ++i)
+      p.x[i] = *reinterpret_cast<const f16x8*>(lds + (ra + i * 32) * kRow + ((2 * k + lane / 32) ^ swizzle(ra)) * 8);
 #pragma unroll
-      for (int i = 0; i < kMi; ++i)
-        x[i] = *reinterpret_cast<const f16x8*>(lds + (ra + i * 32) * kRow + ((2 * k + lane / 32) ^ swizzle(ra)) * 8);
+    for (int j = 0; j < kNj; ++j)
+      p.y[j] = *reinterpret_cast<const f16x8*>(lds + (BM + rb + j * 32) * kRow + ((2 * k + lane / 32) ^ swizzle(rb)) * 8);
+  }
+  __device__ __forceinline__ void multiply(const Part& p) {
 #pragma unroll
-      for (int j = 0; j < kNj; ++j)
-        y[j] = *reinterpret_cast<const f16x8*>(lds + (BM + rb + j * 32) * kRow + ((2 * k + lane / 32) ^ swizzle(rb)) * 8);
+    for (int i = 0; i < kMi; ++i)
 #pragma unroll
-      for (int i = 0; i < kMi; ++i)
-#pragma unroll
-        for (int j = 0; j < kNj; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[j], x[i], acc[i][j], 0, 0, 0);
-    }
+      for (int j = 0; j < kNj; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p.y[j], p.x[i], acc[i][j], 0, 0, 0);
   }
 
-  // The sum over K columns (an even number of stages), of 1 product or (two pieces) 3, the smaller ones first.
+  // The sum over K columns (a multiple of the ring), of 1 product or (two pieces) 3, the smaller ones first.
   __device__ __forceinline__ void run(const NsProduct& p, uint32_t ti, uint32_t tj, int pieces) {
-    f16* const s0 = stage0();
-    f16* const s1 = stage1();
 #pragma unroll
     for (int i = 0; i < kMi; ++i)
 #pragma unroll
       for (int j = 0; j < kNj; ++j) acc[i][j] = f32x16{};
-    const Fetch<BM, kWaves> fa(ti * BM < p.M ? p.M - ti * BM : 1, p.K);
-    const Fetch<BN, kWaves> fb(tj * BN < p.N ? p.N - tj * BN : 1, p.K);
-    const char* a0 = reinterpret_cast<const char*>(p.a + static_cast<size_t>(ti) * BM * p.K);
-    const char* b0 = reinterpret_cast<const char*>(p.b + static_cast<size_t>(tj) * BN * p.K);
-    const size_t a_piece = static_cast<size_t>(p.M) * p.K * 2, b_piece = static_cast<size_t>(p.N) * p.K * 2;
+    if (ti * BM >= p.M || tj * BN >= p.N) return;  // columns past the matrix alone
+    const Fetch<BM, kWaves> fa(p.M - ti * BM);
+    const Fetch<BN, kWaves> fb(p.N - tj * BN);
+    const f16* const a0 = p.a + size_t{ti} * BM * kNsK;
+    const f16* const b0 = p.b + size_t{tj} * BN * kNsK;
+    const size_t a_panel = size_t{p.M} * kNsK, b_panel = size_t{p.N} * kNsK;
     const uint32_t per = p.K / kNsK, steps = pieces == 2 ? 3 * per : per;
-    uint32_t at = 0, seg = 0;  // of the next fetch
+    // where the next stage comes from: with two pieces, hi lo + lo hi + hi hi
+    const f16* a = a0;
+    const f16* b = pieces == 2 ? b0 + per * b_panel : b0;
+    uint32_t ahead = 0;
     auto fetch = [&](f16* s) {
-      const char* a = a0 + (pieces == 2 && seg == 1 ? a_piece : 0) + static_cast<size_t>(at) * kNsK * 2;
-      const char* b = b0 + (pieces == 2 && seg == 0 ? b_piece : 0) + static_cast<size_t>(at) * kNsK * 2;
       fa.issue(a, s);
       fb.issue(b, s + BM * kRow);
-      if (++at == per) at = 0, ++seg;
+      // past the end the last stage is fetched again, which nobody reads: so that every wait counts the same loads
+      const bool more = ++ahead < steps;
+      a += more ? a_panel : 0;
+      b += more ? b_panel : 0;
+      if (pieces == 2) {
+        a = ahead == per ? a0 + per * a_panel : ahead == 2 * per ? a0 : a;
+        b = ahead == per || ahead == 2 * per ? b0 : b;
+      }
     };
-    if (ti * BM >= p.M || tj * BN >= p.N) return;  // columns past the matrix alone
-    fetch(s0);
-    for (uint32_t k = 0; k < steps; k += 2) {
-      __syncthreads();  // this stage has arrived, and the other one has been read
-      fetch(s1);
-      __builtin_amdgcn_sched_barrier(0);  // on their way before the products, not between them
-      multiply(s0);
-      __syncthreads();
-      if (k + 2 < steps) fetch(s0);
+    fetch(stage<0>());
+    fetch(stage<1>());
+    fetch(stage<2>());
+    Part even, odd;
+#pragma unroll
+    for (int i = 0; i < kMi; ++i) odd.x[i] = f16x8{};
+#pragma unroll
+    for (int j = 0; j < kNj; ++j) odd.y[j] = f16x8{};
+    // One stage.  The products of its second half are made after the next barrier, while that stage's first operands are read.
+    auto turn = [&](const f16* now, f16* last) {
+      constexpr int kAhead = 2 * (Fetch<BM, kWaves>::kLoads + Fetch<BN, kWaves>::kLoads);  // loads of the two stages after this one
+      __builtin_amdgcn_s_waitcnt(0x0070 | kAhead);  // vmcnt(kAhead): this stage is here; lgkmcnt(0): the one before it has been read
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      fetch(last);
+      read(even, now, 0);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(s1);
+      multiply(odd);
+      __builtin_amdgcn_sched_barrier(0);
+      read(odd, now, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(even);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    for (uint32_t k = 0; k < steps; k += kStages) {
+      turn(stage<0>(), stage<3>());
+      turn(stage<1>(), stage<0>());
+      turn(stage<2>(), stage<1>());
+      turn(stage<3>(), stage<2>());
     }
+    multiply(odd);
   }
 
   // Results leave through LDS, where each wave turns chunks of kCr x kCc of its part in a place of its own, so that a lane has 8
@@ -280,7 +310,7 @@ struct Tile {
   // lies at c ^ spread(r): both a wave's writes (32 rows, one place each) and its reads down the columns meet all banks.
   static constexpr int kCr = BM / WR < 64 ? BM / WR : 64, kCc = BN / WC;
   static_assert((kCr == 64 && kCc == 64) || (kCr == 32 && kCc == 32), "chunks");
-  static_assert(kCr * kCc * 4 * kWaves <= 4 * kHalves, "room in the stages");
+  static_assert(kCr * kCc * 4 * kWaves <= kStages * 2 * kHalves && kWaves % kStages == 0, "room in the stages");
   static __device__ __forceinline__ uint32_t place(uint32_t r, uint32_t c) {
     return r * kCc + (((c / 4) ^ ((r ^ r >> 3) & (kCc / 4 - 1))) * 4) + c % 4;
   }
@@ -289,7 +319,10 @@ struct Tile {
   template <bool Rows, bool Columns, class R, class C>
   __device__ __forceinline__ void leave(uint32_t ti, uint32_t tj, R row, C column) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    float* lds = reinterpret_cast<float*>(wave < kWaves / 2 ? stage0() : stage1()) + wave % (kWaves / 2) * (kHalves / kWaves);
+    constexpr uint32_t kPer = kWaves / kStages;  // waves whose places share a stage
+    const uint32_t in = wave / kPer;
+    float* lds = reinterpret_cast<float*>(in == 0 ? stage<0>() : in == 1 ? stage<1>() : in == 2 ? stage<2>() : stage<3>()) +
+                 wave % kPer * (kHalves / 2 / kPer);
     const uint32_t r0 = ti * BM + wave / WC * (BM / WR), c0 = tj * BN + wave % WC * (BN / WC);
     __syncthreads();  // the stages have been read
 #pragma unroll
@@ -362,7 +395,7 @@ __global__ __launch_bounds__(WR* WC * 64) void ns_product(NsArgs a) {
           float add[8] = {};
           if (in) {  // P's columns are A's
             for (int s = 0; s < a.pieces; ++s) {
-              const f16x8 x = *reinterpret_cast<const f16x8*>(p.a + s * a_piece + static_cast<size_t>(r) * p.K + c);
+              const f16x8 x = *reinterpret_cast<const f16x8*>(p.a + s * a_piece + in_panels(p.M, r, c));
 #pragma unroll
               for (int q = 0; q < 8; ++q) add[q] += static_cast<float>(x[q]);
             }
@@ -376,10 +409,10 @@ __global__ __launch_bounds__(WR* WC * 64) void ns_product(NsArgs a) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (c + q >= p.N || r >= p.M) v[q] = 0.0f;  // what lies past the matrix, in C and in its transpose
-        if (in) store8_pieces(p.c + static_cast<size_t>(r) * p.ldc + c, c_piece, a.pieces, v);
+        if (in) store8_pieces(p.c + in_panels(p.M, r, c), c_piece, a.pieces, v);
       },
       [&](uint32_t r, uint32_t c, float (&v)[8]) {
-        if (both && r < p.ldct && c < p.N) store8_pieces((kSym ? p.c : p.ct) + static_cast<size_t>(c) * p.ldct + r, ct_piece, a.pieces, v);
+        if (both && r < p.ldct && c < p.N) store8_pieces((kSym ? p.c : p.ct) + in_panels(p.N, c, r), ct_piece, a.pieces, v);
       });
 }
 
