@@ -170,13 +170,11 @@ struct Fetch {
     off = static_cast<int>((r * kNsK + ((lane % 4) ^ swizzle(r)) * 8) * 2);
     bytes = static_cast<int>((rows_left < R ? rows_left : R) * kNsK * 2);
   }
-  __device__ __forceinline__ void issue(const f16* base, f16* lds) const {
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // One of the loads.  `wave` is in a scalar register.
+  __device__ __forceinline__ void issue(const f16* base, f16* lds, uint32_t wave, int i) const {
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<f16*>(base), 0, bytes, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + (i * Waves + wave) * 16 * kRow), 16,
-                                               off + i * Waves * 16 * kRow * 2, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + (i * Waves + wave) * 16 * kRow), 16,
+                                             off + i * Waves * 16 * kRow * 2, 0, 0, 0);
   }
 };
 
@@ -225,21 +223,22 @@ struct Tile {
   struct Part {
     f16x8 x[kMi], y[kNj];
   };
-  __device__ __forceinline__ void read(Part& p, const f16* lds, int k) const {
+  static constexpr int kReads = kMi + kNj, kProducts = kMi * kNj;
+  // The n-th of them from LDS: x0 y0 x1 y1 ..., as the products take them.
+  __device__ __forceinline__ void read(Part& p, const f16* lds, int k, int n) const {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t ra = wave / WC * (BM / WR) + lane % 32, rb = wave % WC * (BN / WC) + lane % 32;
-#pragma unroll
-    for (int i = 0; i < kMi; ++i)
+    const int most = kMi < kNj ? kMi : kNj;
+    const bool is_x = n < 2 * most ? n % 2 == 0 : kMi > kNj;
+    const int i = n < 2 * most ? n / 2 : n - most;
+    if (is_x)
       p.x[i] = *reinterpret_cast<const f16x8*>(lds + (ra + i * 32) * kRow + ((2 * k + lane / 32) ^ swizzle(ra)) * 8);
-#pragma unroll
-    for (int j = 0; j < kNj; ++j)
-      p.y[j] = *reinterpret_cast<const f16x8*>(lds + (BM + rb + j * 32) * kRow + ((2 * k + lane / 32) ^ swizzle(rb)) * 8);
+    else
+      p.y[i] = *reinterpret_cast<const f16x8*>(lds + (BM + rb + i * 32) * kRow + ((2 * k + lane / 32) ^ swizzle(rb)) * 8);
   }
-  __device__ __forceinline__ void multiply(const Part& p) {
-#pragma unroll
-    for (int i = 0; i < kMi; ++i)
-#pragma unroll
-      for (int j = 0; j < kNj; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p.y[j], p.x[i], acc[i][j], 0, 0, 0);
+  __device__ __forceinline__ void product(const Part& p, int n) {
+    const int i = n / kNj, j = n % kNj;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p.y[j], p.x[i], acc[i][j], 0, 0, 0);
   }
 
   // The sum over K columns (a multiple of the ring), of 1 product or (two pieces) 3, the smaller ones first.
@@ -259,9 +258,15 @@ struct Tile {
     const f16* a = a0;
     const f16* b = pieces == 2 ? b0 + per * b_panel : b0;
     uint32_t ahead = 0;
-    auto fetch = [&](f16* s) {
-      fa.issue(a, s);
-      fb.issue(b, s + BM * kRow);
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kLoads = Fetch<BM, kWaves>::kLoads + Fetch<BN, kWaves>::kLoads;  // of a stage
+    auto fetch = [&](f16* s, int i) {
+      if (i < Fetch<BM, kWaves>::kLoads)
+        fa.issue(a, s, wave, i);
+      else
+        fb.issue(b, s + BM * kRow, wave, i - Fetch<BM, kWaves>::kLoads);
+    };
+    auto advance = [&] {
       // past the end the last stage is fetched again, which nobody reads: so that every wait counts the same loads
       const bool more = ++ahead < steps;
       a += more ? a_panel : 0;
@@ -271,30 +276,45 @@ struct Tile {
         b = ahead == per || ahead == 2 * per ? b0 : b;
       }
     };
-    fetch(stage<0>());
-    fetch(stage<1>());
-    fetch(stage<2>());
+    for (f16* s : {stage<0>(), stage<1>(), stage<2>()}) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) fetch(s, i);
+      advance();
+    }
     Part even, odd;
 #pragma unroll
     for (int i = 0; i < kMi; ++i) odd.x[i] = f16x8{};
 #pragma unroll
     for (int j = 0; j < kNj; ++j) odd.y[j] = f16x8{};
-    // One stage.  The products of its second half are made after the next barrier, while that stage's first operands are read.
+    // One stage.  The products of its second half are made after the next barrier, while that stage's first operands are read:
+    // the matrix cores have work on both sides of it.  Reads and fetches are issued between the products, not before them.
     auto turn = [&](const f16* now, f16* last) {
-      constexpr int kAhead = 2 * (Fetch<BM, kWaves>::kLoads + Fetch<BN, kWaves>::kLoads);  // loads of the two stages after this one
-      __builtin_amdgcn_s_waitcnt(0x0070 | kAhead);  // vmcnt(kAhead): this stage is here; lgkmcnt(0): the one before it has been read
+      __builtin_amdgcn_s_waitcnt(0x0070 | (2 * kLoads));  // vmcnt: all but the next two stages' loads are here; lgkmcnt(0): the last is read
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      fetch(last);
-      read(even, now, 0);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(odd);
-      __builtin_amdgcn_sched_barrier(0);
-      read(odd, now, 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(even);
-      __builtin_amdgcn_sched_barrier(0);
+      constexpr int kFirst = (kReads + kLoads + kProducts - 1) / kProducts, kSecond = (kReads + kProducts - 1) / kProducts;
+#pragma unroll
+      for (int n = 0; n < kProducts; ++n) {
+        product(odd, n);
+#pragma unroll
+        for (int o = n * kFirst; o < (n + 1) * kFirst; ++o) {
+          if (o < kReads)
+            read(even, now, 0, o);
+          else if (o < kReads + kLoads)
+            fetch(last, o - kReads);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      advance();
+#pragma unroll
+      for (int n = 0; n < kProducts; ++n) {
+        product(even, n);
+#pragma unroll
+        for (int o = n * kSecond; o < (n + 1) * kSecond; ++o)
+          if (o < kReads) read(odd, now, 1, o);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     };
     for (uint32_t k = 0; k < steps; k += kStages) {
       turn(stage<0>(), stage<3>());
@@ -302,7 +322,8 @@ struct Tile {
       turn(stage<2>(), stage<1>());
       turn(stage<3>(), stage<2>());
     }
-    multiply(odd);
+#pragma unroll
+    for (int n = 0; n < kProducts; ++n) product(odd, n);
   }
 
   // Results leave through LDS, where each wave turns chunks of kCr x kCc of its part in a place of its own, so that a lane has 8
