@@ -360,7 +360,7 @@ struct Tile {
                 f32x4{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]};
           }
       if constexpr (Rows) {
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < kCr * kCc / 512; ++k) {
           const uint32_t r = k * (512 / kCc) + lane / (kCc / 8), c = lane % (kCc / 8) * 8;
           float v[8];
@@ -373,7 +373,7 @@ struct Tile {
         }
       }
       if constexpr (Columns) {
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < kCr * kCc / 512; ++k) {
           const uint32_t c = k * (512 / kCr) + lane / (kCr / 8), r = lane % (kCr / 8) * 8;
           float v[8];
