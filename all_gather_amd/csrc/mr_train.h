@@ -148,10 +148,10 @@ hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st);
 // A matrix of rows x cols is orthogonalised as X, m x n with m <= n: itself, or its transpose where rows > cols.  The
 // stream's workspace holds, in fp16, in panels of kNsK columns and each as `pieces` matrices after one another, X [m][ldn], its transpose [n][ldm] twice (a
 // product reads one and writes the other), A = X X^T and P = a I + b A + c A^2 [m][ldm]; ldm and ldn are m and n rounded up to
-// four of a product's stages (ns_padded), and columns past m and n are zero.
+// three of a product's stages (ns_padded), and columns past m and n are zero.
 constexpr int kMuonMats = 32;       // matrices of one launch
 constexpr uint32_t kNsK = 32;       // columns that a product takes at a time: a stage
-constexpr uint32_t kNsPad = 4 * kNsK;
+constexpr uint32_t kNsPad = 3 * kNsK;
 __host__ __device__ inline uint32_t ns_padded(uint32_t n) { return (n + kNsPad - 1) / kNsPad * kNsPad; }
 constexpr int kNsShift = 12;        // matrices are held times 2^12
 constexpr uint32_t kMomentumTile = 4096;  // elements
@@ -218,7 +218,8 @@ struct NsLastArgs {
   const float* clip;
   float keep;
 };
-uint32_t ns_tile(uint32_t m, uint32_t n);  // rows and columns of a product's tiles for a matrix of this shape
+uint32_t ns_tile(uint32_t m, uint32_t n);  // columns of a product's tiles for a matrix of this shape
+uint32_t ns_tiles(uint32_t tile, uint32_t rows, uint32_t cols, bool symmetric);
 hipError_t launch_momentum(const MomentumArgs& a, mr_dtype gdt, hipStream_t st);
 hipError_t launch_orient(const OrientArgs& a, mr_dtype gdt, hipStream_t st);
 hipError_t launch_ns(const NsArgs& a, NsKind kind, uint32_t tile, hipStream_t st);

@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256) void orient(OrientArgs a) {
   __shared__ float tile[64][65];
   const Clip clip = clip_of(a.clip);
   const uint32_t i = entry_of(a.tile_prefix, a.P, blockIdx.x), t = blockIdx.x - a.tile_prefix[i];
-  const uint32_t rows = a.rows[i], cols = a.cols[i], ld_direct = ns_padded(cols), ld_turned = ns_padded(rows), across = ld_direct / 64;
+  const uint32_t rows = a.rows[i], cols = a.cols[i], ld_direct = ns_padded(cols), ld_turned = ns_padded(rows), across = (ld_direct + 63) / 64;
   const uint32_t r0 = t / across * 64, c0 = t % across * 64, x = threadIdx.x & 63, y = threadIdx.x >> 6;
   const double norm = a.norms[i];
   const double by = norm > a.eps ? norm : norm == norm ? a.eps : norm;  // NaN stays
@@ -137,13 +137,13 @@ __global__ __launch_bounds__(256) void orient(OrientArgs a) {
       u = update_of(a.m[a.at[i] + e], clip.f * load1<G>(a.g[i] + e * G::kSize), a.mu, a.c, a.nesterov) * inv;
     }
     tile[k * 4 + y][x] = u;
-    if (r < rows) store_pieces(a.direct[i] + in_panels(rows, r, c), static_cast<size_t>(rows) * ld_direct, a.pieces, u);
+    if (r < rows && c < ld_direct) store_pieces(a.direct[i] + in_panels(rows, r, c), static_cast<size_t>(rows) * ld_direct, a.pieces, u);
   }
   __syncthreads();
 #pragma unroll 4
   for (uint32_t k = 0; k < 16; ++k) {
     const uint32_t c = c0 + k * 4 + y, r = r0 + x;
-    if (c < cols) store_pieces(a.turned[i] + in_panels(cols, c, r), static_cast<size_t>(cols) * ld_turned, a.pieces, tile[x][k * 4 + y]);
+    if (c < cols && r < ld_turned) store_pieces(a.turned[i] + in_panels(cols, c, r), static_cast<size_t>(cols) * ld_turned, a.pieces, tile[x][k * 4 + y]);
   }
 }
 
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(256) void orient(OrientArgs a) {
 // multiplied, so that a wait finds a load that was issued two stages' products ago.  In LDS a row of a stage is 4 chunks of 16 bytes;
 // chunk c of row r lies at place c ^ swizzle(r), so that the 16 rows that are read at once fall on all 64 banks.  (The hardware
 // writes a wave's 64 chunks one after another: the lane that fills a place fetches the chunk that belongs there.)
-constexpr int kStages = 4, kRow = kNsK;  // halves of an LDS row
+constexpr int kStages = 3, kRow = kNsK;  // halves of an LDS row
 __device__ __forceinline__ uint32_t swizzle(uint32_t r) { return r >> 2 & 3; }
 
 // Rows [0, R) of an operand's tile, one stage, by all waves of the workgroup.  The buffer ends with the matrix's rows: past them
@@ -190,12 +190,14 @@ __device__ __forceinline__ Where tile_of(const NsArgs& a, bool symmetric) {
   const uint32_t per = total / kXcds, rest = total % kXcds, x = b % kXcds;
   const uint32_t q = x * per + (x < rest ? x : rest) + b / kXcds;
   const uint32_t tm = (a.p[w.i].ldct + BM - 1) / BM, tn = (a.p[w.i].ldc + BN - 1) / BN;
-  if (symmetric) {  // the lower triangle, row by row
-    uint32_t r = static_cast<uint32_t>((__builtin_sqrtf(8.0f * q + 1.0f) - 1.0f) * 0.5f);
-    while (r * (r + 1) / 2 > q) --r;
-    while ((r + 1) * (r + 2) / 2 <= q) ++r;
-    w.ti = r;
-    w.tj = q - r * (r + 1) / 2;
+  if (symmetric) {  // tiles that meet the lower triangle, by blocks of BN rows
+    constexpr uint32_t kRatio = BN / BM;
+    uint32_t r = static_cast<uint32_t>((__builtin_sqrtf(8.0f / kRatio * q + 1.0f) - 1.0f) * 0.5f);  // kRatio r (r + 1) / 2 tiles lie before block r
+    while (kRatio * r * (r + 1) / 2 > q) --r;
+    while (kRatio * (r + 1) * (r + 2) / 2 <= q) ++r;
+    const uint32_t in = q - kRatio * r * (r + 1) / 2;
+    w.ti = kRatio * r + in / (r + 1);
+    w.tj = in % (r + 1);
   } else {  // panels of 8 tile rows, column by column
     const uint32_t panel = q / (8 * tn), rows = tm - panel * 8 < 8 ? tm - panel * 8 : 8, in = q - panel * 8 * tn;
     w.ti = panel * 8 + in % rows;
@@ -276,7 +278,7 @@ struct Tile {
         b = ahead == per || ahead == 2 * per ? b0 : b;
       }
     };
-    for (f16* s : {stage<0>(), stage<1>(), stage<2>()}) {
+    for (f16* s : {stage<0>(), stage<1>()}) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) fetch(s, i);
       advance();
@@ -289,61 +291,60 @@ struct Tile {
     // One stage.  The products of its second half are made after the next barrier, while that stage's first operands are read:
     // the matrix cores have work on both sides of it.  Reads and fetches are issued between the products, not before them.
     auto turn = [&](const f16* now, f16* last) {
-      __builtin_amdgcn_s_waitcnt(0x0070 | (2 * kLoads));  // vmcnt: all but the next two stages' loads are here; lgkmcnt(0): the last is read
+      __builtin_amdgcn_s_waitcnt(0x0070 | kLoads);  // vmcnt: all but the next stage's loads are here; lgkmcnt(0): the last one is read
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      constexpr int kFirst = (kReads + kLoads + kProducts - 1) / kProducts, kSecond = (kReads + kProducts - 1) / kProducts;
+      constexpr int kEach = (kReads + kProducts - 1) / kProducts;  // reads beside a product
+      auto beside = [&](int slot) {  // the fetches, evenly over the stage: one that finds the memory pipeline full holds its wave up
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (i * 2 * kProducts / kLoads == slot) fetch(last, i);
+        __builtin_amdgcn_sched_barrier(0);
+      };
 #pragma unroll
       for (int n = 0; n < kProducts; ++n) {
         product(odd, n);
 #pragma unroll
-        for (int o = n * kFirst; o < (n + 1) * kFirst; ++o) {
-          if (o < kReads)
-            read(even, now, 0, o);
-          else if (o < kReads + kLoads)
-            fetch(last, o - kReads);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        for (int o = n * kEach; o < (n + 1) * kEach; ++o)
+          if (o < kReads) read(even, now, 0, o);
+        beside(n);
       }
-      advance();
 #pragma unroll
       for (int n = 0; n < kProducts; ++n) {
         product(even, n);
 #pragma unroll
-        for (int o = n * kSecond; o < (n + 1) * kSecond; ++o)
+        for (int o = n * kEach; o < (n + 1) * kEach; ++o)
           if (o < kReads) read(odd, now, 1, o);
-        __builtin_amdgcn_sched_barrier(0);
+        beside(kProducts + n);
       }
+      advance();
     };
     for (uint32_t k = 0; k < steps; k += kStages) {
-      turn(stage<0>(), stage<3>());
+      turn(stage<0>(), stage<2>());
       turn(stage<1>(), stage<0>());
       turn(stage<2>(), stage<1>());
-      turn(stage<3>(), stage<2>());
     }
 #pragma unroll
     for (int n = 0; n < kProducts; ++n) product(odd, n);
   }
 
-  // Results leave through LDS, where each wave turns chunks of kCr x kCc of its part in a place of its own, so that a lane has 8
-  // values that lie together in memory, and 8 lanes 128 bytes (kCr = 64).  A row is kCc / 4 places of 16 bytes; place c of row r
-  // lies at c ^ spread(r): both a wave's writes (32 rows, one place each) and its reads down the columns meet all banks.
-  static constexpr int kCr = BM / WR < 64 ? BM / WR : 64, kCc = BN / WC;
-  static_assert((kCr == 64 && kCc == 64) || (kCr == 32 && kCc == 32), "chunks");
-  static_assert(kCr * kCc * 4 * kWaves <= kStages * 2 * kHalves && kWaves % kStages == 0, "room in the stages");
+  // Results leave through LDS, where each wave turns 32 rows of its part at a time in a place of its own, so that a lane has 8
+  // values that lie together in memory.  A row is kCc / 4 places of 16 bytes; place c of row r lies at c ^ spread(r): a wave's
+  // writes (32 rows, one place each), its reads along the rows and those down the columns each meet all banks.
+  static constexpr int kCr = 32, kCc = BN / WC;
   static __device__ __forceinline__ uint32_t place(uint32_t r, uint32_t c) {
-    return r * kCc + (((c / 4) ^ ((r ^ r >> 3) & (kCc / 4 - 1))) * 4) + c % 4;
+    return r * kCc + (((c / 4) ^ ((r ^ (r >> 3) << 2) & (kCc / 4 - 1))) * 4) + c % 4;
   }
 
   // row(r, c, v): 8 values of row r from column c on, which it may change; column(r, c, v): 8 values of column c from row r on.
   template <bool Rows, bool Columns, class R, class C>
   __device__ __forceinline__ void leave(uint32_t ti, uint32_t tj, R row, C column) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    constexpr uint32_t kPer = kWaves / kStages;  // waves whose places share a stage
+    constexpr uint32_t kPer = (kWaves + kStages - 1) / kStages;  // waves whose places share a stage
+    static_assert(kPer * kCr * kCc * 4 <= 2 * kHalves, "room in a stage");
     const uint32_t in = wave / kPer;
-    float* lds = reinterpret_cast<float*>(in == 0 ? stage<0>() : in == 1 ? stage<1>() : in == 2 ? stage<2>() : stage<3>()) +
-                 wave % kPer * (kHalves / 2 / kPer);
+    float* lds = reinterpret_cast<float*>(in == 0 ? stage<0>() : in == 1 ? stage<1>() : stage<2>()) + wave % kPer * (kCr * kCc);
     const uint32_t r0 = ti * BM + wave / WC * (BM / WR), c0 = tj * BN + wave % WC * (BN / WC);
     __syncthreads();  // the stages have been read
 #pragma unroll
@@ -407,7 +408,7 @@ __global__ __launch_bounds__(WR* WC * 64) void ns_product(NsArgs a) {
   t.run(p, w.ti, w.tj, a.pieces);
   const size_t c_piece = static_cast<size_t>(p.M) * p.ldc, ct_piece = static_cast<size_t>(p.N) * p.ldct;
   const size_t a_piece = static_cast<size_t>(p.M) * p.K;
-  const bool both = !kSym || w.ti != w.tj;
+  const bool both = !kSym || w.tj < w.ti / (BN / BM);  // else the transpose's places are another tile's, or this one's
   t.template leave<true, true>(
       w.ti, w.tj,
       [&](uint32_t r, uint32_t c, float (&v)[8]) {
@@ -474,7 +475,7 @@ template <NsKind Kind>
 void product(const NsArgs& a, uint32_t tile, hipStream_t st) {
   const dim3 grid(a.tile_prefix[a.P]);
   if (tile == 256)
-    hipLaunchKernelGGL((ns_product<Kind, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((ns_product<Kind, 128, 256, 1, 4>), grid, dim3(256), 0, st, a);
   else if (tile == 128)
     hipLaunchKernelGGL((ns_product<Kind, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
   else
@@ -484,7 +485,7 @@ template <class T>
 void last(const NsLastArgs& a, uint32_t tile, hipStream_t st) {
   const dim3 grid(a.s.tile_prefix[a.s.P]);
   if (tile == 256)
-    hipLaunchKernelGGL((ns_last<T, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((ns_last<T, 128, 256, 1, 4>), grid, dim3(256), 0, st, a);
   else if (tile == 128)
     hipLaunchKernelGGL((ns_last<T, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
   else
@@ -504,6 +505,14 @@ void by_type(mr_dtype dt, F f) {
 }  // namespace
 
 uint32_t ns_tile(uint32_t m, uint32_t) { return m >= 2048 ? 256 : m >= 512 ? 128 : 64; }
+
+uint32_t ns_tiles(uint32_t tile, uint32_t rows, uint32_t cols, bool symmetric) {
+  const uint32_t bm = tile == 256 ? 128 : tile, bn = tile, ratio = bn / bm;
+  const uint32_t tm = (rows + bm - 1) / bm, tn = (cols + bn - 1) / bn;
+  if (!symmetric) return tm * tn;
+  const uint32_t h = tm / ratio;  // whole blocks of bn rows
+  return ratio * h * (h + 1) / 2 + tm % ratio * (h + 1);
+}
 
 hipError_t launch_momentum(const MomentumArgs& a, mr_dtype gdt, hipStream_t st) {
   by_type(gdt, [&](auto g) { hipLaunchKernelGGL((momentum<decltype(g)>), dim3(a.tile_prefix[a.P]), dim3(256), 0, st, a); });

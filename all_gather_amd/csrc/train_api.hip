@@ -734,7 +734,7 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
       od.at[k] = at;
       od.rows[k] = static_cast<uint32_t>(rows[i]);
       od.cols[k] = static_cast<uint32_t>(cols[i]);
-      od.tile_prefix[k + 1] = od.tile_prefix[k] + (z.ldm / 64) * (z.ldn / 64);
+      od.tile_prefix[k + 1] = od.tile_prefix[k] + ((z.ldm + 63) / 64) * ((z.ldn + 63) / 64);
       at += (count(i) + mr::kMxBlock - 1) / mr::kMxBlock * mr::kMxBlock;
     }
     first = g.end;
@@ -775,7 +775,6 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
             const MuonShape& z = q.s;
             if (mr::ns_tile(z.m, z.n) != tile) continue;
             mr::NsProduct& p = a.p[a.P];
-            const uint32_t tm = (z.ldm + tile - 1) / tile, tn = (z.ldn + tile - 1) / tile;
             p.M = z.m;
             p.ldct = z.ldm;
             if (kind == mr::kNsStep) {
@@ -786,7 +785,7 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
               p.c = kind == mr::kNsGram ? q.a : q.p;
               p.N = z.m, p.K = kind == mr::kNsGram ? z.ldn : z.ldm, p.ldc = z.ldm;
             }
-            a.tile_prefix[a.P + 1] = a.tile_prefix[a.P] + (kind == mr::kNsStep ? tm * tn : tm * (tm + 1) / 2);
+            a.tile_prefix[a.P + 1] = a.tile_prefix[a.P] + mr::ns_tiles(tile, z.ldm, kind == mr::kNsStep ? z.ldn : z.ldm, kind != mr::kNsStep);
             if (final) {
               mr::NsUpdate& u = la.u[a.P];
               u.p = static_cast<const char*>(param_in(q.i));
