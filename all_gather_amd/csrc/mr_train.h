@@ -154,13 +154,13 @@ constexpr uint32_t kNsK = 32;       // columns that a product takes at a time: a
 constexpr uint32_t kNsPad = 3 * kNsK;
 __host__ __device__ inline uint32_t ns_padded(uint32_t n) { return (n + kNsPad - 1) / kNsPad * kNsPad; }
 constexpr int kNsShift = 12;        // matrices are held times 2^12
-constexpr uint32_t kMomentumTile = 4096;  // elements
+inline uint32_t momentum_tile(uint64_t n) { return n < uint64_t{1} << 23 ? 4096 : 16384; }  // elements, for n in all
 struct MomentumArgs {
   const char* g[kMuonMats];
   uint64_t n[kMuonMats];
   uint64_t at[kMuonMats];  // first element in the flat state
   uint32_t tile_prefix[kMuonMats + 1];
-  uint32_t P;
+  uint32_t P, tile;
   const float* m;
   float* m_out;
   float* master_out;      // null: none (its elements between matrices become zeros)

@@ -589,25 +589,28 @@ MuonShape muon_shape(uint64_t rows, uint64_t cols, int pieces) {
   s.halves = pieces * (uint64_t{s.m} * s.ldn + 2 * (uint64_t{s.n} * s.ldm) + 2 * (uint64_t{s.m} * s.ldm));
   return s;
 }
-uint32_t momentum_tiles(uint64_t n) { return static_cast<uint32_t>((n + mr::kMomentumTile - 1) / mr::kMomentumTile); }
+uint32_t momentum_tiles(uint64_t n, uint32_t tile) { return static_cast<uint32_t>((n + tile - 1) / tile); }
 
 // Matrices of one workspace: those from `first` on that fit together, and the bytes they take.
 struct MuonGroup {
   int first, end, count;  // count: those that are not empty
   uint64_t bytes;         // of halves, then sums, then norms
   uint64_t sums;
+  uint32_t tile;  // of the momentum's elements
 };
 MuonGroup muon_group(const uint64_t* rows, const uint64_t* cols, int P, int first, int pieces) {
-  MuonGroup g{first, first, 0, 0, 0};
-  uint64_t halves = 0;
+  MuonGroup g{first, first, 0, 0, 0, 0};
+  uint64_t halves = 0, elems = 0;
   for (; g.end < P && g.count < mr::kMuonMats; ++g.end) {
     if (rows[g.end] * cols[g.end] == 0) continue;
     const uint64_t more = muon_shape(rows[g.end], cols[g.end], pieces).halves;
     if (g.count && (halves + more) * 2 > kMuonGroupBytes) break;
     halves += more;
-    g.sums += momentum_tiles(rows[g.end] * cols[g.end]);
+    elems += rows[g.end] * cols[g.end];
     ++g.count;
   }
+  g.tile = mr::momentum_tile(elems);
+  for (int i = first; i < g.end; ++i) g.sums += momentum_tiles(rows[i] * cols[i], g.tile);
   g.bytes = halves * 2 + g.sums * 8 + mr::kMuonMats * 8;
   return g;
 }
@@ -727,7 +730,7 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
       mo.g[k] = static_cast<const char*>(grads[i]);
       mo.n[k] = count(i);
       mo.at[k] = at;
-      mo.tile_prefix[k + 1] = mo.tile_prefix[k] + momentum_tiles(count(i));
+      mo.tile_prefix[k + 1] = mo.tile_prefix[k] + momentum_tiles(count(i), g.tile);
       od.g[k] = mo.g[k];
       od.direct[k] = z.turned ? q.xt[0] : q.x;
       od.turned[k] = z.turned ? q.x : q.xt[0];
@@ -739,6 +742,7 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
     }
     first = g.end;
     if (mo.P == 0) continue;
+    mo.tile = g.tile;
     mo.m = in->momentum;
     mo.m_out = out->momentum;
     mo.master_out = out->master;
