@@ -106,10 +106,14 @@ struct PolicyRow {
   float g;
   double loss, kl, held, w;
 };
-__device__ __forceinline__ PolicyRow policy_row(const LogitArgs& a, size_t row, double logp) {
-  const double w = a.weights ? static_cast<double>(a.weights[row]) : 1.0;
-  const double adv = static_cast<double>(a.adv[row]);
-  const double r = a.old_logp ? static_cast<double>(expf(static_cast<float>(logp - static_cast<double>(a.old_logp[row])))) : logp - logp + 1.0;
+struct PolicyIn {
+  float w, adv, old, ref;
+  __device__ PolicyIn(const LogitArgs& a, size_t row)
+      : w(a.weights ? a.weights[row] : 1.0f), adv(a.adv[row]), old(a.old_logp ? a.old_logp[row] : 0.0f), ref(a.ref_logp ? a.ref_logp[row] : 0.0f) {}
+};
+__device__ __forceinline__ PolicyRow policy_row(const LogitArgs& a, const PolicyIn& in, double logp) {
+  const double w = static_cast<double>(in.w), adv = static_cast<double>(in.adv);
+  const double r = a.old_logp ? static_cast<double>(expf(static_cast<float>(logp - static_cast<double>(in.old)))) : logp - logp + 1.0;
   double near = r < 1.0 - a.clip_lo ? 1.0 - a.clip_lo : r;
   near = near > 1.0 + a.clip_hi ? 1.0 + a.clip_hi : near;
   const double free = -adv * r, held = -adv * near;
@@ -117,7 +121,7 @@ __device__ __forceinline__ PolicyRow policy_row(const LogitArgs& a, size_t row, 
   PolicyRow p;
   double g = cut ? 0.0 : free, k = 0.0;
   if (a.ref_logp) {
-    const float d = static_cast<float>(static_cast<double>(a.ref_logp[row]) - logp);
+    const float d = static_cast<float>(static_cast<double>(in.ref) - logp);
     g -= a.kl * static_cast<double>(expm1f(d));
     k = static_cast<double>(excess(d));
   }
@@ -129,47 +133,81 @@ __device__ __forceinline__ PolicyRow policy_row(const LogitArgs& a, size_t row, 
   return p;
 }
 
-// Workgroups' sums to the record: each leaves four through write-through stores, acknowledged before its arrival is counted,
-// and the one that arrives last adds them all up in their order.  Every lane of the workgroup calls this.
-__device__ __forceinline__ bool arrive_last(uint32_t (*arrived)[64], uint32_t groups) {
-  __shared__ bool last;
-  if (threadIdx.x == 0) {
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    const uint32_t sets = groups < 4 * kNormSets ? 1 : kNormSets, set = blockIdx.x % sets;
-    const uint32_t members = (groups - set + sets - 1) / sets;
-    last = __hip_atomic_fetch_add(&arrived[set][0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == members - 1;
-    if (last && sets > 1)
-      last = __hip_atomic_fetch_add(&arrived[kNormSets][0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == sets - 1;
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  }
-  __syncthreads();
+// Workgroups' sums to the record, in up to 8 sets of workgroups.  Each leaves four through write-through stores, acknowledged
+// before its arrival is counted; the one that arrives last of its set adds the set's up, and the last of those the sets', all
+// in their order.  (One set of 1024: 46 us of a preference loss, most of it one wave's loads after another.)
+__device__ __forceinline__ void leave4(double* p, double v0, double v1, double v2, double v3) {
+  __hip_atomic_store(p, v0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(p + 1, v1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(p + 2, v2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(p + 3, v3, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Counts an arrival after this lane's stores; is it the last of `members`?
+__device__ __forceinline__ bool arrive(uint32_t* count, uint32_t members) {
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  const bool last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == members - 1;
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
   return last;
 }
-// The first wave's sum over all workgroups of their four values; lane 0 to 3 has one each.
-__device__ __forceinline__ double total_of(const double* sums, uint32_t groups) {
-  const uint32_t j = threadIdx.x & 3;
+// A wave's sum of n entries of four values, `stride` entries apart; lane j has value j % 4.  8 loads of a lane are on their way at once.
+__device__ __forceinline__ double sum4(const double* p, uint32_t n, uint32_t stride) {
+  const uint32_t lane = threadIdx.x & 63;
   double s = 0.0;
-  for (uint32_t i = threadIdx.x >> 2; i < groups; i += 16)
-    s += __hip_atomic_load(sums + size_t{i} * 4 + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (uint32_t i0 = lane >> 2; i0 < n; i0 += 128) {
+    double v[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+      const uint32_t i = i0 + 16 * k < n ? i0 + 16 * k : i0;
+      v[k] = __hip_atomic_load(p + size_t{i} * stride * 4 + (lane & 3), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) s += i0 + 16 * k < n ? v[k] : 0.0;
+  }
 #pragma unroll
   for (int m = 32; m >= 4; m >>= 1) s += __shfl_xor(s, m);
   return s;
 }
+// By the first wave of every workgroup, with the sums in its first lane.
 __device__ __forceinline__ void finish_record(double v0, double v1, double v2, double v3, double* sums, uint32_t (*arrived)[64],
-                                              uint32_t groups, float* record, int words) {
-  if (threadIdx.x == 0) {
-    double* p = sums + size_t{blockIdx.x} * 4;
-    __hip_atomic_store(p, v0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(p + 1, v1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(p + 2, v2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(p + 3, v3, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                                              float* record, uint32_t words) {
+  const uint32_t groups = gridDim.x, lane = threadIdx.x;
+  if (lane >= 64) return;
+  const uint32_t sets = groups < 4 * kNormSets ? 1 : kNormSets, set = blockIdx.x % sets, members = (groups - set + sets - 1) / sets;
+  int last = 0;
+  if (lane == 0) {
+    leave4(sums + size_t{blockIdx.x} * 4, v0, v1, v2, v3);
+    last = arrive(&arrived[set][0], members);
   }
-  if (!arrive_last(arrived, groups) || threadIdx.x >= 64) return;
-  const double s = total_of(sums, groups);
-  if (threadIdx.x <= kNormSets) __hip_atomic_store(&arrived[threadIdx.x][0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (static_cast<int>(threadIdx.x) < words) record[threadIdx.x] = static_cast<float>(s);
+  if (!__shfl(last, 0)) return;
+  double s = sum4(sums + size_t{set} * 4, members, sets);
+  if (sets > 1) {
+    double* of_sets = sums + size_t{groups} * 4;
+    if (lane < 4) __hip_atomic_store(of_sets + set * 4 + lane, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = arrive(&arrived[kNormSets][0], 64 * sets) ? 1 : 0;  // (every lane arrives: its own store is acknowledged)
+    if (!__any(last)) return;
+    s = sum4(of_sets, sets, 1);
+  }
+  if (lane <= kNormSets) __hip_atomic_store(&arrived[lane][0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (lane < words) record[lane] = static_cast<float>(s);
 }
+
+// Rows are read in packs on z's 16-byte grid, so the first pack of a row that starts off it holds `off` elements less.
+template <class T>
+__device__ __forceinline__ uint32_t row_off(const char* z) {
+  return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z) & 15u)) / T::kSize;
+}
+// The columns of pack p of a row: `n` (0 or less: none) from `col` on.
+template <int V>
+struct PackAt {
+  size_t col;
+  int n;
+  __device__ PackAt(size_t p, uint32_t off, size_t cols) {
+    const int64_t c = static_cast<int64_t>(p * V) - off, end = c + V < static_cast<int64_t>(cols) ? c + V : static_cast<int64_t>(cols);
+    col = c < 0 ? 0 : static_cast<size_t>(c);
+    n = end - static_cast<int64_t>(col) < 0 ? 0 : static_cast<int>(end - static_cast<int64_t>(col));
+  }
+};
 
 constexpr int kMostWaves = 16;
 
@@ -187,7 +225,7 @@ __global__ __launch_bounds__(1024) void row_stats(LogitArgs a) {
   __shared__ bool last;
   const uint32_t lanes = blockDim.x, lane = threadIdx.x;
   const size_t parts = a.rows * a.splits;
-  const size_t packs = (a.cols + V - 1) / V, per = (packs + a.splits - 1) / a.splits;
+  const size_t packs = a.packs, per = (packs + a.splits - 1) / a.splits;
   double loss = 0.0, kl = 0.0, cut = 0.0, weight = 0.0;
   for (size_t part = blockIdx.x; part < parts; part += gridDim.x) {
     const size_t row = part / a.splits;
@@ -202,23 +240,27 @@ __global__ __launch_bounds__(1024) void row_stats(LogitArgs a) {
       continue;
     }
     const char* z = a.z + row * a.stride * T::kSize;
+    const uint32_t off = row_off<T>(z);
+    const char* grid = z - off * T::kSize;  // where pack 0 would start
     const size_t first = split * per, end = first + per < packs ? first + per : packs;
     Stat st{kNone, 0.0f};
     for (size_t p = first + lane; p < end; p += static_cast<size_t>(lanes) * kStatPacks) {
       float f[kStatPacks * V];
       Raw<T, V> raw[kStatPacks];
-      if (p + static_cast<size_t>(lanes) * (kStatPacks - 1) < end && (p + static_cast<size_t>(lanes) * (kStatPacks - 1) + 1) * V <= a.cols) {
+      const size_t top = p + static_cast<size_t>(lanes) * (kStatPacks - 1);
+      if (top < end && (top + 1) * V <= a.cols + off && (p > 0 || off == 0)) {
 #pragma unroll
-        for (int k = 0; k < kStatPacks; ++k) raw[k] = load_raw<T, V, true>(z + (p + static_cast<size_t>(lanes) * k) * V * T::kSize);
+        for (int k = 0; k < kStatPacks; ++k) raw[k] = load_raw<T, V, true>(grid + (p + static_cast<size_t>(lanes) * k) * 16);
 #pragma unroll
         for (int k = 0; k < kStatPacks; ++k) widen(raw[k], reinterpret_cast<float(&)[V]>(f[k * V]));
       } else {
 #pragma unroll
         for (int k = 0; k < kStatPacks; ++k) {
           const size_t q = p + static_cast<size_t>(lanes) * k;
-          const int n = q >= end ? 0 : a.cols - q * V < V ? static_cast<int>(a.cols - q * V) : V;
+          const PackAt<V> at(q, off, a.cols);
+          const int n = q < end ? at.n : 0;
           float (&g)[V] = reinterpret_cast<float(&)[V]>(f[k * V]);
-          widen(load_part<T, V, true>(z + q * V * T::kSize, n), g);
+          widen(load_part<T, V, true>(z + at.col * T::kSize, n), g);
 #pragma unroll
           for (int i = 0; i < V; ++i)
             if (i >= n) g[i] = kNone;
@@ -266,13 +308,13 @@ __global__ __launch_bounds__(1024) void row_stats(LogitArgs a) {
         a.stats[2 * row + 1] = st.s;
       }
       if constexpr (Policy) {
-        const PolicyRow p = policy_row(a, row, lp);
+        const PolicyRow p = policy_row(a, PolicyIn(a, row), lp);
         if (a.dz) const_cast<float*>(a.dlogp)[row] = p.g;
         loss += p.loss, kl += p.kl, cut += p.held, weight += p.w;
       }
     }
   }
-  if constexpr (Policy) finish_record(loss, kl, cut, weight, a.sums, a.arrived, gridDim.x, a.record, 4);
+  if constexpr (Policy) finish_record(loss, kl, cut, weight, a.sums, a.arrived, a.record, 4);
 }
 
 // ------------------------------------------------------------------------------ gradient of the logits
@@ -284,7 +326,7 @@ template <class T>
 __global__ __launch_bounds__(256) void logit_grad(LogitArgs a) {
   constexpr int V = 16 / T::kSize;
   const uint32_t lanes = blockDim.x, lane = threadIdx.x;
-  const size_t packs = (a.cols + V - 1) / V, run = static_cast<size_t>(lanes) * kGradPacks;
+  const size_t packs = a.packs, run = static_cast<size_t>(lanes) * kGradPacks;
   const size_t runs = (packs + run - 1) / run;
   for (size_t item = blockIdx.x; item < a.rows * runs; item += gridDim.x) {
     const size_t row = item / runs, p0 = item % runs * run + lane;
@@ -292,14 +334,14 @@ __global__ __launch_bounds__(256) void logit_grad(LogitArgs a) {
     const bool live = row_live(a, row, &t);  // (the backward pass has no weights)
     const char* z = a.z + row * a.stride * T::kSize;
     char* dz = a.dz + row * a.dstride * T::kSize;
-    const bool whole = (p0 - lane + run) * V <= a.cols;
+    const uint32_t off = row_off<T>(z);
+    const bool whole = (p0 - lane + run) * V <= a.cols + off && (p0 > lane || off == 0);
     if (!live) {
       const float none[V] = {};
 #pragma unroll
       for (int k = 0; k < kGradPacks; ++k) {
-        const size_t q = p0 + static_cast<size_t>(lanes) * k;
-        const int n = whole ? V : q >= packs ? 0 : a.cols - q * V < V ? static_cast<int>(a.cols - q * V) : V;
-        if (n) store_part<T, V, true>(dz + q * V * T::kSize, none, n);
+        const PackAt<V> at(p0 + static_cast<size_t>(lanes) * k, off, a.cols);
+        if (at.n > 0) store_part<T, V, true>(dz + at.col * T::kSize, none, at.n);
       }
       continue;
     }
@@ -307,31 +349,33 @@ __global__ __launch_bounds__(256) void logit_grad(LogitArgs a) {
 #pragma unroll
     for (int k = 0; k < kGradPacks; ++k) {
       const size_t q = p0 + static_cast<size_t>(lanes) * k;
-      if (whole)
-        raw[k] = load_raw<T, V, true>(z + q * V * T::kSize);
-      else if (q < packs)
-        raw[k] = load_part<T, V, true>(z + q * V * T::kSize, a.cols - q * V < V ? static_cast<int>(a.cols - q * V) : V);
+      if (whole) {
+        raw[k] = load_raw<T, V, true>(z + q * 16 - off * T::kSize);
+      } else {
+        const PackAt<V> at(q, off, a.cols);
+        raw[k] = load_part<T, V, true>(z + at.col * T::kSize, at.n);
+      }
     }
     const float base = base_of(a.stats[2 * row]), g = static_cast<float>(static_cast<double>(a.dlogp[row]) * a.inv_temp);
     const float share = -g / a.stats[2 * row + 1];
 #pragma unroll
     for (int k = 0; k < kGradPacks; ++k) {
-      const size_t q = p0 + static_cast<size_t>(lanes) * k;
-      if (!whole && q >= packs) continue;
+      const PackAt<V> p(p0 + static_cast<size_t>(lanes) * k, off, a.cols);
+      if (!whole && p.n <= 0) continue;
       float f[V];
       widen(raw[k], f);
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = share * power(f[i], base, a.c);
-      const uint64_t at = static_cast<uint64_t>(t) - q * V;
+      const uint64_t at = static_cast<uint64_t>(t) - p.col;
       if (at < V) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if (at == static_cast<uint64_t>(i)) f[i] += g;
       }
       if (whole)
-        store_raw<T, V, true>(dz + q * V * T::kSize, narrow<T, V>(f));
+        store_raw<T, V, true>(dz + p.col * T::kSize, narrow<T, V>(f));
       else
-        store_part<T, V, true>(dz + q * V * T::kSize, f, a.cols - q * V < V ? static_cast<int>(a.cols - q * V) : V);
+        store_part<T, V, true>(dz + p.col * T::kSize, f, p.n);
     }
   }
 }
@@ -340,33 +384,36 @@ __global__ __launch_bounds__(256) void logit_grad(LogitArgs a) {
 //
 // A workgroup holds a row in registers, K packs a lane, and walks the rows.  As each pack's gradient leaves, the next row's
 // pack is loaded into its place, so that reads and writes flow together.  One barrier a row: its words are of alternating
-// sets.  Only the last two of the K strips of packs can pass the row's end (held_row).  Its last pack, if short, is read as the
-// row's last V elements (the first `lo` of which the neighbouring pack has too, so they add nothing to the sums; both store
-// the same bits), and packs past the end are read, and stored, as that one.
+// sets; the next row's target is read a row ahead.  Packs lie on z's 16-byte grid; only the first strip's first pack and
+// the last two of the K strips can pass the row's ends (held_row).  Such a pack is read, and stored, as V whole elements from the
+// nearest end on; those that are another pack's add nothing to the sums, and both store the same bits.
 template <class T, int K>
 __global__ __launch_bounds__(1024) void policy_held(LogitArgs a) {
   constexpr int V = 16 / T::kSize, kEnd = K < 2 ? K : 2;
   __shared__ Stat words[2][kMostWaves];
   __shared__ double sums[4];  // the first lane's
   const uint32_t lanes = blockDim.x, lane = threadIdx.x, nw = lanes / 64;
-  const uint32_t cols = static_cast<uint32_t>(a.cols);
-  uint32_t end_at[kEnd];  // the last strips' columns
-  int end_lo[kEnd];
-#pragma unroll
-  for (int i = 0; i < kEnd; ++i) {
-    const uint32_t col = ((K - kEnd + i) * lanes + lane) * V;
-    end_at[i] = col < cols - V ? col : cols - V;
-    end_lo[i] = static_cast<int>(col - end_at[i] < V ? col - end_at[i] : V);
-  }
-  // a lane's column in strip k, as a part of all lanes and its own: the first rides in scalar registers
-  auto strip = [&](int k) { return k < K - kEnd ? k * lanes * V : 0u; };
-  auto own = [&](int k) { return k < K - kEnd ? lane * V : end_at[k - (K - kEnd)]; };
+  const int last = static_cast<int>(a.cols) - V;  // the last column where a pack can start
+  auto at_end = [](int k) { return k == 0 || k >= K - kEnd; };
+  // Bytes from the row's start to a lane's pack of strip k, as a part of all lanes (scalar) and its own.
+  struct Place {
+    int64_t all;
+    uint32_t own;
+  };
+  auto column = [&](uint32_t off, int k) { return static_cast<int>((k * lanes + lane) * V) - static_cast<int>(off); };
+  auto place = [&](uint32_t off, int k) {
+    if (!at_end(k)) return Place{(static_cast<int64_t>(k * lanes * V) - off) * T::kSize, lane * 16};
+    int c = column(off, k);
+    c = c < last ? c : last;
+    return Place{0, static_cast<uint32_t>(c < 0 ? 0 : c) * T::kSize};
+  };
   if (lane == 0) sums[0] = sums[1] = sums[2] = sums[3] = 0.0;
   Raw<T, V> raw[K];
-  // A row's packs; where there is no row to load, every lane reads one pack of this one.  Loads behind a branch would keep the
-  // packs that leave and those that come in registers of their own.
-  auto load = [&](const char* z, uint32_t some, int k) {
-    raw[k] = load_raw<T, V, true>(z + (size_t{strip(k)} & static_cast<int32_t>(some)) * T::kSize + (own(k) & some) * T::kSize);
+  // A row's packs; where there is no row to load, every lane reads the first pack of this one.  Loads behind a branch would keep
+  // the packs that leave and those that come in registers of their own.
+  auto load = [&](const char* z, uint32_t off, uint32_t some, int k) {
+    const Place p = place(off, k);
+    raw[k] = load_raw<T, V, true>(z + (p.all & static_cast<int32_t>(some)) + (p.own & some));
   };
   const size_t step = gridDim.x;
   uint32_t t_next = 0;
@@ -374,25 +421,33 @@ __global__ __launch_bounds__(1024) void policy_held(LogitArgs a) {
   auto advance = [&](size_t r) {
     for (; r < a.rows && !row_live(a, r, &t_next); r += step) {
       char* dz = a.dz + r * a.dstride * T::kSize;
+      const uint32_t off = row_off<T>(a.z + r * a.stride * T::kSize);
       if (lane == 0 && a.logp) a.logp[r] = 0.0f;
       const float none[V] = {};
 #pragma unroll
-      for (int k = 0; k < K; ++k) store_raw<T, V, true>(dz + size_t{strip(k)} * T::kSize + own(k) * T::kSize, narrow<T, V>(none));
+      for (int k = 0; k < K; ++k) {
+        const Place p = place(off, k);
+        store_raw<T, V, true>(dz + p.all + p.own, narrow<T, V>(none));
+      }
     }
     return r;
   };
   size_t row = advance(blockIdx.x), next = row;
-  uint32_t t = t_next;
-  float zt = 0.0f;
-  if (row < a.rows) zt = load1<T>(a.z + (row * a.stride + t) * T::kSize);
+  uint32_t t = t_next, off = 0;
+  const char* z = a.z;
+  if (row < a.rows) {
+    z += row * a.stride * T::kSize;
+    off = row_off<T>(z);
+  }
 #pragma unroll
-  for (int k = 0; k < K; ++k) load(a.z + (row < a.rows ? row : 0) * a.stride * T::kSize, row < a.rows ? ~0u : 0u, k);
+  for (int k = 0; k < K; ++k) load(z, off, row < a.rows ? ~0u : 0u, k);
   for (uint32_t turn = 0; row < a.rows; row = next, ++turn) {
+    const float zt = load1<T>(z + size_t{t} * T::kSize);
+    const PolicyIn in(a, row);
     next = advance(row + step);
     const uint32_t some = next < a.rows ? ~0u : 0u;
     const char* z_next = a.z + (some ? next : row) * a.stride * T::kSize;
-    float zt_next = 0.0f;
-    if (some) zt_next = load1<T>(z_next + static_cast<size_t>(t_next) * T::kSize);
+    const uint32_t off_next = row_off<T>(z_next);
     char* dz = a.dz + row * a.dstride * T::kSize;
     Stat st{kNone, 0.0f};
 #pragma unroll
@@ -402,12 +457,14 @@ __global__ __launch_bounds__(1024) void policy_held(LogitArgs a) {
       for (int i = 0; i < Raw<T, V>::kWords; ++i) asm volatile("" : "+v"(raw[k].w[i]), "+v"(st.m), "+v"(st.s));
       float f[V];
       widen(raw[k], f);
-      if (k >= K - kEnd) {
-        int lo = end_lo[k >= K - kEnd ? k - (K - kEnd) : 0];
-        asm volatile("" : "+v"(lo));  // compared anew: kept, the comparisons' masks would take 16 scalar registers a strip
+      if (at_end(k)) {
+        // columns of the pack that are its own: from its place on the grid on, V of them
+        const int c = column(off, k), at = c < last ? c < 0 ? 0 : c : last;
+        int from = c - at;
+        asm volatile("" : "+v"(from));  // compared anew in every row: kept, the comparisons' masks would take 16 scalar registers a strip
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (i < lo) f[i] = kNone;
+          if (k == 0 ? i < from || i >= from + V : i < from) f[i] = kNone;
       }
       add_values(st, f, a.c);
     }
@@ -417,7 +474,7 @@ __global__ __launch_bounds__(1024) void policy_held(LogitArgs a) {
     st = words[turn & 1][0];
     for (uint32_t i = 1; i < nw; ++i) st = joined(st, words[turn & 1][i], a.c);
     const double lp = logp_of(a, st.m, st.s, zt);
-    const PolicyRow p = policy_row(a, row, lp);
+    const PolicyRow p = policy_row(a, in, lp);
     if (lane == 0) {
       if (a.logp) a.logp[row] = static_cast<float>(lp);
       sums[0] += p.loss, sums[1] += p.kl, sums[2] += p.held, sums[3] += p.w;
@@ -432,20 +489,23 @@ __global__ __launch_bounds__(1024) void policy_held(LogitArgs a) {
       widen(raw[k], f);
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = share * power(f[i], base, a.c);
-      store_raw<T, V, true>(dz + size_t{strip(k)} * T::kSize + own(k) * T::kSize, narrow<T, V>(f));
-      load(z_next, some, k);
+      const Place to = place(off, k);
+      store_raw<T, V, true>(dz + to.all + to.own, narrow<T, V>(f));
+      load(z_next, off_next, some, k);
       __builtin_amdgcn_sched_barrier(0);
     }
     // The target's own element, by every lane that stored a pack with it, after that pack: one of them writes it last.
-    const uint32_t q = t / V;
-    bool mine = K > kEnd && q < (K - kEnd) * lanes && q % lanes == lane;
+    const uint32_t q = (t + off) / V;
+    bool mine = q % lanes == lane;  // it is on the grid
 #pragma unroll
-    for (int i = 0; i < kEnd; ++i) mine = mine || t - end_at[i] < V;
+    for (int k = 0; k < K; ++k)
+      if (at_end(k)) mine = mine || t - place(off, k).own / T::kSize < V;
     if (mine) store1<T>(dz + size_t{t} * T::kSize, share * power(zt, base, a.c) + g);
     t = t_next;
-    zt = zt_next;
+    off = off_next;
+    z = z_next;
   }
-  finish_record(sums[0], sums[1], sums[2], sums[3], a.sums, a.arrived, gridDim.x, a.record, 4);
+  finish_record(sums[0], sums[1], sums[2], sums[3], a.sums, a.arrived, a.record, 4);
 }
 
 // ------------------------------------------------------------------------------------- preference loss
@@ -460,8 +520,10 @@ __device__ __forceinline__ double group_sum(double x, double* lds) {
   return x;
 }
 
+constexpr int kPrefPacks = 2;  // of 4 floats that a lane has in flight, of each input
+
 // A workgroup takes a pair: the sums of both sequences' log ratios in fp64, then the gradient of each of their tokens.
-__global__ __launch_bounds__(1024) void preference(PreferenceArgs a) {
+__global__ __launch_bounds__(512, 4) void preference(PreferenceArgs a) {
   __shared__ double lds[kMostWaves];
   const uint32_t lanes = blockDim.x, lane = threadIdx.x;
   const int64_t rows = static_cast<int64_t>(a.rows);
@@ -473,10 +535,27 @@ __global__ __launch_bounds__(1024) void preference(PreferenceArgs a) {
   for (size_t pair = blockIdx.x; pair < a.pairs; pair += gridDim.x) {
     const int64_t from = bound(2 * pair), mid = bound(2 * pair + 1), to = bound(2 * pair + 2);
     double s = 0.0;  // the chosen sequence's sum less the rejected one's
-#pragma unroll 4
-    for (int64_t i = from + lane; i < to; i += lanes) {
-      const double x = static_cast<double>(a.logp[i]) - (a.ref ? static_cast<double>(a.ref[i]) : 0.0);
-      s += i < mid ? x : -x;
+    for (int64_t i0 = from + lane * 4; i0 < to; i0 += int64_t{lanes} * 4 * kPrefPacks) {
+      Raw<EFp32, 4> x[kPrefPacks], y[kPrefPacks];
+#pragma unroll
+      for (int k = 0; k < kPrefPacks; ++k) {
+        const int64_t i = i0 + int64_t{lanes} * 4 * k;
+        const int n = i >= to ? 0 : to - i < 4 ? static_cast<int>(to - i) : 4;
+        x[k] = load_part<EFp32, 4, false>(reinterpret_cast<const char*>(a.logp + i), n);
+        y[k] = load_part<EFp32, 4, false>(reinterpret_cast<const char*>(a.ref + i), a.ref ? n : 0);
+      }
+#pragma unroll
+      for (int k = 0; k < kPrefPacks; ++k) {
+        const int64_t i = i0 + int64_t{lanes} * 4 * k;
+        float u[4], v[4];
+        widen(x[k], u);
+        widen(y[k], v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const double d = static_cast<double>(u[j]) - static_cast<double>(v[j]);
+          s += i + j < mid ? d : -d;
+        }
+      }
     }
     const double h = a.beta * group_sum(s, lds);
     const double e = exp(-fabs(h)), small = log1p(e);  // -ln sigmoid(x) = log1p(exp(-|x|)) + max(-x, 0)
@@ -490,7 +569,10 @@ __global__ __launch_bounds__(1024) void preference(PreferenceArgs a) {
     }
     if (a.dlogp) {
       const float g = static_cast<float>(a.grad_scale * a.loss_scale * a.beta * (a.smoothing - sig_minus));
-      for (int64_t i = from + lane; i < to; i += lanes) a.dlogp[i] = i < mid ? g : -g;
+      for (int64_t i = from + lane * 4; i < to; i += int64_t{lanes} * 4) {
+        const float v[4] = {i < mid ? g : -g, i + 1 < mid ? g : -g, i + 2 < mid ? g : -g, i + 3 < mid ? g : -g};
+        store_part<EFp32, 4, false>(reinterpret_cast<char*>(a.dlogp + i), v, to - i < 4 ? static_cast<int>(to - i) : 4);
+      }
     }
   }
   if (a.dlogp) {  // rows of no sequence
@@ -500,7 +582,7 @@ __global__ __launch_bounds__(1024) void preference(PreferenceArgs a) {
     for (int64_t i = (end > first ? end : first) + me; i < rows; i += step) a.dlogp[i] = 0.0f;
   }
   const double n = a.pairs ? 1.0 / static_cast<double>(a.pairs) : 0.0;
-  finish_record(loss * a.loss_scale, right * n, margin * n, 0.0, a.sums, a.arrived, gridDim.x, a.record, 3);
+  finish_record(loss * a.loss_scale, right * n, margin * n, 0.0, a.sums, a.arrived, a.record, 3);
 }
 
 // ---------------------------------------------------------------------------------------------- launches
@@ -512,18 +594,24 @@ inline uint32_t stat_lanes(size_t packs_of_part) {
   return packs_of_part <= 256 ? 64 : packs_of_part <= 2048 ? 256 : 512;
 }
 
+bool rows_on_grid(const char* z, size_t rows, size_t stride, size_t es) {
+  return (reinterpret_cast<uintptr_t>(z) | (rows > 1 ? stride * es : 0)) % 16 == 0;
+}
+
 // Rows in registers: lanes and packs a lane.
 struct Held {
   uint32_t waves;
   int K;
 };
 constexpr int kHeldMost = 16;
-Held held_row(size_t cols, int V) {
-  const size_t packs = (cols + V - 1) / V;
-  if (cols < static_cast<size_t>(V) || packs > size_t{64} * kMostWaves * kHeldMost) return {0, 0};
-  const uint32_t waves = static_cast<uint32_t>((packs + 64 * kHeldMost - 1) / (64 * kHeldMost));
-  const int need = static_cast<int>((packs + 64 * waves - 1) / (64 * waves));
-  return {waves, need <= 2 ? need : (need + 1) / 2 * 2};
+Held held_row(size_t cols, int V, bool on_grid) {
+  const size_t packs = (cols + (on_grid ? V - 1 : 2 * V - 2)) / V, whole = cols / V;  // packs of any row; those that no row's end cuts
+  if (whole == 0) return {0, 0};
+  for (uint32_t waves = static_cast<uint32_t>((packs + 64 * kHeldMost - 1) / (64 * kHeldMost)); waves <= kMostWaves; ++waves) {
+    const int need = static_cast<int>((packs + 64 * waves - 1) / (64 * waves)), K = need <= 2 ? need : (need + 1) / 2 * 2;
+    if (K <= 2 || static_cast<size_t>(K - 2) * 64 * waves <= whole) return {waves, K};  // only the last two strips pass an end
+  }
+  return {0, 0};
 }
 
 constexpr uint32_t kCus = 256;
@@ -534,7 +622,7 @@ void held(const LogitArgs& a, uint32_t waves, uint32_t groups, hipStream_t st) {
 }
 template <class T>
 void launch_held(const LogitArgs& a, uint32_t groups, hipStream_t st) {
-  const Held h = held_row(a.cols, 16 / T::kSize);
+  const Held h = held_row(a.cols, 16 / T::kSize, rows_on_grid(a.z, a.rows, a.stride, T::kSize));
   switch (h.K) {
     case 1: held<T, 1>(a, h.waves, groups, st); break;
     case 2: held<T, 2>(a, h.waves, groups, st); break;
@@ -550,17 +638,21 @@ void launch_held(const LogitArgs& a, uint32_t groups, hipStream_t st) {
 
 template <class T, bool Policy>
 void stats(const LogitArgs& a, uint32_t groups, hipStream_t st) {
-  constexpr size_t V = 16 / T::kSize;
-  const size_t packs = (a.cols + V - 1) / V;
+  const size_t packs = a.packs;
   hipLaunchKernelGGL((row_stats<T, Policy>), dim3(groups), dim3(stat_lanes((packs + a.splits - 1) / a.splits)), 0, st, a);
 }
 template <class T>
 void grad(const LogitArgs& a, hipStream_t st) {
-  constexpr size_t V = 16 / T::kSize;
-  const size_t packs = (a.cols + V - 1) / V;
+  const size_t packs = a.packs;
   const uint32_t lanes = packs <= 256 ? 64 : 256;
   const size_t run = static_cast<size_t>(lanes) * kGradPacks, runs = (packs + run - 1) / run;
   hipLaunchKernelGGL((logit_grad<T>), dim3(grid_of(a.rows * runs)), dim3(lanes), 0, st, a);
+}
+
+// Packs that cover every row: one more where rows start off the grid.
+uint32_t packs_of(const LogitArgs& a, mr_dtype dt) {
+  const size_t es = elem_size(dt), V = 16 / es;
+  return static_cast<uint32_t>((a.cols + (rows_on_grid(a.z, a.rows, a.stride, es) ? V - 1 : 2 * V - 2)) / V);
 }
 
 template <class F>
@@ -575,16 +667,16 @@ void by_type(mr_dtype dt, F f) {
 
 }  // namespace
 
-LogitPlan plan_logits(size_t rows, size_t cols, mr_dtype dt, bool gradient) {
+LogitPlan plan_logits(const char* z, size_t rows, size_t cols, size_t stride, mr_dtype dt, bool gradient) {
   const int V = 16 / elem_size(dt);
   const size_t packs = (cols + V - 1) / V;
   LogitPlan pl{};
-  const Held h = held_row(cols, V);
+  const Held h = held_row(cols, V, rows_on_grid(z, rows, stride, elem_size(dt)));
   if (gradient && h.K && rows >= kCus / 2) {
     pl.held = 1;
     pl.splits = 1;
-    const size_t per_cu = 16 / h.waves;  // 128 registers a lane
-    const size_t most = kCus * (per_cu > 8 ? 8 : per_cu), rounds = (rows + most - 1) / most;
+    const size_t per_cu = (h.K <= 4 ? 24 : 16) / h.waves;  // waves that a compute unit's registers hold
+    const size_t most = kCus * (per_cu > 16 ? 16 : per_cu), rounds = (rows + most - 1) / most;
     pl.groups = static_cast<uint32_t>((rows + rounds - 1) / rounds);
     return pl;
   }
@@ -601,17 +693,23 @@ LogitPlan plan_logits(size_t rows, size_t cols, mr_dtype dt, bool gradient) {
   return pl;
 }
 
-hipError_t launch_logprob(const LogitArgs& a, mr_dtype dt, hipStream_t st) {
+hipError_t launch_logprob(const LogitArgs& args, mr_dtype dt, hipStream_t st) {
+  LogitArgs a = args;
+  a.packs = packs_of(a, dt);
   by_type(dt, [&](auto t) { stats<decltype(t), false>(a, grid_of(a.rows * a.splits), st); });
   return hipGetLastError();
 }
 
-hipError_t launch_logprob_bwd(const LogitArgs& a, mr_dtype dt, hipStream_t st) {
+hipError_t launch_logprob_bwd(const LogitArgs& args, mr_dtype dt, hipStream_t st) {
+  LogitArgs a = args;
+  a.packs = packs_of(a, dt);
   by_type(dt, [&](auto t) { grad<decltype(t)>(a, st); });
   return hipGetLastError();
 }
 
-hipError_t launch_policy(const LogitArgs& a, const LogitPlan& pl, mr_dtype dt, hipStream_t st) {
+hipError_t launch_policy(const LogitArgs& args, const LogitPlan& pl, mr_dtype dt, hipStream_t st) {
+  LogitArgs a = args;
+  a.packs = packs_of(a, dt);
   if (pl.held) {
     by_type(dt, [&](auto t) { launch_held<decltype(t)>(a, pl.groups, st); });
     return hipGetLastError();
@@ -627,7 +725,7 @@ uint32_t preference_groups(size_t pairs) { return static_cast<uint32_t>(pairs < 
 
 hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st) {
   const uint32_t groups = preference_groups(a.pairs);
-  const uint32_t lanes = a.rows / (a.pairs ? a.pairs : 1) > 4096 ? 1024 : 256;
+  const uint32_t lanes = a.rows / (a.pairs ? a.pairs : 1) > 2048 ? 512 : 256;
   hipLaunchKernelGGL(preference, dim3(groups), dim3(lanes), 0, st, a);
   return hipGetLastError();
 }

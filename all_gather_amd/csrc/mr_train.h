@@ -113,17 +113,19 @@ struct LogitArgs {
   // workspace
   float* part;            // [rows][splits][3]: maximum, sum, target's logit (or -inf) of a part of a row
   uint32_t* row_arrived;  // [rows] parts that are done; zero between launches
-  double* sums;           // [workgroups][4] parts of the policy loss's record
+  double* sums;           // [workgroups + kNormSets][4] parts of the policy loss's record
   uint32_t (*arrived)[64];
   uint32_t splits;        // parts of a row (set by the plan)
+  uint32_t packs;         // 16-byte packs that cover a row wherever it starts (set by the launch)
 };
-// How a call over logits is launched: a function of its shape alone.
+// How a call over logits is launched: a function of its shape and alignment alone.
 struct LogitPlan {
   int held;          // policy loss: rows in registers, one launch
   uint32_t splits;   // else: parts of a row in the statistics pass
   uint32_t groups;   // workgroups that add up the policy loss's record
 };
-LogitPlan plan_logits(size_t rows, size_t cols, mr_dtype dt, bool gradient);
+LogitPlan plan_logits(const char* z, size_t rows, size_t cols, size_t stride, mr_dtype dt, bool gradient);
+inline size_t record_bytes(uint32_t groups) { return (size_t{groups} + kNormSets) * 32; }
 hipError_t launch_logprob(const LogitArgs& a, mr_dtype dt, hipStream_t st);
 hipError_t launch_logprob_bwd(const LogitArgs& a, mr_dtype dt, hipStream_t st);
 hipError_t launch_policy(const LogitArgs& a, const LogitPlan& pl, mr_dtype dt, hipStream_t st);
@@ -137,7 +139,7 @@ struct PreferenceArgs {
   float* margins;  // may be null
   float* dlogp;    // may be null
   float* record;
-  double* sums;    // [workgroups][4]
+  double* sums;    // [workgroups + kNormSets][4]
   uint32_t (*arrived)[64];
 };
 uint32_t preference_groups(size_t pairs);

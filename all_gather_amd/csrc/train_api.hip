@@ -409,7 +409,7 @@ mr_status token_logprob_forward(const void* logits, size_t rows, size_t cols, si
   mr::LogitArgs a = logit_args(logits, rows, cols, stride, targets, temperature);
   a.logp = logp;
   a.stats = stats;
-  a.splits = mr::plan_logits(rows, cols, dtype, false).splits;
+  a.splits = mr::plan_logits(a.z, rows, cols, stride, dtype, false).splits;
   std::unique_lock<std::mutex> use;  // to the last launch
   if (a.splits > 1) {
     mr::Ctrl* ctrl = nullptr;
@@ -487,10 +487,10 @@ mr_status policy_loss(const void* logits, size_t rows, size_t cols, size_t strid
   a.logp = logp;
   a.dz = cols ? static_cast<char*>(dlogits) : nullptr;
   a.dstride = dstride;
-  const mr::LogitPlan pl = mr::plan_logits(rows, cols, dtype, a.dz != nullptr);
+  const mr::LogitPlan pl = mr::plan_logits(a.z, rows, cols, stride, dtype, a.dz != nullptr);
   a.splits = pl.splits;
   // the workspace: workgroups' sums, then (on the path of two passes) rows' statistics, gradients and parts
-  const size_t sums = size_t{pl.groups} * 32, two = pl.held ? 0 : rows * 12 + rows * (pl.splits > 1 ? pl.splits * 8 : 0);
+  const size_t sums = mr::record_bytes(pl.groups), two = pl.held ? 0 : rows * 12 + rows * (pl.splits > 1 ? pl.splits * 8 : 0);
   mr::Ctrl* ctrl = nullptr;
   char* data = nullptr;
   std::unique_lock<std::mutex> use;  // to the last launch
@@ -530,7 +530,7 @@ mr_status preference_loss(const float* logp, const float* ref_logp, size_t rows,
   mr::Ctrl* ctrl = nullptr;
   char* data = nullptr;
   std::unique_lock<std::mutex> use;  // to the last launch
-  const mr_status s = mr::stream_workspace(st, size_t{mr::preference_groups(pairs)} * 32, &ctrl, &data, &use);
+  const mr_status s = mr::stream_workspace(st, mr::record_bytes(mr::preference_groups(pairs)), &ctrl, &data, &use);
   if (s != MR_OK) return s;
   a.sums = reinterpret_cast<double*>(data);
   a.arrived = ctrl->arrived;
