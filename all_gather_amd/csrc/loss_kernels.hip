@@ -45,14 +45,6 @@ __device__ __forceinline__ void add_values(Stat& a, const float (&f)[N], float c
   a.m = m;
   a.s = s0 + s1;
 }
-__device__ __forceinline__ Stat joined(const Stat& a, const Stat& b, float c) {
-  Stat r;
-  r.m = fmaxf(a.m, b.m);
-  const float base = base_of(r.m);
-  r.s = a.s * power(a.m, base, c) + b.s * power(b.m, base, c);
-  return r;
-}
-
 __device__ __forceinline__ float wave_max(float x) {
   x = fmaxf(x, dpp<0xB1>(x));   // quad lanes 1 0 3 2
   x = fmaxf(x, dpp<0x4E>(x));   // quad lanes 2 3 0 1
@@ -69,6 +61,15 @@ __device__ __forceinline__ Stat wave_join(Stat a, float c) {
   return a;
 }
 
+// The sum of a workgroup's waves, in every lane: one join over the lanes, not one after another.
+constexpr int kMostWaves = 16;
+__device__ __forceinline__ Stat all_waves(const Stat* words, uint32_t waves, float c) {
+  const uint32_t lane = threadIdx.x & 63;
+  Stat st{kNone, 0.0f};
+  if (lane < waves) st = words[lane];
+  return waves > 1 ? wave_join(st, c) : Stat{__shfl(st.m, 0), __shfl(st.s, 0)};
+}
+
 // ln S without the rounding of a large logarithm: S = f * 2^e with f around 1, so that ln 1 is 0.
 __device__ __forceinline__ double ln(float S) {
   int e;
@@ -80,14 +81,21 @@ __device__ __forceinline__ double logp_of(const LogitArgs& a, float m, float S, 
   return (static_cast<double>(zt) - static_cast<double>(m)) * a.inv_temp - ln(S);
 }
 
+// A value of a row, at an address that is the same for every lane and that this launch does not write: by way of the scalar
+// cache, whose loads do not wait in line behind the vector loads of a row.
+template <class X>
+__device__ __forceinline__ X row_value(const X* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) X*>(reinterpret_cast<uintptr_t>(p));
+}
+
 // A row that carries a loss: its target is one of the columns, and its weight is not zero.
 // (The same for every lane: read into scalar registers, so that rows' addresses are too.)
 __device__ __forceinline__ bool row_live(const LogitArgs& a, size_t row, uint32_t* t) {
-  const uint64_t x = static_cast<uint64_t>(a.targets[row]);
+  const uint64_t x = static_cast<uint64_t>(row_value(a.targets + row));
   *t = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
   const uint32_t high = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
   uint32_t weight = 1;
-  if (a.weights) weight = __builtin_amdgcn_readfirstlane(__float_as_uint(a.weights[row])) << 1;
+  if (a.weights) weight = __builtin_amdgcn_readfirstlane(__float_as_uint(row_value(a.weights + row))) << 1;
   return high == 0 && *t < static_cast<uint32_t>(a.cols) && weight != 0;
 }
 
@@ -109,7 +117,8 @@ struct PolicyRow {
 struct PolicyIn {
   float w, adv, old, ref;
   __device__ PolicyIn(const LogitArgs& a, size_t row)
-      : w(a.weights ? a.weights[row] : 1.0f), adv(a.adv[row]), old(a.old_logp ? a.old_logp[row] : 0.0f), ref(a.ref_logp ? a.ref_logp[row] : 0.0f) {}
+      : w(a.weights ? row_value(a.weights + row) : 1.0f), adv(row_value(a.adv + row)), old(a.old_logp ? row_value(a.old_logp + row) : 0.0f),
+        ref(a.ref_logp ? row_value(a.ref_logp + row) : 0.0f) {}
 };
 __device__ __forceinline__ PolicyRow policy_row(const LogitArgs& a, const PolicyIn& in, double logp) {
   const double w = static_cast<double>(in.w), adv = static_cast<double>(in.adv);
@@ -209,8 +218,6 @@ struct PackAt {
   }
 };
 
-constexpr int kMostWaves = 16;
-
 // --------------------------------------------------------------------------------- statistics of rows
 //
 // A workgroup takes one of `splits` parts of a row.  The parts' maxima and sums are joined, in their order, by the workgroup
@@ -221,38 +228,58 @@ template <class T, bool Policy>
 __global__ __launch_bounds__(1024) void row_stats(LogitArgs a) {
   constexpr int V = 16 / T::kSize;
   __shared__ Stat waves[kMostWaves];
-  __shared__ float shared_zt;
   __shared__ bool last;
   const uint32_t lanes = blockDim.x, lane = threadIdx.x;
   const size_t parts = a.rows * a.splits;
   const size_t packs = a.packs, per = (packs + a.splits - 1) / a.splits;
   double loss = 0.0, kl = 0.0, cut = 0.0, weight = 0.0;
-  for (size_t part = blockIdx.x; part < parts; part += gridDim.x) {
-    const size_t row = part / a.splits;
+  uint32_t t = 0, t_next = 0;
+  bool live = blockIdx.x < parts && row_live(a, blockIdx.x / a.splits, &t), live_next = false;
+  for (size_t part = blockIdx.x; part < parts; part += gridDim.x, t = t_next, live = live_next) {
+    const size_t row = part / a.splits, next = part + gridDim.x;
     const uint32_t split = static_cast<uint32_t>(part % a.splits);
-    uint32_t t;
-    if (!row_live(a, row, &t)) {  // the same for every lane, and for every part of the row
+    if (!live) {  // the same for every lane, and for every part of the row
       if (lane == 0 && split == 0) {
         if (a.logp) a.logp[row] = 0.0f;
         if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
         if (Policy && a.dz) const_cast<float*>(a.dlogp)[row] = 0.0f;
       }
+      live_next = next < parts && row_live(a, next / a.splits, &t_next);
       continue;
     }
     const char* z = a.z + row * a.stride * T::kSize;
     const uint32_t off = row_off<T>(z);
     const char* grid = z - off * T::kSize;  // where pack 0 would start
+    const float zt = load1<T>(z + static_cast<size_t>(t) * T::kSize);
     const size_t first = split * per, end = first + per < packs ? first + per : packs;
     Stat st{kNone, 0.0f};
     for (size_t p = first + lane; p < end; p += static_cast<size_t>(lanes) * kStatPacks) {
       float f[kStatPacks * V];
       Raw<T, V> raw[kStatPacks];
-      const size_t top = p + static_cast<size_t>(lanes) * (kStatPacks - 1);
-      if (top < end && (top + 1) * V <= a.cols + off && (p > 0 || off == 0)) {
+      const size_t p0 = p - lane, top = p0 + static_cast<size_t>(lanes) * kStatPacks;
+      if (top <= end && top * V <= a.cols + off && (p0 > 0 || off == 0)) {  // the same for every lane
 #pragma unroll
         for (int k = 0; k < kStatPacks; ++k) raw[k] = load_raw<T, V, true>(grid + (p + static_cast<size_t>(lanes) * k) * 16);
 #pragma unroll
         for (int k = 0; k < kStatPacks; ++k) widen(raw[k], reinterpret_cast<float(&)[V]>(f[k * V]));
+      } else if (a.cols >= V) {
+        // packs that pass an end of the row are read as V elements from that end on; those that are another pack's are left out
+        int from[kStatPacks];
+#pragma unroll
+        for (int k = 0; k < kStatPacks; ++k) {
+          const size_t q = p + static_cast<size_t>(lanes) * k;
+          const int64_t c = static_cast<int64_t>(q * V) - off, last = static_cast<int64_t>(a.cols) - V, at = c < 0 ? 0 : c < last ? c : last;
+          from[k] = q < end && c - at < V ? static_cast<int>(c - at) : V;
+          raw[k] = load_raw<T, V, true>(z + at * T::kSize);
+        }
+#pragma unroll
+        for (int k = 0; k < kStatPacks; ++k) {
+          float (&g)[V] = reinterpret_cast<float(&)[V]>(f[k * V]);
+          widen(raw[k], g);
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (i < from[k] || i >= from[k] + V) g[i] = kNone;
+        }
       } else {
 #pragma unroll
         for (int k = 0; k < kStatPacks; ++k) {
@@ -268,17 +295,15 @@ __global__ __launch_bounds__(1024) void row_stats(LogitArgs a) {
       }
       add_values(st, f, a.c);
     }
+    live_next = next < parts && row_live(a, next / a.splits, &t_next);
     st = wave_join(st, a.c);
-    __syncthreads();  // the last row's words have been read
-    if ((lane & 63) == 0) waves[lane >> 6] = st;
-    if (lane == 0) shared_zt = load1<T>(z + static_cast<size_t>(t) * T::kSize);
-    __syncthreads();
-    if (lane >= 64) {
-      if (a.splits == 1) continue;
-    } else {
-      st = waves[0];
-      for (uint32_t w = 1; w < lanes / 64; ++w) st = joined(st, waves[w], a.c);
+    if (lanes > 64) {
+      __syncthreads();  // the last row's words have been read
+      if ((lane & 63) == 0) waves[lane >> 6] = st;
+      __syncthreads();
+      if (lane < 64) st = all_waves(waves, lanes / 64, a.c);
     }
+    if (lane >= 64 && a.splits == 1) continue;
     if (a.splits > 1) {
       if (lane == 0) {
         float* at = a.part + part * 2;
@@ -300,7 +325,7 @@ __global__ __launch_bounds__(1024) void row_stats(LogitArgs a) {
       }
       st = wave_join(mine, a.c);
     }
-    const double lp = logp_of(a, st.m, st.s, shared_zt);
+    const double lp = logp_of(a, st.m, st.s, zt);
     if (lane == 0) {
       if (a.logp) a.logp[row] = static_cast<float>(lp);
       if (a.stats) {
@@ -471,8 +496,7 @@ __global__ __launch_bounds__(1024) void policy_held(LogitArgs a) {
     st = wave_join(st, a.c);
     if ((lane & 63) == 0) words[turn & 1][lane >> 6] = st;
     __syncthreads();
-    st = words[turn & 1][0];
-    for (uint32_t i = 1; i < nw; ++i) st = joined(st, words[turn & 1][i], a.c);
+    st = all_waves(words[turn & 1], nw, a.c);
     const double lp = logp_of(a, st.m, st.s, zt);
     const PolicyRow p = policy_row(a, in, lp);
     if (lane == 0) {
@@ -688,7 +712,7 @@ LogitPlan plan_logits(const char* z, size_t rows, size_t cols, size_t stride, mr
     splits = splits > 64 ? 64 : splits;
   }
   pl.splits = static_cast<uint32_t>(splits);
-  const size_t parts = rows * splits, most = size_t{kCus} * 8;
+  const size_t parts = rows * splits, most = size_t{kCus} * 16;
   pl.groups = static_cast<uint32_t>(parts < 1 ? 1 : parts < most ? parts : most);
   return pl;
 }
@@ -696,7 +720,9 @@ LogitPlan plan_logits(const char* z, size_t rows, size_t cols, size_t stride, mr
 hipError_t launch_logprob(const LogitArgs& args, mr_dtype dt, hipStream_t st) {
   LogitArgs a = args;
   a.packs = packs_of(a, dt);
-  by_type(dt, [&](auto t) { stats<decltype(t), false>(a, grid_of(a.rows * a.splits), st); });
+  // rows of one wave: as many as the device holds, each walking its rows (a launch starts about one workgroup a nanosecond)
+  const size_t parts = a.rows * a.splits, most = (a.packs + a.splits - 1) / a.splits <= 256 ? size_t{kCus} * 24 : parts;
+  by_type(dt, [&](auto t) { stats<decltype(t), false>(a, grid_of(parts < most ? parts : most), st); });
   return hipGetLastError();
 }
 
