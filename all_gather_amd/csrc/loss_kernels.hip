@@ -622,23 +622,28 @@ bool rows_on_grid(const char* z, size_t rows, size_t stride, size_t es) {
   return (reinterpret_cast<uintptr_t>(z) | (rows > 1 ? stride * es : 0)) % 16 == 0;
 }
 
+constexpr uint32_t kCus = 256;
+
 // Rows in registers: lanes and packs a lane.
 struct Held {
   uint32_t waves;
   int K;
 };
 constexpr int kHeldMost = 16;
-Held held_row(size_t cols, int V, bool on_grid) {
+Held held_row(size_t rows, size_t cols, int V, bool on_grid) {
   const size_t packs = (cols + (on_grid ? V - 1 : 2 * V - 2)) / V, whole = cols / V;  // packs of any row; those that no row's end cuts
   if (whole == 0) return {0, 0};
-  for (uint32_t waves = static_cast<uint32_t>((packs + 64 * kHeldMost - 1) / (64 * kHeldMost)); waves <= kMostWaves; ++waves) {
+  uint32_t least = static_cast<uint32_t>((packs + 64 * kHeldMost - 1) / (64 * kHeldMost));
+  if (rows <= kCus) {  // a compute unit each: as many waves as a row feeds
+    const uint32_t wide = static_cast<uint32_t>((packs + 63) / 64);
+    least = wide < kMostWaves ? wide : least > kMostWaves ? least : kMostWaves;
+  }
+  for (uint32_t waves = least; waves <= kMostWaves; ++waves) {
     const int need = static_cast<int>((packs + 64 * waves - 1) / (64 * waves)), K = need <= 2 ? need : (need + 1) / 2 * 2;
     if (K <= 2 || static_cast<size_t>(K - 2) * 64 * waves <= whole) return {waves, K};  // only the last two strips pass an end
   }
   return {0, 0};
 }
-
-constexpr uint32_t kCus = 256;
 
 template <class T, int K>
 void held(const LogitArgs& a, uint32_t waves, uint32_t groups, hipStream_t st) {
@@ -646,7 +651,7 @@ void held(const LogitArgs& a, uint32_t waves, uint32_t groups, hipStream_t st) {
 }
 template <class T>
 void launch_held(const LogitArgs& a, uint32_t groups, hipStream_t st) {
-  const Held h = held_row(a.cols, 16 / T::kSize, rows_on_grid(a.z, a.rows, a.stride, T::kSize));
+  const Held h = held_row(a.rows, a.cols, 16 / T::kSize, rows_on_grid(a.z, a.rows, a.stride, T::kSize));
   switch (h.K) {
     case 1: held<T, 1>(a, h.waves, groups, st); break;
     case 2: held<T, 2>(a, h.waves, groups, st); break;
@@ -695,8 +700,10 @@ LogitPlan plan_logits(const char* z, size_t rows, size_t cols, size_t stride, mr
   const int V = 16 / elem_size(dt);
   const size_t packs = (cols + V - 1) / V;
   LogitPlan pl{};
-  const Held h = held_row(cols, V, rows_on_grid(z, rows, stride, elem_size(dt)));
-  if (gradient && h.K && rows >= kCus / 2) {
+  const Held h = held_row(rows, cols, V, rows_on_grid(z, rows, stride, elem_size(dt)));
+  // One row of 131072 16-bit columns by one compute unit takes 16.8 us, in parts by two launches 12.2; 8 rows 16.9 and 17.7; one of
+  // 65536 10.3 and 11.9, 24 of 32768 7.5 and 14.4, 256 of 131072 31 and 46.
+  if (gradient && h.K && (rows >= 8 || h.K <= 8)) {
     pl.held = 1;
     pl.splits = 1;
     const size_t per_cu = (h.K <= 4 ? 24 : 16) / h.waves;  // waves that a compute unit's registers hold
