@@ -344,16 +344,17 @@ __global__ __launch_bounds__(1024) void row_stats(LogitArgs a) {
 
 // ------------------------------------------------------------------------------ gradient of the logits
 //
-// dz_j = g/T ([j = t] - exp((z_j - m) / T) / S), element by element; a workgroup takes a run of packs of one row.
+// dz_j = g/T ([j = t] - exp((z_j - m) / T) / S), element by element; a wave takes a run of packs of one row.
 constexpr int kGradPacks = 4;
 
 template <class T>
 __global__ __launch_bounds__(256) void logit_grad(LogitArgs a) {
   constexpr int V = 16 / T::kSize;
-  const uint32_t lanes = blockDim.x, lane = threadIdx.x;
-  const size_t packs = a.packs, run = static_cast<size_t>(lanes) * kGradPacks;
+  constexpr uint32_t lanes = 64;
+  const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const size_t packs = a.packs, run = size_t{lanes} * kGradPacks;
   const size_t runs = (packs + run - 1) / run;
-  for (size_t item = blockIdx.x; item < a.rows * runs; item += gridDim.x) {
+  for (size_t item = size_t{blockIdx.x} * 4 + wave; item < a.rows * runs; item += size_t{gridDim.x} * 4) {
     const size_t row = item / runs, p0 = item % runs * run + lane;
     uint32_t t;
     const bool live = row_live(a, row, &t);  // (the backward pass has no weights)
@@ -672,10 +673,8 @@ void stats(const LogitArgs& a, uint32_t groups, hipStream_t st) {
 }
 template <class T>
 void grad(const LogitArgs& a, hipStream_t st) {
-  const size_t packs = a.packs;
-  const uint32_t lanes = packs <= 256 ? 64 : 256;
-  const size_t run = static_cast<size_t>(lanes) * kGradPacks, runs = (packs + run - 1) / run;
-  hipLaunchKernelGGL((logit_grad<T>), dim3(grid_of(a.rows * runs)), dim3(lanes), 0, st, a);
+  const size_t run = size_t{64} * kGradPacks, items = a.rows * ((a.packs + run - 1) / run);
+  hipLaunchKernelGGL((logit_grad<T>), dim3(grid_of((items + 3) / 4)), dim3(256), 0, st, a);
 }
 
 // Packs that cover every row: one more where rows start off the grid.
