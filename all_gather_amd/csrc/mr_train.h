@@ -220,7 +220,9 @@ struct NsLastArgs {
   const float* clip;
   float keep;
 };
-uint32_t ns_tile(uint32_t m, uint32_t n);  // columns of a product's tiles for a matrix of this shape
+// Columns of a product's tiles for a matrix of m rows, in a list whose larger matrices have many such tiles or few.
+uint32_t ns_tile(uint32_t m, bool many);
+bool ns_many(uint64_t wide_tiles);
 uint32_t ns_tiles(uint32_t tile, uint32_t rows, uint32_t cols, bool symmetric);
 hipError_t launch_momentum(const MomentumArgs& a, mr_dtype gdt, hipStream_t st);
 hipError_t launch_orient(const OrientArgs& a, mr_dtype gdt, hipStream_t st);

@@ -541,7 +541,11 @@ void by_type(mr_dtype dt, F f) {
 
 }  // namespace
 
-uint32_t ns_tile(uint32_t m, uint32_t) { return m >= 2048 ? 256 : m >= 512 ? 128 : 64; }
+// Tiles of 128 x 256 ask least of LDS and L2, tiles of 128 x 128 leave fewer compute units idle at a launch's end.  A step, wide tiles
+// and square ones (ms): eight of 4096 x 4096 11.2 and 12.7; one (512 wide tiles a product) 1.98 and 1.91; one of 2048 x 2048 0.56 and
+// 0.47; one of 4096 x 8192 (1024) 3.08 and 3.04, of 4096 x 16384 (2048) 5.33 and 5.41.
+uint32_t ns_tile(uint32_t m, bool many) { return m >= 1024 && many ? 256 : m >= 512 ? 128 : 64; }
+bool ns_many(uint64_t wide_tiles) { return wide_tiles > 1024; }
 
 uint32_t ns_tiles(uint32_t tile, uint32_t rows, uint32_t cols, bool symmetric) {
   const uint32_t bm = tile == 256 ? 128 : tile, bn = tile, ratio = bn / bm;

@@ -106,6 +106,23 @@ def test_lists_of_every_size(products):
             assert torch.equal(got[i], alone), (i, s)
 
 
+@pytest.mark.parametrize("products", [16, 32])
+def test_many_large_matrices(products):
+    """Enough of them for the wide tiles: each against the iteration in 64 bits, both ways round.  Alone, on square tiles, a matrix gives
+    the same bits: its sums run over the same columns in the same order.  Not so in two pieces, where an element of A or P is the sum
+    hi lo + lo hi + hi hi of its row and column or, mirrored, of its column and row, by the tile that it falls in."""
+    gen = torch.Generator(device=device()).manual_seed(14)
+    shapes = [(2049, 2500)] * 4 + [(2500, 2047), (1025, 6001), (2304, 3001), (1500, 1100), (600, 700)]
+    u = [matrix(*s, "low" if i % 2 else "full", gen) for i, s in enumerate(shapes)]
+    got = update_alone(u, products)
+    for i in (0, 3, 4, 5, 6, 7, 8):
+        want, tol = bound(u[i], products)
+        off = float((got[i] - want).norm())
+        assert off <= tol, (shapes[i], off, tol)
+        alone, = update_alone([u[i]], products)
+        assert torch.equal(got[i], alone) if products == 16 else float((got[i] - alone).norm()) <= 2 * tol, shapes[i]
+
+
 def test_group_larger_than_the_workspace_limit():
     """Matrices whose workspace passes 2 GiB together are worked off in parts."""
     gen = torch.Generator(device=device()).manual_seed(12)
