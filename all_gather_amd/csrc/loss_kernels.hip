@@ -193,8 +193,8 @@ __device__ __forceinline__ void finish_record(double v0, double v1, double v2, d
   if (sets > 1) {
     double* of_sets = sums + size_t{groups} * 4;
     if (lane < 4) __hip_atomic_store(of_sets + set * 4 + lane, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = arrive(&arrived[kNormSets][0], 64 * sets) ? 1 : 0;  // (every lane arrives: its own store is acknowledged)
-    if (!__any(last)) return;
+    if (lane == 0) last = arrive(&arrived[kNormSets][0], sets);  // (waits for the stores of the whole wave)
+    if (!__shfl(last, 0)) return;
     s = sum4(of_sets, sets, 1);
   }
   if (lane <= kNormSets) __hip_atomic_store(&arrived[lane][0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -634,14 +634,18 @@ constexpr int kHeldMost = 16;
 Held held_row(size_t rows, size_t cols, int V, bool on_grid) {
   const size_t packs = (cols + (on_grid ? V - 1 : 2 * V - 2)) / V, whole = cols / V;  // packs of any row; those that no row's end cuts
   if (whole == 0) return {0, 0};
-  uint32_t least = static_cast<uint32_t>((packs + 64 * kHeldMost - 1) / (64 * kHeldMost));
-  if (rows <= kCus) {  // a compute unit each: as many waves as a row feeds
-    const uint32_t wide = static_cast<uint32_t>((packs + 63) / 64);
-    least = wide < kMostWaves ? wide : least > kMostWaves ? least : kMostWaves;
-  }
-  for (uint32_t waves = least; waves <= kMostWaves; ++waves) {
+  const auto shape = [&](uint32_t waves) {
     const int need = static_cast<int>((packs + 64 * waves - 1) / (64 * waves)), K = need <= 2 ? need : (need + 1) / 2 * 2;
-    if (K <= 2 || static_cast<size_t>(K - 2) * 64 * waves <= whole) return {waves, K};  // only the last two strips pass an end
+    const bool fits = K <= kHeldMost && (K <= 2 || static_cast<size_t>(K - 2) * 64 * waves <= whole);  // only the last two strips pass an end
+    return fits ? Held{waves, K} : Held{0, 0};
+  };
+  if (rows <= kCus) {  // a compute unit each: as many waves as a row feeds
+    const size_t wide = (packs + 63) / 64;
+    for (uint32_t waves = wide < kMostWaves ? static_cast<uint32_t>(wide) : kMostWaves; waves >= 1; --waves)
+      if (const Held h = shape(waves); h.K) return h;
+  } else {
+    for (uint32_t waves = 1; waves <= kMostWaves; ++waves)
+      if (const Held h = shape(waves); h.K) return h;
   }
   return {0, 0};
 }
@@ -702,7 +706,7 @@ LogitPlan plan_logits(const char* z, size_t rows, size_t cols, size_t stride, mr
   const Held h = held_row(rows, cols, V, rows_on_grid(z, rows, stride, elem_size(dt)));
   // One row of 131072 16-bit columns by one compute unit takes 16.8 us, in parts by two launches 12.2; 8 rows 16.9 and 17.7; one of
   // 65536 10.3 and 11.9, 24 of 32768 7.5 and 14.4, 256 of 131072 31 and 46.
-  if (gradient && h.K && (rows >= 8 || h.K <= 8)) {
+  if (gradient && rows && h.K && (rows >= 8 || h.K <= 8)) {
     pl.held = 1;
     pl.splits = 1;
     const size_t per_cu = (h.K <= 4 ? 24 : 16) / h.waves;  // waves that a compute unit's registers hold

@@ -485,7 +485,7 @@ mr_status policy_loss(const void* logits, size_t rows, size_t cols, size_t strid
   a.grad_scale = h->grad_scale;
   a.record = record;
   a.logp = logp;
-  a.dz = cols ? static_cast<char*>(dlogits) : nullptr;
+  a.dz = rows && cols ? static_cast<char*>(dlogits) : nullptr;
   a.dstride = dstride;
   const mr::LogitPlan pl = mr::plan_logits(a.z, rows, cols, stride, dtype, a.dz != nullptr);
   a.splits = pl.splits;
