@@ -148,7 +148,7 @@ hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st);
 // ------------------------------------------------------------------------------------------------ Muon
 //
 // A matrix of rows x cols is orthogonalised as X, m x n with m <= n: itself, or its transpose where rows > cols.  The
-// stream's workspace holds, in fp16, in panels of kNsK columns and each as `pieces` matrices after one another, X [m][ldn], its transpose [n][ldm] twice (a
+// stream's workspace holds, in fp16, in one or two pieces and in panels of kNsK of them, X [m][ldn], its transpose [n][ldm] twice (a
 // product reads one and writes the other), A = X X^T and P = a I + b A + c A^2 [m][ldm]; ldm and ldn are m and n rounded up to
 // three of a product's stages (ns_padded), and columns past m and n are zero.
 constexpr int kMuonMats = 32;       // matrices of one launch

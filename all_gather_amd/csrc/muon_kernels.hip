@@ -16,6 +16,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "mr_train.h"
 #include "packs.h"
 
@@ -30,8 +32,13 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr float kUp = 1 << kNsShift, kDown = 1.0f / (1 << kNsShift);
 
 // A matrix of `rows` rows lies in panels of 32 columns, each panel's rows after one another (64 bytes a row): what a product
-// fetches at a time is one run of memory, and no stride of a power of two.
-__device__ __forceinline__ size_t in_panels(size_t rows, uint32_t r, uint32_t c) { return (c / kNsK * rows + r) * kNsK + c % kNsK; }
+// fetches at a time is one run of memory, and no stride of a power of two.  In two pieces a panel is 16 columns, their first
+// pieces and then their second: a stage holds both, and every operand that it brings in is used twice.
+constexpr uint32_t kPieceAt = kNsK / 2;  // from a value's first piece to its second
+__device__ __forceinline__ size_t in_panels(size_t rows, uint32_t r, uint32_t c, int pieces) {
+  const uint32_t w = kNsK / pieces;
+  return (c / w * rows + r) * kNsK + c % w;
+}
 
 // The matrix whose tiles hold tile t.
 __device__ __forceinline__ uint32_t entry_of(const uint32_t* prefix, uint32_t P, uint32_t t) {
@@ -134,7 +141,7 @@ __global__ __launch_bounds__(256) void momentum(MomentumArgs a) {
 
 // N values in fp16 (the rest of them in a second piece) to `at`.
 template <int N>
-__device__ __forceinline__ void store_pieces(f16* at, size_t piece, int pieces, const float (&v)[N]) {
+__device__ __forceinline__ void store_pieces(f16* at, int pieces, const float (&v)[N]) {
   typedef f16 Pack __attribute__((ext_vector_type(N)));
   Pack hi, lo;
 #pragma unroll
@@ -143,7 +150,7 @@ __device__ __forceinline__ void store_pieces(f16* at, size_t piece, int pieces, 
     lo[q] = static_cast<f16>(v[q] - static_cast<float>(hi[q]));
   }
   *reinterpret_cast<Pack*>(at) = hi;
-  if (pieces == 2) *reinterpret_cast<Pack*>(at + piece) = lo;
+  if (pieces == 2) *reinterpret_cast<Pack*>(at + kPieceAt) = lo;
 }
 
 // u / |u| of a 64 x 64 tile, times 2^12, in fp16: as it lies, and transposed.  Columns past the matrix become zeros.
@@ -181,7 +188,7 @@ __global__ __launch_bounds__(256) void orient(OrientArgs a) {
         u[j] = r < rows && j < live ? update_of(mf[j], clip.f * gf[j], a.mu, a.c, a.nesterov) * inv : 0.0f;
         tile[k * 16 + y][x + j] = u[j];
       }
-      if (r < rows && c < ld_direct) store_pieces(a.direct[i] + in_panels(rows, r, c), static_cast<size_t>(rows) * ld_direct, a.pieces, u);
+      if (r < rows && c < ld_direct) store_pieces(a.direct[i] + in_panels(rows, r, c, a.pieces), a.pieces, u);
     }
   }
   __syncthreads();
@@ -192,7 +199,7 @@ __global__ __launch_bounds__(256) void orient(OrientArgs a) {
     float u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] = tile[y + j][x];
-    store_pieces(a.turned[i] + in_panels(cols, c, r), static_cast<size_t>(cols) * ld_turned, a.pieces, u);
+    store_pieces(a.turned[i] + in_panels(cols, c, r, a.pieces), a.pieces, u);
   }
 }
 
@@ -287,13 +294,21 @@ struct Tile {
     else
       p.y[i] = *reinterpret_cast<const f16x8*>(lds + (BM + rb + i * 32) * kRow + ((2 * k + lane / 32) ^ swizzle(rb)) * 8);
   }
-  __device__ __forceinline__ void product(const Part& p, int n) {
+  // The n-th block's product of px's x and py's y.
+  __device__ __forceinline__ void product(const Part& px, const Part& py, int n) {
     const int i = n / kNj, j = n % kNj;
-    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p.y[j], p.x[i], acc[i][j], 0, 0, 0);
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(py.y[j], px.x[i], acc[i][j], 0, 0, 0);
+  }
+  static __device__ __forceinline__ void clear(Part& p) {
+#pragma unroll
+    for (int i = 0; i < kMi; ++i) p.x[i] = f16x8{};
+#pragma unroll
+    for (int j = 0; j < kNj; ++j) p.y[j] = f16x8{};
   }
 
-  // The sum over K columns (a multiple of the ring), of 1 product or (two pieces) 3, the smaller ones first.
-  __device__ __forceinline__ void run(const NsProduct& p, uint32_t ti, uint32_t tj, int pieces) {
+  // The sum over K columns (a whole number of turns of the ring, an even one for two pieces).
+  template <int Pieces>
+  __device__ __forceinline__ void run(const NsProduct& p, uint32_t ti, uint32_t tj) {
 #pragma unroll
     for (int i = 0; i < kMi; ++i)
 #pragma unroll
@@ -301,13 +316,10 @@ struct Tile {
     if (ti * BM >= p.M || tj * BN >= p.N) return;  // columns past the matrix alone
     const Fetch<BM, kWaves> fa(p.M - ti * BM);
     const Fetch<BN, kWaves> fb(p.N - tj * BN);
-    const f16* const a0 = p.a + size_t{ti} * BM * kNsK;
-    const f16* const b0 = p.b + size_t{tj} * BN * kNsK;
+    const f16* a = p.a + size_t{ti} * BM * kNsK;
+    const f16* b = p.b + size_t{tj} * BN * kNsK;
     const size_t a_panel = size_t{p.M} * kNsK, b_panel = size_t{p.N} * kNsK;
-    const uint32_t per = p.K / kNsK, steps = pieces == 2 ? 3 * per : per;
-    // where the next stage comes from: with two pieces, hi lo + lo hi + hi hi
-    const f16* a = a0;
-    const f16* b = pieces == 2 ? b0 + per * b_panel : b0;
+    const uint32_t steps = p.K / kNsK * Pieces;
     uint32_t ahead = 0;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     constexpr int kLoads = Fetch<BM, kWaves>::kLoads + Fetch<BN, kWaves>::kLoads;  // of a stage
@@ -322,60 +334,100 @@ struct Tile {
       const bool more = ++ahead < steps;
       a += more ? a_panel : 0;
       b += more ? b_panel : 0;
-      if (pieces == 2) {
-        a = ahead == per ? a0 + per * a_panel : ahead == 2 * per ? a0 : a;
-        b = ahead == per || ahead == 2 * per ? b0 : b;
-      }
     };
     for (f16* s : {stage<0>(), stage<1>()}) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) fetch(s, i);
       advance();
     }
-    Part even, odd;
-#pragma unroll
-    for (int i = 0; i < kMi; ++i) odd.x[i] = f16x8{};
-#pragma unroll
-    for (int j = 0; j < kNj; ++j) odd.y[j] = f16x8{};
-    // One stage.  The products of its second half are made after the next barrier, while that stage's first operands are read:
-    // the matrix cores have work on both sides of it.  Reads and fetches are issued between the products, not before them.
-    auto turn = [&](const f16* now, f16* last) {
+    auto enter = [&] {
       __builtin_amdgcn_s_waitcnt(0x0070 | kLoads);  // vmcnt: all but the next stage's loads are here; lgkmcnt(0): the last one is read
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      constexpr int kEach = (kReads + kProducts - 1) / kProducts;  // reads beside a product
-      auto beside = [&](int slot) {  // the fetches, evenly over the stage: one that finds the memory pipeline full holds its wave up
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-          if (i * 2 * kProducts / kLoads == slot) fetch(last, i);
-        __builtin_amdgcn_sched_barrier(0);
-      };
-#pragma unroll
-      for (int n = 0; n < kProducts; ++n) {
-        product(odd, n);
-#pragma unroll
-        for (int o = n * kEach; o < (n + 1) * kEach; ++o)
-          if (o < kReads) read(even, now, 0, o);
-        beside(n);
-      }
-#pragma unroll
-      for (int n = 0; n < kProducts; ++n) {
-        product(even, n);
-#pragma unroll
-        for (int o = n * kEach; o < (n + 1) * kEach; ++o)
-          if (o < kReads) read(odd, now, 1, o);
-        beside(kProducts + n);
-      }
-      advance();
     };
-    for (uint32_t k = 0; k < steps; k += kStages) {
-      turn(stage<0>(), stage<2>());
-      turn(stage<1>(), stage<0>());
-      turn(stage<2>(), stage<1>());
-    }
+    // Beside one of a stage's Pieces + 1 groups of products: reads from LDS, and the fetches evenly over the stage (one that finds the
+    // memory pipeline full holds its wave up).
+    auto beside = [&](f16* last, int slot) {
 #pragma unroll
-    for (int n = 0; n < kProducts; ++n) product(odd, n);
+      for (int i = 0; i < kLoads; ++i)
+        if (i * (Pieces + 1) * kProducts / kLoads == slot) fetch(last, i);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // One stage.  Its last group of products is made after the next barrier, while that stage's first operands are read: the
+    // matrix cores have work on both sides of it.
+    if constexpr (Pieces == 1) {
+      Part even, odd;  // the stage's first 16 columns, and its others
+      clear(odd);
+      auto turn = [&](const f16* now, f16* last) {
+        constexpr int kEach = (kReads + kProducts - 1) / kProducts;  // reads beside a product
+        enter();
+#pragma unroll
+        for (int n = 0; n < kProducts; ++n) {
+          product(odd, odd, n);
+#pragma unroll
+          for (int o = n * kEach; o < (n + 1) * kEach; ++o)
+            if (o < kReads) read(even, now, 0, o);
+          beside(last, n);
+        }
+#pragma unroll
+        for (int n = 0; n < kProducts; ++n) {
+          product(even, even, n);
+#pragma unroll
+          for (int o = n * kEach; o < (n + 1) * kEach; ++o)
+            if (o < kReads) read(odd, now, 1, o);
+          beside(last, kProducts + n);
+        }
+        advance();
+      };
+      for (uint32_t k = 0; k < steps; k += kStages) {
+        turn(stage<0>(), stage<2>());
+        turn(stage<1>(), stage<0>());
+        turn(stage<2>(), stage<1>());
+      }
+#pragma unroll
+      for (int n = 0; n < kProducts; ++n) product(odd, odd, n);
+    } else {
+      Part hi0, hi1, lo;  // first pieces of this stage and the last one, by turns; second pieces
+      clear(hi1);
+      auto turn = [&](const f16* now, f16* last, Part& hi, Part& before) {
+        constexpr int kEach = (2 * kReads + kProducts - 1) / kProducts;
+        enter();
+#pragma unroll
+        for (int n = 0; n < kProducts; ++n) {
+          product(before, before, n);
+#pragma unroll
+          for (int o = n * kEach; o < (n + 1) * kEach; ++o) {
+            if (o < kReads)
+              read(hi, now, 0, o);
+            else if (o < 2 * kReads)
+              read(lo, now, 1, o - kReads);
+          }
+          beside(last, n);
+        }
+#pragma unroll
+        for (int n = 0; n < kProducts; ++n) {
+          product(hi, lo, n);
+          beside(last, kProducts + n);
+        }
+#pragma unroll
+        for (int n = 0; n < kProducts; ++n) {
+          product(lo, hi, n);
+          beside(last, 2 * kProducts + n);
+        }
+        advance();
+      };
+      for (uint32_t k = 0; k < steps; k += 2 * kStages) {
+        turn(stage<0>(), stage<2>(), hi0, hi1);
+        turn(stage<1>(), stage<0>(), hi1, hi0);
+        turn(stage<2>(), stage<1>(), hi0, hi1);
+        turn(stage<0>(), stage<2>(), hi1, hi0);
+        turn(stage<1>(), stage<0>(), hi0, hi1);
+        turn(stage<2>(), stage<1>(), hi1, hi0);
+      }
+#pragma unroll
+      for (int n = 0; n < kProducts; ++n) product(hi1, hi1, n);
+    }
   }
 
   // Results leave through LDS, where each wave turns 32 rows of its part at a time in a place of its own, so that a lane has 8
@@ -436,15 +488,13 @@ struct Tile {
   }
 };
 
-template <NsKind Kind, int BM, int BN, int WR, int WC>
+template <NsKind Kind, int Pieces, int BM, int BN, int WR, int WC>
 __global__ __launch_bounds__(WR* WC * 64) void ns_product(NsArgs a) {
   constexpr bool kSym = Kind != kNsStep;
   const Where w = tile_of<BM, BN>(a, kSym);
   const NsProduct p = a.p[w.i];
   Tile<BM, BN, WR, WC> t;
-  t.run(p, w.ti, w.tj, a.pieces);
-  const size_t c_piece = static_cast<size_t>(p.M) * p.ldc, ct_piece = static_cast<size_t>(p.N) * p.ldct;
-  const size_t a_piece = static_cast<size_t>(p.M) * p.K;
+  t.template run<Pieces>(p, w.ti, w.tj);
   const bool both = !kSym || w.tj < w.ti / (BN / BM);  // else the transpose's places are another tile's, or this one's
   t.template leave<true, true>(
       w.ti, w.tj,
@@ -453,8 +503,8 @@ __global__ __launch_bounds__(WR* WC * 64) void ns_product(NsArgs a) {
         if constexpr (Kind == kNsPoly) {
           float add[8] = {};
           if (in) {  // P's columns are A's
-            for (int s = 0; s < a.pieces; ++s) {
-              const f16x8 x = *reinterpret_cast<const f16x8*>(p.a + s * a_piece + in_panels(p.M, r, c));
+            for (int s = 0; s < Pieces; ++s) {
+              const f16x8 x = *reinterpret_cast<const f16x8*>(p.a + s * kPieceAt + in_panels(p.M, r, c, Pieces));
 #pragma unroll
               for (int q = 0; q < 8; ++q) add[q] += static_cast<float>(x[q]);
             }
@@ -468,22 +518,22 @@ __global__ __launch_bounds__(WR* WC * 64) void ns_product(NsArgs a) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (c + q >= p.N || r >= p.M) v[q] = 0.0f;  // what lies past the matrix, in C and in its transpose
-        if (in) store_pieces(p.c + in_panels(p.M, r, c), c_piece, a.pieces, v);
+        if (in) store_pieces(p.c + in_panels(p.M, r, c, Pieces), Pieces, v);
       },
       [&](uint32_t r, uint32_t c, float (&v)[8]) {
-        if (both && r < p.ldct && c < p.N) store_pieces((kSym ? p.c : p.ct) + in_panels(p.N, c, r), ct_piece, a.pieces, v);
+        if (both && r < p.ldct && c < p.N) store_pieces((kSym ? p.c : p.ct) + in_panels(p.N, c, r, Pieces), Pieces, v);
       });
 }
 
 // The last product of the last step, which updates the parameters instead of being stored.
-template <class T, int BM, int BN, int WR, int WC>
+template <class T, int Pieces, int BM, int BN, int WR, int WC>
 __global__ __launch_bounds__(WR* WC * 64) void ns_last(NsLastArgs a) {
   const Where w = tile_of<BM, BN>(a.s, false);
   const NsProduct p = a.s.p[w.i];
   const NsUpdate u = a.u[w.i];
   const Clip clip = clip_of(a.clip);
   Tile<BM, BN, WR, WC> t;
-  t.run(p, w.ti, w.tj, a.s.pieces);
+  t.template run<Pieces>(p, w.ti, w.tj);
   const float by = u.scale * kDown * kDown;
   // n (1 to 8) of the values v belong to the matrix, from its element e on
   auto update = [&](size_t e, int n, const float (&v)[8]) {
@@ -508,25 +558,25 @@ __global__ __launch_bounds__(WR* WC * 64) void ns_last(NsLastArgs a) {
     }, [](uint32_t, uint32_t, float (&)[8]) {});
 }
 
-template <NsKind Kind>
+template <NsKind Kind, int Pieces>
 void product(const NsArgs& a, uint32_t tile, hipStream_t st) {
   const dim3 grid(a.tile_prefix[a.P]);
   if (tile == 256)
-    hipLaunchKernelGGL((ns_product<Kind, 128, 256, 1, 4>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((ns_product<Kind, Pieces, 128, 256, 1, 4>), grid, dim3(256), 0, st, a);
   else if (tile == 128)
-    hipLaunchKernelGGL((ns_product<Kind, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((ns_product<Kind, Pieces, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((ns_product<Kind, 64, 64, 2, 2>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((ns_product<Kind, Pieces, 64, 64, 2, 2>), grid, dim3(256), 0, st, a);
 }
-template <class T>
+template <class T, int Pieces>
 void last(const NsLastArgs& a, uint32_t tile, hipStream_t st) {
   const dim3 grid(a.s.tile_prefix[a.s.P]);
   if (tile == 256)
-    hipLaunchKernelGGL((ns_last<T, 128, 256, 1, 4>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((ns_last<T, Pieces, 128, 256, 1, 4>), grid, dim3(256), 0, st, a);
   else if (tile == 128)
-    hipLaunchKernelGGL((ns_last<T, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((ns_last<T, Pieces, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((ns_last<T, 64, 64, 2, 2>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((ns_last<T, Pieces, 64, 64, 2, 2>), grid, dim3(256), 0, st, a);
 }
 
 template <class F>
@@ -564,16 +614,28 @@ hipError_t launch_orient(const OrientArgs& a, mr_dtype gdt, hipStream_t st) {
   return hipGetLastError();
 }
 hipError_t launch_ns(const NsArgs& a, NsKind kind, uint32_t tile, hipStream_t st) {
-  if (kind == kNsGram)
-    product<kNsGram>(a, tile, st);
-  else if (kind == kNsPoly)
-    product<kNsPoly>(a, tile, st);
+  auto go = [&](auto pieces) {
+    constexpr int kPieces = decltype(pieces)::value;
+    if (kind == kNsGram)
+      product<kNsGram, kPieces>(a, tile, st);
+    else if (kind == kNsPoly)
+      product<kNsPoly, kPieces>(a, tile, st);
+    else
+      product<kNsStep, kPieces>(a, tile, st);
+  };
+  if (a.pieces == 2)
+    go(std::integral_constant<int, 2>{});
   else
-    product<kNsStep>(a, tile, st);
+    go(std::integral_constant<int, 1>{});
   return hipGetLastError();
 }
 hipError_t launch_ns_last(const NsLastArgs& a, mr_dtype dt, uint32_t tile, hipStream_t st) {
-  by_type(dt, [&](auto t) { last<decltype(t)>(a, tile, st); });
+  by_type(dt, [&](auto t) {
+    if (a.s.pieces == 2)
+      last<decltype(t), 2>(a, tile, st);
+    else
+      last<decltype(t), 1>(a, tile, st);
+  });
   return hipGetLastError();
 }
 
