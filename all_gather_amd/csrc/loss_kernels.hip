@@ -221,8 +221,11 @@ struct PackAt {
 // --------------------------------------------------------------------------------- statistics of rows
 //
 // A workgroup takes one of `splits` parts of a row.  The parts' maxima and sums are joined, in their order, by the workgroup
-// that finishes its row last.  Bound by the reads.
-constexpr int kStatPacks = 4;  // packs a lane has in flight
+// that finishes its row last.  Bound by the reads: 16384 rows of 50001 fp16 columns, a tenth of them without a loss, in 225 us (6.5 TB/s
+// of 1.475 GB); 8192 of 32768 fp32 in 154 (6.97 TB/s).  Rows of a wave or less are bound by the 600 instructions a row: 65536 of 512
+// bf16 in 39 us.
+// Packs a lane has in flight: 4 take 62 us there, 2 take 39; 16384 rows of 50001 271 and 262 at the same lanes; 8 take 410.
+constexpr int kStatPacks = 2;
 
 template <class T, bool Policy>
 __global__ __launch_bounds__(1024) void row_stats(LogitArgs a) {
@@ -344,8 +347,10 @@ __global__ __launch_bounds__(1024) void row_stats(LogitArgs a) {
 
 // ------------------------------------------------------------------------------ gradient of the logits
 //
-// dz_j = g/T ([j = t] - exp((z_j - m) / T) / S), element by element; a wave takes a run of packs of one row.
-constexpr int kGradPacks = 4;
+// dz_j = g/T ([j = t] - exp((z_j - m) / T) / S), element by element; a wave takes a run of packs of one row.  Bound by the bytes: 8192
+// rows of 32768 fp32 columns in 339 us (6.33 TB/s, what a copy reaches); 16384 of 50001 bf16, off the 16-byte grid, in 565 (5.8).
+// A wave's packs a lane, 2, 4 and 8: 4096 rows of 131072 bf16 344, 352 and 362 us; 65536 of 512 27, 36 and 56.
+constexpr int kGradPacks = 2;
 
 template <class T>
 __global__ __launch_bounds__(256) void logit_grad(LogitArgs a) {
@@ -413,6 +418,11 @@ __global__ __launch_bounds__(256) void logit_grad(LogitArgs a) {
 // sets; the next row's target is read a row ahead.  Packs lie on z's 16-byte grid; only the first strip's first pack and
 // the last two of the K strips can pass the row's ends (held_row).  Such a pack is read, and stored, as V whole elements from the
 // nearest end on; those that are another pack's add nothing to the sums, and both store the same bits.
+//
+// Bound by the bytes, and by what a workgroup waits between a row's last load and its first store: 8192 rows of 131072 bf16 in
+// 817 us (5.26 TB/s; 833 with the exponentials left out), 8192 of 32768 fp32 in 376 (5.7), 16384 of 50001 bf16, off the grid, in 695
+// (4.7).  (Statistics and gradient as two passes over the same rows: 160 + 344 us for 4096 of 131072, here 408; at most 8, 10 or 12 packs
+// a lane instead of 16 are no faster, nor are loads and stores that stay in the caches.)
 template <class T, int K>
 __global__ __launch_bounds__(1024) void policy_held(LogitArgs a) {
   constexpr int V = 16 / T::kSize, kEnd = K < 2 ? K : 2;
@@ -547,7 +557,8 @@ __device__ __forceinline__ double group_sum(double x, double* lds) {
 
 constexpr int kPrefPacks = 2;  // of 4 floats that a lane has in flight, of each input
 
-// A workgroup takes a pair: the sums of both sequences' log ratios in fp64, then the gradient of each of their tokens.
+// A workgroup takes a pair: the sums of both sequences' log ratios in fp64, then the gradient of each of their tokens.  1024 pairs of
+// 4.4M tokens in 20.4 us: 52.8 MB, 2.6 TB/s.  The longest pairs set it: a workgroup's share is two trips through a few rounds of loads.
 __global__ __launch_bounds__(256, 4) void preference(PreferenceArgs a) {
   __shared__ double lds[kMostWaves];
   const uint32_t lanes = blockDim.x, lane = threadIdx.x;
@@ -615,9 +626,6 @@ __global__ __launch_bounds__(256, 4) void preference(PreferenceArgs a) {
 constexpr size_t kMostGrid = size_t{1} << 20;  // below 2^32 lanes; kernels loop over what lies past their grid
 inline uint32_t grid_of(size_t n) { return static_cast<uint32_t>(n < kMostGrid ? n : kMostGrid); }
 
-inline uint32_t stat_lanes(size_t packs_of_part) {
-  return packs_of_part <= 256 ? 64 : packs_of_part <= 2048 ? 256 : 512;
-}
 
 bool rows_on_grid(const char* z, size_t rows, size_t stride, size_t es) {
   return (reinterpret_cast<uintptr_t>(z) | (rows > 1 ? stride * es : 0)) % 16 == 0;
@@ -625,7 +633,19 @@ bool rows_on_grid(const char* z, size_t rows, size_t stride, size_t es) {
 
 constexpr uint32_t kCus = 256;
 
-// Rows in registers: lanes and packs a lane.
+// Lanes of a workgroup of row_stats.  (Forward pass, us.  Waves alone where a row feeds no more: 65536 rows of 2048 16-bit columns 52,
+// by 256 lanes 212.  A workgroup a compute unit, 1024 lanes and 512: 24 of 32768 5.7 and 6.4, 256 of 131072 14.3 and 18.2; 256 lanes
+// 28.0.  Many rows, 256 and 512: 16384 of 50001 248 and 254, 1001 of 32003 14.0 and 15.7, but 4096 of 131072 163 and 160,
+// 8192 of 32768 fp32 161 and 155; 1024 lanes 14 to 340% more.)
+inline uint32_t stat_lanes(size_t parts, size_t packs_of_part) {
+  if (packs_of_part <= 256) return 64;
+  if (parts <= kCus) return packs_of_part <= 2048 ? 256 : 1024;
+  return packs_of_part < 8192 ? 256 : 512;
+}
+
+// Rows in registers: lanes and packs a lane.  Up to a row for each compute unit as many waves as a row feeds (24 rows of 32768 bf16 7.9 us,
+// by as few as hold it 10.2; 100 9.3 and 11.5); else as few as hold it, so that several rows are on their way at once (8192 of 16384 bf16 102 us, by as
+// many as it feeds 121; 65536 of 2048 101 and 154).
 struct Held {
   uint32_t waves;
   int K;
@@ -673,7 +693,7 @@ void launch_held(const LogitArgs& a, uint32_t groups, hipStream_t st) {
 template <class T, bool Policy>
 void stats(const LogitArgs& a, uint32_t groups, hipStream_t st) {
   const size_t packs = a.packs;
-  hipLaunchKernelGGL((row_stats<T, Policy>), dim3(groups), dim3(stat_lanes((packs + a.splits - 1) / a.splits)), 0, st, a);
+  hipLaunchKernelGGL((row_stats<T, Policy>), dim3(groups), dim3(stat_lanes(a.rows * a.splits, (packs + a.splits - 1) / a.splits)), 0, st, a);
 }
 template <class T>
 void grad(const LogitArgs& a, hipStream_t st) {
@@ -704,9 +724,10 @@ LogitPlan plan_logits(const char* z, size_t rows, size_t cols, size_t stride, mr
   const size_t packs = (cols + V - 1) / V;
   LogitPlan pl{};
   const Held h = held_row(rows, cols, V, rows_on_grid(z, rows, stride, elem_size(dt)));
-  // One row of 131072 16-bit columns by one compute unit takes 16.8 us, in parts by two launches 12.2; 8 rows 16.9 and 17.7; one of
-  // 65536 10.3 and 11.9, 24 of 32768 7.5 and 14.4, 256 of 131072 31 and 46.
-  if (gradient && rows && h.K && (rows >= 8 || h.K <= 8)) {
+  // A few rows of many packs a lane take longer in one launch than in two of all compute units (us, one and two): 8 rows of 131072
+  // 16-bit columns 17.2 and 14.0, 48 17.9 and 18.1; 8 of 100000 15.2 and 14.1, 32 16.0 and 16.5; one of 65536 10.5 and 11.5; 24 of 32768
+  // 7.9 and 14.4.
+  if (gradient && rows && h.K && (rows >= kCus / 8 || h.K <= 12)) {
     pl.held = 1;
     pl.splits = 1;
     const size_t per_cu = (h.K <= 4 ? 24 : 16) / h.waves;  // waves that a compute unit's registers hold
@@ -714,11 +735,12 @@ LogitPlan plan_logits(const char* z, size_t rows, size_t cols, size_t stride, mr
     pl.groups = static_cast<uint32_t>((rows + rounds - 1) / rounds);
     return pl;
   }
+  // A few long rows: each over several workgroups, one on every compute unit.  (Forward pass, us, in parts and whole: 1 row of
+  // 131072 16-bit columns 6.0 and 10.5, 63 8.2 and 12.3, 2 of 262144 6.0 and 19.4, 8 of 32768 5.8 and 5.4.  Up to 1024 parts, whose
+  // arrivals wait for one another: 16 of 131072 16.4 against 8.1.)
   size_t splits = 1;
-  if (rows && packs && rows < 4 * kCus) {  // too few rows for the device: each over several workgroups, of at least 64 lanes' loads
-    splits = (4 * kCus + rows - 1) / rows;
-    const size_t most = (packs + 64 * kStatPacks - 1) / (64 * kStatPacks);
-    splits = splits > most ? most : splits;
+  if (rows && rows < kCus / 4 && packs > 4096) {
+    splits = kCus / rows;
     splits = splits > 64 ? 64 : splits;
   }
   pl.splits = static_cast<uint32_t>(splits);

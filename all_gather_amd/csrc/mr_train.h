@@ -111,7 +111,7 @@ struct LogitArgs {
   double clip_lo, clip_hi, kl, grad_scale;
   float* record;
   // workspace
-  float* part;            // [rows][splits][3]: maximum, sum, target's logit (or -inf) of a part of a row
+  float* part;            // [rows][splits][2]: maximum and sum of a part of a row
   uint32_t* row_arrived;  // [rows] parts that are done; zero between launches
   double* sums;           // [workgroups + kNormSets][4] parts of the policy loss's record
   uint32_t (*arrived)[64];

@@ -442,8 +442,8 @@ mr_status mr_preference_loss(const float* logp, const float* ref_logp, size_t ro
  * Growth at least doubles the size and keeps the replaced buffer alive, so launches in flight and HIP
  * graphs that captured a two-shot call on the stream stay valid; replaced buffers are freed only by
  * mr_set_workspace on that stream.  One workspace per (device, stream): eager two-shot calls on
- * different streams never share barrier words.  The layer norm's backward pass and the gradient norm keep their partial
- * sums there too.  Calls on one stream from several host threads are safe: each enqueues its kernels together.
+ * different streams never share barrier words.  The layer norm's backward pass, the gradient norm and the losses keep
+ * their partial sums there too, mr_muon_step its matrices.  Calls on one stream from several host threads are safe: each enqueues its kernels together.
  * (hipStreamPerThread is one handle and a stream of each thread: make such calls on it from one thread only.)
  *
  * A two-shot call made while its stream is being captured into a HIP graph uses a library-owned
@@ -459,7 +459,7 @@ mr_status mr_preference_loss(const float* logp, const float* ref_logp, size_t ro
  * gave up (the call that timed out has invalid output; later calls are unaffected).
  *
  * mr_workspace_bytes: bytes a caller-owned workspace needs for a two-shot call of this shape (and, as described there,
- *                     for mr_layer_norm_backward and mr_grad_norm).
+ *                     for mr_layer_norm_backward, mr_grad_norm and the losses).
  * mr_set_workspace:   bind caller-owned device memory (256-byte aligned) as the workspace of `stream`
  *                     on the current device, replacing any library-owned one; the barrier words and
  *                     flags are cleared on `stream` here.  Memory too small to hold them plus some

@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 
 S_TOL, P_TOL = 2.0 ** -16, 2.0 ** -15
 SHAPES = [(1, 1), (3, 2), (5, 7), (130, 8), (300, 9), (4, 63), (257, 100), (131, 513), (1, 4097), (140, 4096), (200, 8193), (2, 32771),
-          (129, 32771), (3, 131072), (128, 131072), (129, 65537), (130, 131073), (6, 262144)]
+          (129, 32771), (3, 131072), (128, 131072), (129, 65537), (130, 131073), (6, 262144), (62, 50000), (300, 70001)]
 
 
 def case(rows, cols, dtype, pad=0, shift=0, seed=0, dead=0.3):
