@@ -220,9 +220,12 @@ struct NsLastArgs {
   const float* clip;
   float keep;
 };
-// Columns of a product's tiles for a matrix of m rows, in a list whose larger matrices have many such tiles or few.
-uint32_t ns_tile(uint32_t m, bool many);
-bool ns_many(uint64_t wide_tiles);
+// Columns of a product's tiles for a matrix of m rows, in a list of so many tiles of 256 columns and of 128 if all that can take them do.
+struct NsTiles {
+  uint64_t wide, square;
+};
+constexpr uint32_t kNsWideFrom = 512, kNsSquareFrom = 256;  // rows
+uint32_t ns_tile(uint32_t m, const NsTiles& list, int pieces);
 uint32_t ns_tiles(uint32_t tile, uint32_t rows, uint32_t cols, bool symmetric);
 hipError_t launch_momentum(const MomentumArgs& a, mr_dtype gdt, hipStream_t st);
 hipError_t launch_orient(const OrientArgs& a, mr_dtype gdt, hipStream_t st);

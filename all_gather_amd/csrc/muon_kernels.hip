@@ -602,11 +602,21 @@ void by_type(mr_dtype dt, F f) {
 
 }  // namespace
 
-// Tiles of 128 x 256 ask least of LDS and L2, tiles of 128 x 128 leave fewer compute units idle at a launch's end.  A step, wide tiles
-// and square ones (ms): eight of 4096 x 4096 11.2 and 12.7; one (512 wide tiles a product) 1.98 and 1.91; one of 2048 x 2048 0.56 and
-// 0.47; one of 4096 x 8192 (1024) 3.08 and 3.04, of 4096 x 16384 (2048) 5.33 and 5.41.
-uint32_t ns_tile(uint32_t m, bool many) { return m >= 1024 && many ? 256 : m >= 512 ? 128 : 64; }
-bool ns_many(uint64_t wide_tiles) { return wide_tiles > 1024; }
+// Tiles of 128 x 256 ask least of LDS and L2, tiles of 128 x 128 and of 64 x 64 leave fewer compute units idle where a launch has few.
+// A step with wide tiles and square ones (ms): eight of 4096 x 4096 11.2 and 12.7; 32 of 768 x 8192 4.45 and 4.64; one of 4096 x 4096
+// (512 wide tiles a product) 1.98 and 1.91; one of 2048 x 2048 0.56 and 0.47; one of 4096 x 8192 (1024) 3.08 and 3.04, of
+// 4096 x 16384 (2048) 5.33 and 5.41.
+// With tiles of 128 x 128 and of 64 x 64 (us): one of 512 x 512 171 and 124, eight (128 square tiles a product) 200 and 160, 32 (512) 372
+// and 393; one of 1024 x 1024 (64) 237 and 177, one of 1536 x 4096 (384) 452 and 424, eight of 1000 x 1000 (648) 455 and 470; 32 of
+// 384 x 1536 (1152) 439 and 476.
+// In two pieces the order of an element's sums differs between tile sizes (A and P are mirrored), so there a matrix's rows alone choose
+// between the smaller two: in a list without wide tiles it gets the bits that it gets alone.  (One of 512 x 512 255 us by 128 x 128, 172 by 64 x 64.)
+constexpr uint64_t kNsMany = 1024, kNsSome = 400;
+uint32_t ns_tile(uint32_t m, const NsTiles& list, int pieces) {
+  if (m >= kNsWideFrom && list.wide > kNsMany) return 256;
+  if (pieces == 2) return m >= kNsWideFrom ? 128 : 64;
+  return m >= kNsSquareFrom && list.square > kNsSome ? 128 : 64;
+}
 
 uint32_t ns_tiles(uint32_t tile, uint32_t rows, uint32_t cols, bool symmetric) {
   const uint32_t bm = tile == 256 ? 128 : tile, bn = tile, ratio = bn / bm;

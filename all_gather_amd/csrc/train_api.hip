@@ -763,10 +763,12 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
                    static_cast<int>(gdtype), h->products, master ? 1 : 0, static_cast<unsigned long long>(g.bytes));
     hipError_t e = mr::launch_momentum(mo, gdtype, st);
     if (e == hipSuccess) e = mr::launch_orient(od, gdtype, st);
-    uint64_t wide = 0;
-    for (uint32_t k = 0; k < mo.P; ++k)
-      if (mr::ns_tile(mats[k].s.m, true) == 256) wide += mr::ns_tiles(256, mats[k].s.ldm, mats[k].s.ldn, false);
-    const bool many = mr::ns_many(wide);
+    mr::NsTiles list{0, 0};
+    for (uint32_t k = 0; k < mo.P; ++k) {
+      const MuonShape& z = mats[k].s;
+      if (z.m >= mr::kNsWideFrom) list.wide += mr::ns_tiles(256, z.ldm, z.ldn, false);
+      if (z.m >= mr::kNsSquareFrom) list.square += mr::ns_tiles(128, z.ldm, z.ldn, false);
+    }
     // one launch for the matrices of each tile size; those of the longest sums first, so that the short tiles fill the end
     uint32_t order[mr::kMuonMats];
     for (uint32_t k = 0; k < mo.P; ++k) order[k] = k;
@@ -781,7 +783,7 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
           for (uint32_t o = 0; o < mo.P; ++o) {
             const Mat& q = mats[order[o]];
             const MuonShape& z = q.s;
-            if (mr::ns_tile(z.m, many) != tile) continue;
+            if (mr::ns_tile(z.m, list, pieces) != tile) continue;
             mr::NsProduct& p = a.p[a.P];
             p.M = z.m;
             p.ldct = z.ldm;
