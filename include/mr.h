@@ -402,7 +402,8 @@ mr_status mr_muon_step(const void* const* params, const void* const* grads, cons
  *     pass over the logits where a row fits a workgroup's registers (131072 16-bit or 65536 fp32 columns; fewer than 32 rows of more
  *     than three quarters of that are read twice).  A term that is
  *     clipped, and only that, passes no gradient.
- *       old_logp  of the policy that sampled the tokens; NULL: of this one (r = 1).  ref_logp: NULL without a KL term (d = 0).
+ *       old_logp  of the policy that sampled the tokens; NULL: of this one (r = 1).  ref_logp: NULL without a KL term (d = 0); with
+ *       kl_coef 0 the term is reported in record[1] and left out of the loss and the gradient.  exp is finite up to fp64's range.
  *       advantages  rows floats;  weights: rows floats (a mask over its sum, say), or NULL: ones.
  *       logp, dlogits  or NULL.
  * mr_preference_loss:  rows hold 2 * pairs sequences, sequence k in [offsets[k], offsets[k+1]): pair p's chosen one is 2p, its
