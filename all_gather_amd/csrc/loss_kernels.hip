@@ -135,7 +135,7 @@ struct PolicyIn {
 };
 __device__ __forceinline__ PolicyRow policy_row(const LogitArgs& a, const PolicyIn& in, double logp) {
   const double w = static_cast<double>(in.w), adv = static_cast<double>(in.adv);
-  const double r = a.old_logp ? exp_of(static_cast<float>(logp - static_cast<double>(in.old))) : logp - logp + 1.0;
+  const double r = a.old_logp ? exp_of(static_cast<float>(logp - static_cast<double>(in.old))) : logp != logp ? logp : 1.0;  // (NaN stays; a target that is ruled out has r = 1 too)
   double near = r < 1.0 - a.clip_lo ? 1.0 - a.clip_lo : r;
   near = near > 1.0 + a.clip_hi ? 1.0 + a.clip_hi : near;
   const double free = -adv * r, held = -adv * near;

@@ -70,3 +70,28 @@ def test_small_differences_keep_their_bits(rows, cols):
     mr.policy_loss(z, t, adv, a, old_logp=old, ref_logp=ref, kl=0.0, dlogits=da)
     mr.policy_loss(z, t, adv, b, old_logp=old, kl=0.0, dlogits=db)
     assert torch.equal(da, db) and torch.equal(a[[0, 2, 3]], b[[0, 2, 3]]) and float(a[1]) > 0 and float(b[1]) == 0
+
+
+@pytest.mark.parametrize("rows,cols", PATHS)
+def test_a_ruled_out_target_under_its_own_policy(rows, cols):
+    """Without old_logp the ratio is 1 in every row, also where the target's logit is -inf: a loss of -A, and the gradient that r = 1 gives."""
+    z, t, rand = case(rows, cols, "fp32", seed=23, dead=0.0)
+    z[2, 5], t[2] = -float("inf"), 5
+    z[3], t[3] = -float("inf"), 5                    # nothing left in the row: NaN
+    adv = rand(rows)
+    for grad in (True, False):
+        w = torch.ones(rows, device=device())
+        w[3] = 0.0
+        record, logp, out = torch.empty(4, device=device()), torch.empty(rows, device=device()), torch.empty_like(z)
+        mr.policy_loss(z, t, adv, record, weights=w, logp=logp, dlogits=out if grad else None)
+        assert float(logp[2]) == -float("inf")
+        want = -adv.double()[w != 0].sum()
+        assert abs(float(record[0]) - float(want)) <= 2.0 ** -23 * float(adv.double().abs().sum()) and float(record[2]) == 0
+        if grad:
+            lp, p, live = exact_logp(z, t, 1.0)
+            live = live & (w != 0)
+            g, p = torch.where(live, -adv.double(), 0.0), torch.where(live[:, None], p, 0.0)  # (a row of nothing has no probabilities)
+            check_gradient(out, exact_gradient(p, t, live, g, 1.0), p, t, live, g, 1.0, "fp32")
+        w[3] = 1.0
+        mr.policy_loss(z, t, adv, record, weights=w)
+        assert record[0].isnan() and float(record[3]) == rows
