@@ -152,24 +152,27 @@ hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st);
 // product reads one and writes the other), A = X X^T and P = a I + b A + c A^2 [m][ldm]; ldm and ldn are m and n rounded up to
 // three of a product's stages (ns_padded), and columns past m and n are zero.
 constexpr int kMuonMats = 32;       // matrices of one launch
+constexpr uint32_t kMuonCount = 32; // words from a matrix's arrival counter to the next one's
 constexpr uint32_t kNsK = 32;       // columns that a product takes at a time: a stage
 constexpr uint32_t kNsPad = 3 * kNsK;
 __host__ __device__ inline uint32_t ns_padded(uint32_t n) { return (n + kNsPad - 1) / kNsPad * kNsPad; }
 constexpr int kNsShift = 12;        // matrices are held times 2^12
-inline uint32_t momentum_tile(uint64_t n) { return n < uint64_t{1} << 23 ? 4096 : 16384; }  // elements, for n in all
+inline uint32_t momentum_tile(uint64_t n) { return n < uint64_t{1} << 21 ? 4096 : 16384; }  // elements, of a matrix of n
+inline uint32_t momentum_tiles(uint64_t n) { return static_cast<uint32_t>((n + momentum_tile(n) - 1) / momentum_tile(n)); }
 struct MomentumArgs {
   const char* g[kMuonMats];
   uint64_t n[kMuonMats];
   uint64_t at[kMuonMats];  // first element in the flat state
+  uint32_t tile[kMuonMats];  // elements of its tiles
   uint32_t tile_prefix[kMuonMats + 1];
-  uint32_t P, tile;
+  uint32_t P;
   const float* m;
   float* m_out;
   float* master_out;      // null: none (its elements between matrices become zeros)
   const float* clip;      // {norm, factor, all finite} or null
   double* sums;           // [tiles] sums of squares
   double* norms;          // [P] their sums
-  uint32_t* arrived;      // [P] zero between launches
+  uint32_t* arrived;      // [P][kMuonCount] zero between launches: a matrix's arrivals in a line of its own
   float mu, c;            // c = 1 - mu
   int nesterov;
 };

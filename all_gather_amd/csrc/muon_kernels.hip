@@ -69,20 +69,23 @@ __device__ __forceinline__ double group_sum(double x) {
 
 // m' of a tile of one matrix, and its part of |u|^2 in fp64; the workgroup that finishes its matrix last adds the parts up in order.
 // Bound by the bytes (m, g, m'), so every load of 4096 elements is on its way before the first is used: 201M elements with bf16
-// gradients in 360 us (5.6 TB/s).  Large tiles for large
-// matrices: each workgroup counts its arrival at its matrix's one address, which takes 11.6 ns.
+// gradients in 360 us (5.6 TB/s).  A matrix's own size sets its tiles, so that its norm is summed in the same order alone and in any
+// list.  Large tiles for large matrices: a workgroup counts its arrival at its matrix's counter, which takes 11.6 ns (2000 x 2000 16.5 us,
+// by tiles of 4096 21.2; 1500 x 1500 14.3 by both).  Counters lie a line apart: neighbours' arrivals wait for one another (48 of 2048 x 2048
+// by tiles of 4096 took 240 us longer).
 template <class G>
 __global__ __launch_bounds__(256) void momentum(MomentumArgs a) {
   const Clip clip = clip_of(a.clip);
   const uint32_t i = entry_of(a.tile_prefix, a.P, blockIdx.x), tile = blockIdx.x - a.tile_prefix[i];
+  const uint32_t tile_elems = a.tile[i];
   const uint64_t n = a.n[i], padded = (n + kMxBlock - 1) / kMxBlock * kMxBlock;
-  const uint64_t end = uint64_t{tile + 1} * a.tile < padded ? uint64_t{tile + 1} * a.tile : padded;
+  const uint64_t end = uint64_t{tile + 1} * tile_elems < padded ? uint64_t{tile + 1} * tile_elems : padded;
   const char* g = a.g[i];
   const float* m = a.m + a.at[i];
   float* mo = a.m_out + a.at[i];
   constexpr int kU = 4;
   double s = 0.0;
-  for (uint64_t e0 = uint64_t{tile} * a.tile + threadIdx.x * 4; e0 < end; e0 += kU * 1024) {
+  for (uint64_t e0 = uint64_t{tile} * tile_elems + threadIdx.x * 4; e0 < end; e0 += kU * 1024) {
     Raw<G, 4> gr[kU];
     Raw<EFp32, 4> mr[kU];
     const bool whole = e0 - threadIdx.x * 4 + kU * 1024 <= n;
@@ -125,7 +128,7 @@ __global__ __launch_bounds__(256) void momentum(MomentumArgs a) {
     __hip_atomic_store(a.sums + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    last = __hip_atomic_fetch_add(a.arrived + i, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == tiles - 1;
+    last = __hip_atomic_fetch_add(a.arrived + i * kMuonCount, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == tiles - 1;
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
   }
   __syncthreads();
@@ -136,7 +139,7 @@ __global__ __launch_bounds__(256) void momentum(MomentumArgs a) {
   s = group_sum(s);
   if (threadIdx.x == 0) {
     a.norms[i] = __builtin_sqrt(s);
-    __hip_atomic_store(a.arrived + i, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(a.arrived + i * kMuonCount, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
 

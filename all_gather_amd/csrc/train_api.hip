@@ -589,28 +589,24 @@ MuonShape muon_shape(uint64_t rows, uint64_t cols, int pieces) {
   s.halves = pieces * (uint64_t{s.m} * s.ldn + 2 * (uint64_t{s.n} * s.ldm) + 2 * (uint64_t{s.m} * s.ldm));
   return s;
 }
-uint32_t momentum_tiles(uint64_t n, uint32_t tile) { return static_cast<uint32_t>((n + tile - 1) / tile); }
 
 // Matrices of one workspace: those from `first` on that fit together, and the bytes they take.
 struct MuonGroup {
   int first, end, count;  // count: those that are not empty
   uint64_t bytes;         // of halves, then sums, then norms
   uint64_t sums;
-  uint32_t tile;  // of the momentum's elements
 };
 MuonGroup muon_group(const uint64_t* rows, const uint64_t* cols, int P, int first, int pieces) {
-  MuonGroup g{first, first, 0, 0, 0, 0};
-  uint64_t halves = 0, elems = 0;
+  MuonGroup g{first, first, 0, 0, 0};
+  uint64_t halves = 0;
   for (; g.end < P && g.count < mr::kMuonMats; ++g.end) {
     if (rows[g.end] * cols[g.end] == 0) continue;
     const uint64_t more = muon_shape(rows[g.end], cols[g.end], pieces).halves;
     if (g.count && (halves + more) * 2 > kMuonGroupBytes) break;
     halves += more;
-    elems += rows[g.end] * cols[g.end];
+    g.sums += mr::momentum_tiles(rows[g.end] * cols[g.end]);
     ++g.count;
   }
-  g.tile = mr::momentum_tile(elems);
-  for (int i = first; i < g.end; ++i) g.sums += momentum_tiles(rows[i] * cols[i], g.tile);
   g.bytes = halves * 2 + g.sums * 8 + mr::kMuonMats * 8;
   return g;
 }
@@ -630,7 +626,7 @@ size_t muon_workspace(const uint64_t* rows, const uint64_t* cols, int P, int pro
     most = std::max(most, g.bytes);
     i = g.end;
   }
-  return mr::workspace_bytes_for(std::max<uint64_t>(most, row_words_bytes(mr::kMuonMats)), 1);
+  return mr::workspace_bytes_for(std::max<uint64_t>(most, row_words_bytes(mr::kMuonMats * mr::kMuonCount)), 1);
 }
 
 mr_status muon_step(const void* const* params, const void* const* grads, const uint64_t* rows, const uint64_t* cols, int P, mr_dtype dtype,
@@ -689,7 +685,7 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
   mr::Ctrl* ctrl = nullptr;
   char* data = nullptr;
   std::unique_lock<std::mutex> use;  // to the last launch
-  uint64_t most = row_words_bytes(mr::kMuonMats);
+  uint64_t most = row_words_bytes(mr::kMuonMats * mr::kMuonCount);
   for (int i = 0; i < P;) {
     const MuonGroup g = muon_group(rows, cols, P, i, pieces);
     most = std::max(most, g.bytes);
@@ -730,7 +726,8 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
       mo.g[k] = static_cast<const char*>(grads[i]);
       mo.n[k] = count(i);
       mo.at[k] = at;
-      mo.tile_prefix[k + 1] = mo.tile_prefix[k] + momentum_tiles(count(i), g.tile);
+      mo.tile[k] = mr::momentum_tile(count(i));
+      mo.tile_prefix[k + 1] = mo.tile_prefix[k] + mr::momentum_tiles(count(i));
       od.g[k] = mo.g[k];
       od.direct[k] = z.turned ? q.xt[0] : q.x;
       od.turned[k] = z.turned ? q.x : q.xt[0];
@@ -742,7 +739,6 @@ mr_status muon_step(const void* const* params, const void* const* grads, const u
     }
     first = g.end;
     if (mo.P == 0) continue;
-    mo.tile = g.tile;
     mo.m = in->momentum;
     mo.m_out = out->momentum;
     mo.master_out = out->master;
