@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 from typing import Any, Sequence
 
@@ -471,7 +472,7 @@ def _rows2d(t, what: str, ref=None):
     if not t.is_cuda or (ref is not None and (t.dtype != ref.dtype or t.shape != ref.shape)):
         raise ValueError(f"{what} must be a device tensor" + (f" of {ref.dtype}, shaped like the logits" if ref is not None else ""))
     cols = t.shape[-1] if t.dim() else 1
-    rows = t.numel() // cols if cols else (t.shape[0] if t.dim() > 1 else 0)
+    rows = t.numel() // cols if cols else (math.prod(t.shape[:-1]) if t.dim() > 1 else 0)
     if t.is_contiguous() or rows <= 1 and (cols <= 1 or t.stride(-1) == 1):
         return rows, cols, cols
     if t.dim() == 2 and (t.stride(1) == 1 or cols == 1) and t.stride(0) >= cols:
