@@ -192,11 +192,11 @@ struct OrientArgs {
   int nesterov, pieces;
 };
 // C = A B^T with A [M][K], B [N][K], and what becomes of it:
-enum NsKind { kNsGram, kNsPoly, kNsStep, kNsLast };
+enum NsKind { kNsGram, kNsPoly, kNsStep };
 struct NsProduct {
   const _Float16* a;
   const _Float16* b;
-  _Float16* c;       // [M][ldc]; kNsLast: unused
+  _Float16* c;       // [M][ldc]; the last product: unused
   _Float16* ct;      // [N][ldct], the transpose (kNsStep)
   uint32_t M, N, K;    // K: padded
   uint32_t ldc, ldct;  // N and M padded: the tiles cover them

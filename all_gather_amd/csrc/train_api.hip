@@ -614,7 +614,7 @@ MuonGroup muon_group(const uint64_t* rows, const uint64_t* cols, int P, int firs
 mr_status check_matrices(const uint64_t* rows, const uint64_t* cols, int P) {
   if (P < 0 || (P && (!rows || !cols))) return MR_ERR_INVALID_ARG;
   for (int i = 0; i < P; ++i)
-    if (rows[i] > kMostSide || cols[i] > kMostSide || rows[i] * cols[i] > kMaxCount) return MR_ERR_INVALID_ARG;
+    if (rows[i] > kMostSide || cols[i] > kMostSide) return MR_ERR_INVALID_ARG;
   return MR_OK;
 }
 

@@ -350,7 +350,7 @@ mr_status mr_adamw_step(const void* const* params, const void* const* grads, con
  *     p' = (1 - lr*weight_decay)*p - lr*s*X,   s = sqrt(max(1, rows/cols)) (MR_MUON_RATIO) or 0.2 sqrt(max(rows, cols)) (MR_MUON_RMS)
  *
  *  params, grads  host arrays of P device pointers to row-major matrices, as for mr_adamw_step (types, alignment, NULL params
- *           with a master copy and params_out).  rows[i], cols[i] <= 65536, rows[i]*cols[i] <= 2^33, either may be 0.
+ *           with a master copy and params_out).  rows[i], cols[i] <= 65536, either may be 0.
  *  state    momentum and master: floats, laid out as mr_adamw_state_elems says (counts rows[i]*cols[i]), 256-byte aligned;
  *           elements between matrices become 0.  master NULL: none; with it, p is read from master and written to both.
  *  params_out, state_out  where results go; NULL: in place.  Each output may be its own input exactly; any other overlap
