@@ -460,6 +460,9 @@ struct Tile {
     const uint32_t in = wave / kPer;
     float* lds = reinterpret_cast<float*>(in == 0 ? stage<0>() : in == 1 ? stage<1>() : stage<2>()) + wave % kPer * (kCr * kCc);
     const uint32_t r0 = ti * BM + wave / WC * (BM / WR), c0 = tj * BN + wave % WC * (BN / WC);
+    // What was fetched past the end is on its way to the stages that are written next, and a barrier does not wait for it.
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    asm volatile("" ::: "memory");
     __syncthreads();  // the stages have been read
 #pragma unroll
     for (int h = 0; h < kMi * 32 / kCr; ++h) {
