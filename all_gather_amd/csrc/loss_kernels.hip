@@ -99,23 +99,22 @@ __device__ __forceinline__ bool row_live(const LogitArgs& a, size_t row, uint32_
   return high == 0 && *t < static_cast<uint32_t>(a.cols) && weight != 0;
 }
 
-// exp(d) past fp32's range, finite as far as fp64 goes: what a coefficient of 0 or a small weight multiplies stays a number.
-// (expf's error 8 times over: 2^-20.)
+// exp(d), past fp32's range as an eighth power, finite as far as fp64 goes (expf's error 8 times over: 2^-20): what a coefficient of 0 or a
+// small weight multiplies stays a number.
 constexpr float kExpRange = 88.0f;
-__device__ __forceinline__ double exp_past(float d) {
-  double e = static_cast<double>(expf(0.125f * d));
+__device__ __forceinline__ double exp_of(float d) {
+  const bool past = d > kExpRange;
+  double e = static_cast<double>(expf(past ? 0.125f * d : d));
+  if (!past) return e;
   e *= e;
   e *= e;
   return e * e;
 }
-__device__ __forceinline__ double exp_of(float d) { return d > kExpRange ? exp_past(d) : static_cast<double>(expf(d)); }
-__device__ __forceinline__ double expm1_of(float d) { return d > kExpRange ? exp_past(d) : static_cast<double>(expm1f(d)); }
 
-// exp(d) - d - 1, without the cancellation of its leading terms where d is small: there its power series, whose first
-// term left out, d^11 / 11!, is below 2^-24 of the sum for |d| <= 1.
-__device__ __forceinline__ double excess(float d) {
-  if (d > kExpRange) return exp_past(d);
-  if (fabsf(d) > 1.0f) return expm1f(d) - d;
+// exp(d) - d - 1 (`e` is expm1f(d)), without the cancellation of its leading terms where d is small: there its power series,
+// whose first term left out, d^11 / 11!, is below 2^-23 of the sum for |d| <= 1 (2^-24 down to d = -0.98).
+__device__ __forceinline__ float excess(float d, float e) {
+  if (fabsf(d) > 1.0f) return e - d;
   float p = 1.0f + d * (1.0f / 10.0f);
 #pragma unroll
   for (int n = 9; n >= 3; --n) p = 1.0f + d * p * (1.0f / static_cast<float>(n));
@@ -135,20 +134,27 @@ struct PolicyIn {
 };
 __device__ __forceinline__ PolicyRow policy_row(const LogitArgs& a, const PolicyIn& in, double logp) {
   const double w = static_cast<double>(in.w), adv = static_cast<double>(in.adv);
-  const double r = a.old_logp ? exp_of(static_cast<float>(logp - static_cast<double>(in.old))) : logp != logp ? logp : 1.0;  // (NaN stays; a target that is ruled out has r = 1 too)
+  // (without old_logp: NaN stays, and a target that is ruled out has r = 1 too)
+  const double r = a.old_logp ? exp_of(static_cast<float>(logp - static_cast<double>(in.old))) : logp != logp ? logp : 1.0;
   double near = r < 1.0 - a.clip_lo ? 1.0 - a.clip_lo : r;
   near = near > 1.0 + a.clip_hi ? 1.0 + a.clip_hi : near;
   const double free = -adv * r, held = -adv * near;
   const bool cut = held > free;
   PolicyRow p;
-  double g = cut ? 0.0 : free, k = 0.0;
+  double g = cut ? 0.0 : free, k = 0.0, term = 0.0;
   if (a.ref_logp) {
     const float d = static_cast<float>(static_cast<double>(in.ref) - logp);
-    k = excess(d);
-    if (a.kl != 0.0) g -= a.kl * expm1_of(d);
+    const float e = expm1f(d);
+    double more = static_cast<double>(e);
+    k = static_cast<double>(excess(d, e));
+    if (d > kExpRange) more = k = exp_of(d);
+    if (a.kl != 0.0) {  // a coefficient of 0 leaves the term out, whatever it is
+      g -= a.kl * more;
+      term = a.kl * k;
+    }
   }
   p.g = static_cast<float>(a.grad_scale * w * g);
-  p.loss = w * ((cut ? held : free) + (a.kl != 0.0 ? a.kl * k : 0.0));  // (a coefficient of 0 leaves the term out)
+  p.loss = w * ((cut ? held : free) + term);
   p.kl = w * k;
   p.held = cut ? w : 0.0;
   p.w = w;
