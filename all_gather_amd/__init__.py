@@ -520,7 +520,7 @@ def policy_loss(logits, targets, advantages, record, old_logp=None, ref_logp=Non
     """The clipped policy loss with a KL term, and its gradient, in one pass over the logits.
 
     Each token's loss is max(-A r, -A min(max(r, 1 - clip[0]), 1 + clip[1])) + kl * (exp(d) - d - 1), where r = exp(logp - old_logp)
-    and d = ref_logp - logp (old_logp None: r = 1; ref_logp None: no KL term).  ``record`` (4 floats) receives the sums over the
+    and d = ref_logp - logp (old_logp None: r = 1; ref_logp None: no KL term; kl = 0: the term is reported in the record alone).  ``record`` (4 floats) receives the sums over the
     tokens of weight * loss, weight * (exp(d) - d - 1), weight * [clipped], and weight; ``weights`` None stands for ones, and rows of
     weight 0 or a target outside the vocabulary are left out.  ``dlogits`` (the logits themselves, or shaped like them), if given,
     receives the gradient of grad_scale * record[0]; ``logp`` the tokens' log-probabilities.  advantages, old_logp, ref_logp,
@@ -804,8 +804,8 @@ def muon_step(params: Sequence, grads: Sequence, state: MuonState, lr: float, pa
               steps: int = 5, adjust: str = "ratio", products: int = 16, clip=None, stream=None) -> None:
     """One Muon step over the matrices ``params``, in place or into ``params_out`` / ``state_out``: momentum, ``steps`` Newton-Schulz
     iterations on the update, and p' = (1 - lr * weight_decay) * p - lr * s * X, where s is sqrt(max(1, rows / cols)) (``adjust``
-    "ratio") or 0.2 * sqrt(max(rows, cols)) ("rms").  ``products``: 16 (operands rounded to fp16) or 32 (as exact as fp32, at three
-    times the work).  ``coefficients``: one (a, b, c) or one for every step.  ``clip``: grad_norm's record, whose factor multiplies the
+    "ratio") or 0.2 * sqrt(max(rows, cols)) ("rms").  ``products``: 16 (operands rounded to fp16: X is off by 1e-3 to 2e-2 of its norm,
+    which 16-bit parameters hardly resolve and fp32 parameters or master copies do) or 32 (as exact as fp32, at three times the work).  ``coefficients``: one (a, b, c) or one for every step.  ``clip``: grad_norm's record, whose factor multiplies the
     gradients and which leaves the step out where a gradient is not finite."""
     prepare_muon(params, grads, state, params_out, state_out, momentum, nesterov, weight_decay, eps, coefficients, steps, adjust, products,
                  clip, stream)(lr)

@@ -439,9 +439,11 @@ __global__ __launch_bounds__(256) void logit_grad(LogitArgs a) {
 // nearest end on; those that are another pack's add nothing to the sums, and both store the same bits.
 //
 // Bound by the bytes, and by what a workgroup waits between a row's last load and its first store: 8192 rows of 131072 bf16 in
-// 817 us (5.26 TB/s; 833 with the exponentials left out), 8192 of 32768 fp32 in 376 (5.7), 16384 of 50001 bf16, off the grid, in 695
-// (4.7).  (Statistics and gradient as two passes over the same rows: 160 + 344 us for 4096 of 131072, here 408; at most 8, 10 or 12 packs
-// a lane instead of 16 are no faster, nor are loads and stores that stay in the caches.)
+// 802 to 822 us (5.3 TB/s; no less with the exponentials left out), 8192 of 32768 fp32 in 379 (5.7), 16384 of 50001 bf16 in 685 (4.8;
+// of 50048, whose rows start on 128-byte lines, 616 to 626).  Rows are dealt out by a stride, so the workgroups that meet no ignored row set
+// the time: 4096 of 50001 take 169 to 179 all live, and 173 with a quarter ignored.  K = 16 keeps 4 registers in scratch (20 bytes a lane), which
+// its row loop loads again; no other K does.  (Statistics and gradient as two passes over the same rows: 160 + 344 us for 4096 of 131072,
+// here 402; at most 8, 10 or 12 packs a lane instead of 16 are no faster, nor are loads and stores that stay in the caches.)
 template <class T, int K>
 __global__ __launch_bounds__(1024) void policy_held(LogitArgs a) {
   constexpr int V = 16 / T::kSize, kEnd = K < 2 ? K : 2;
@@ -577,7 +579,8 @@ __device__ __forceinline__ double group_sum(double x, double* lds) {
 constexpr int kPrefPacks = 2;  // of 4 floats that a lane has in flight, of each input
 
 // A workgroup takes a pair: the sums of both sequences' log ratios in fp64, then the gradient of each of their tokens.  1024 pairs of
-// 4.4M tokens in 20.4 us: 52.8 MB, 2.6 TB/s.  The longest pairs set it: a workgroup's share is two trips through a few rounds of loads.
+// 4.4M tokens in 20.4 us: 52.8 MB, 2.6 TB/s.  The longest pairs set it: a workgroup's share is two trips through a few rounds of loads
+// (8 pairs of 2 x 16384 20.5 us, one of 2 x 100000 96).
 __global__ __launch_bounds__(256, 4) void preference(PreferenceArgs a) {
   __shared__ double lds[kMostWaves];
   const uint32_t lanes = blockDim.x, lane = threadIdx.x;
@@ -756,7 +759,8 @@ LogitPlan plan_logits(const char* z, size_t rows, size_t cols, size_t stride, mr
   }
   // A few long rows: each over several workgroups, one on every compute unit.  (Forward pass, us, in parts and whole: 1 row of
   // 131072 16-bit columns 6.0 and 10.5, 63 8.2 and 12.3, 2 of 262144 6.0 and 19.4, 8 of 32768 5.8 and 5.4.  Up to 1024 parts, whose
-  // arrivals wait for one another: 16 of 131072 16.4 against 8.1.)
+  // arrivals wait for one another: 16 of 131072 16.4 against 8.1.  Whole rows leave compute units idle below 256 of them: 64 take 11.8,
+  // 128 12.7; two to four parts for those were not measured.)
   size_t splits = 1;
   if (rows && rows < kCus / 4 && packs > 4096) {
     splits = kCus / rows;

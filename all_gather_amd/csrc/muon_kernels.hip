@@ -217,11 +217,11 @@ __global__ __launch_bounds__(256) void orient(OrientArgs a) {
 // chunk c of row r lies at place c ^ swizzle(r), so that the 16 rows that are read at once fall on all 64 banks.  (The hardware
 // writes a wave's 64 chunks one after another: the lane that fills a place fetches the chunk that belongs there.)
 //
-// Bound by the matrix cores and the clock that the power limit leaves them (1.6 to 1.7 GHz of 2.4).  For four matrices of 4096 x 4096 and two
-// of 4096 x 16384 P X takes 1.46 ms a launch (1.13 PFLOP/s), X X^T 0.82 (1.01) and A^2 0.43 (0.97); the cores are busy for 69% of the
-// cycles, the epilogue takes 7%.
-// The library's plain 4096^3 fp16 product reaches 1.30 PFLOP/s on this card, 8192^3 1.43.  In two pieces a step of those matrices takes 36.6 ms, 1.18
-// PFLOP/s.  Measured and no faster: tiles of 256 x 256 on 8 waves, of 128 x 128 a wave on 4 (15.1 against 14.6 ms a step), results stored past the
+// The matrix cores are busy for 69% of the cycles at the 1.6 to 1.7 GHz (of 2.4) that such products run at, the epilogue takes 7%; what the
+// rest waits for was not found.  (The library's plain 4096^3 fp16 product reaches 1.30 PFLOP/s on this card, 8192^3 1.43, so the power limit
+// alone is not it.)  For four matrices of 4096 x 4096 and two of 4096 x 16384 P X takes 1.46 to 1.51 ms a launch (1.10 to 1.13 PFLOP/s),
+// X X^T 0.82 (1.01) and A^2 0.43 to 0.44 (0.95 to 0.97).  In two pieces a step of those matrices takes 36.6 to 37.5 ms, 1.16 to 1.18 PFLOP/s.
+// Measured and no faster: tiles of 256 x 256 on 8 waves, of 128 x 128 a wave on 4 (15.1 against 14.6 ms a step), results stored past the
 // caches, panels of 4 tile rows instead of 8.
 constexpr int kStages = 3, kRow = kNsK;  // halves of an LDS row
 __device__ __forceinline__ uint32_t swizzle(uint32_t r) { return r >> 2 & 3; }
@@ -610,7 +610,7 @@ void by_type(mr_dtype dt, F f) {
 
 // Tiles of 128 x 256 ask least of LDS and L2, tiles of 128 x 128 and of 64 x 64 leave fewer compute units idle where a launch has few.
 // A step with wide tiles and square ones (ms): eight of 4096 x 4096 11.2 and 12.7; 32 of 768 x 8192 4.45 and 4.64; one of 4096 x 4096
-// (512 wide tiles a product) 1.98 and 1.91; one of 2048 x 2048 0.56 and 0.47; one of 4096 x 8192 (1024) 3.08 and 3.04, of
+// (512 wide tiles a product) 1.98 and 1.91; one of 2048 x 2048 0.56 and 0.47 (0.39 to 0.42 by 64 x 64); one of 4096 x 8192 (1024) 3.08 and 3.04, of
 // 4096 x 16384 (2048) 5.33 and 5.41.
 // With tiles of 128 x 128 and of 64 x 64 (us): one of 512 x 512 171 and 124, eight (128 square tiles a product) 200 and 160, 32 (512) 372
 // and 393; one of 1024 x 1024 (64) 237 and 177, one of 1536 x 4096 (384) 452 and 424, eight of 1000 x 1000 (648) 455 and 470; 32 of

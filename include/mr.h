@@ -363,8 +363,10 @@ mr_status mr_adamw_step(const void* const* params, const void* const* grads, con
  *  clip     device, mr_grad_norm's 3 floats, or NULL.  Where clip[2] is 0 the step is not taken: outputs are the inputs.
  *  A gradient or momentum that is not finite gives NaN in its own matrix only.
  *  Matrices are worked off up to 32 at a time, in the stream's library workspace (see mr_set_workspace), about six to ten bytes
- *  an element for products = 16 and twice that for 32, up to 2 GiB or what the largest matrix takes.  mr_muon_workspace_bytes: bytes that one
- *  bound by the caller needs for a list (0: invalid arguments).  hyper is read on the host: a graph repeats its lr.
+ *  an element for products = 16 and twice that for 32, with sides rounded up to multiples of 96 (a matrix of few rows or columns takes
+ *  more: 65536 x 1 25 MB), up to 2 GiB or what the largest matrix takes.  The library's own is kept, as for the other calls, until
+ *  mr_set_workspace replaces it.  mr_muon_workspace_bytes: bytes that one bound by the caller needs for a list (0: invalid
+ *  arguments).  hyper is read on the host: a graph repeats its lr.
  */
 typedef enum mr_muon_adjust { MR_MUON_RATIO = 0, MR_MUON_RMS = 1 } mr_muon_adjust;
 typedef struct mr_muon_state {
@@ -398,10 +400,10 @@ mr_status mr_muon_step(const void* const* params, const void* const* grads, cons
  * mr_policy_loss:  for each row, with r = exp(logp - old_logp) and d = ref_logp - logp,
  *         loss_i = max(-A r, -A min(max(r, 1 - clip_low), 1 + clip_high)) + kl_coef * (exp(d) - d - 1)
  *     record[0..3] = sums over the rows of  w loss_i,  w (exp(d) - d - 1),  w [the clipped term is the larger],  w
- *     (fp64 sums in an order set by the sizes alone), and with dlogits the gradient of grad_scale * record[0], from the same
- *     pass over the logits where a row fits a workgroup's registers (131072 16-bit or 65536 fp32 columns; fewer than 32 rows of more
- *     than three quarters of that are read twice).  A term that is
- *     clipped, and only that, passes no gradient.
+ *     (fp64 sums in an order set by the sizes and the rows' alignment), and with dlogits the gradient of grad_scale * record[0], from the same
+ *     pass over the logits where a row fits a workgroup's registers: 131072 16-bit or 65536 fp32 columns on the 16-byte grid, 131065
+ *     or 65533 where rows start off it.  Longer rows, fewer than 32 rows of more than three quarters of that, and rows of less
+ *     than 16 bytes are read twice.  A term that is clipped, and only that, passes no gradient.
  *       old_logp  of the policy that sampled the tokens; NULL: of this one (r = 1).  ref_logp: NULL without a KL term (d = 0); with
  *       kl_coef 0 the term is reported in record[1] and left out of the loss and the gradient.  exp is finite up to fp64's range.
  *       advantages  rows floats;  weights: rows floats (a mask over its sum, say), or NULL: ones.
